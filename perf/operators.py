@@ -191,7 +191,7 @@ def _quantise(x):
     b = x.unflatten(-1, (-1, 32))
     amax = b.abs().amax(-1)
     m, e = torch.frexp(amax)
-    e = torch.where(m <= 0.875, e - 3, e - 2).clamp(-126, 127)
+    e = torch.where(m <= 0.875, e - 3, e - 2).clamp(-126, 125)
     e = torch.where(amax == 0, torch.zeros_like(e), e)
     t = torch.ldexp(b, -e[..., None])
     a = t.abs()
@@ -424,9 +424,9 @@ def _exact_append(s, rows, lens):
         b = x.double().reshape(*x.shape[:2], -1, 32)
         top = b.abs().amax(-1, keepdim=True)
         # The least whole e with top / 7 <= 2^e; log2 near a whole number is put right by the test.
-        e = torch.ceil(torch.log2(top / 7).clamp(-200, 200)).clamp(-126, 127)
+        e = torch.ceil(torch.log2(top / 7).clamp(-200, 200)).clamp(-126, 125)
         e = torch.where(top > 7 * 2.0 ** e, e + 1, e)
-        e = torch.where(top <= 7 * 2.0 ** (e - 1), e - 1, e).clamp(-126, 127)
+        e = torch.where(top <= 7 * 2.0 ** (e - 1), e - 1, e).clamp(-126, 125)
         t = b / 2.0 ** e
         step = torch.where(t.abs() < 2, 0.5, torch.where(t.abs() < 4, 1.0, 2.0)).double()
         return ((t / step).round() * step).clamp(-6, 6).mul(2.0 ** e).reshape(x.shape)
