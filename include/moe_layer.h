@@ -137,6 +137,9 @@ extern "C" {
 #define MOE_Q2_K 3
 #define MOE_Q3_K 4
 #define MOE_Q6_K 5
+/* Activation types of moe_kv.h and moe_logprobs.h (no tensor type of the layer). */
+#define MOE_BF16 6
+#define MOE_F16 7
 
 /* Status codes. */
 #define MOE_OK 0

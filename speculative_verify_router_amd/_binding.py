@@ -1,4 +1,4 @@
-"""ctypes binding of the C ABI in include/moe_layer.h.
+"""ctypes binding of the C ABI in include/*.h.
 
 Argument marshalling only: torch tensors are checked for device, dtype and
 contiguity and passed as raw device pointers; the HIP stream is torch's
@@ -42,6 +42,20 @@ class _Weights(ctypes.Structure):
     _fields_ = [("router", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("up", ctypes.c_void_p),
                 ("down", ctypes.c_void_p), ("shared_gate", ctypes.c_void_p),
                 ("shared_up", ctypes.c_void_p), ("shared_down", ctypes.c_void_p)]
+
+
+class _KvDesc(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("rotary_dims", ctypes.c_int32),
+                ("flags", ctypes.c_int32), ("scale", ctypes.c_float), ("norm_eps", ctypes.c_float)]
+
+
+class _KvBatch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("q_offsets", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p)]
 
 
 @dataclasses.dataclass(frozen=True)
@@ -91,6 +105,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         i32, i64, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
         D, W = ctypes.POINTER(_Desc), ctypes.POINTER(_Weights)
+        KD, KB = ctypes.POINTER(_KvDesc), ctypes.POINTER(_KvBatch)
         sig = {
             "moe_version": (i32, []),
             "moe_strerror": (ctypes.c_char_p, [i32]),
@@ -106,6 +121,14 @@ def lib():
             "moe_dequant_rows": (i32, [i32, vp, i64, i32, i64, i64, vp, vp]),
             "moe_accept_workspace_bytes": (i32, [i32, i64, ctypes.POINTER(sz)]),
             "moe_verify_accept": (i32, [vp, i32, i64, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]),
+            "moe_kv_cache_bytes": (i32, [KD, i64, ctypes.POINTER(i64)]),
+            "moe_kv_append": (i32, [KD, KB, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i32,
+                                    vp, vp]),
+            "moe_kv_attention_workspace_bytes": (i32, [KD, KB, ctypes.POINTER(sz)]),
+            "moe_kv_attention": (i32, [KD, KB, i32, vp, i64, vp, i32, vp, vp, vp, sz, vp]),
+            "moe_kv_read": (i32, [KD, KB, vp, i32, vp, vp, vp]),
+            "moe_logprobs_workspace_bytes": (i32, [i32, i64, i32, ctypes.POINTER(sz)]),
+            "moe_logprobs": (i32, [vp, i32, i32, i64, i64, vp, vp, vp, i32, vp, vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -120,7 +143,9 @@ C_SYMBOLS = ("moe_version", "moe_strerror", "moe_tensor_bytes", "moe_workspace_b
              "moe_route", "moe_layer_forward", "moe_layer_forward_timed",
              "moe_layer_forward_noalloc", "moe_stage_count",
              "moe_stage_name", "moe_dequant_rows", "moe_accept_workspace_bytes",
-             "moe_verify_accept")
+             "moe_verify_accept", "moe_kv_cache_bytes", "moe_kv_append",
+             "moe_kv_attention_workspace_bytes", "moe_kv_attention", "moe_kv_read",
+             "moe_logprobs_workspace_bytes", "moe_logprobs")
 
 
 def _ptr(t: Optional[torch.Tensor], dtype) -> Optional[int]:
@@ -338,3 +363,244 @@ def moe_verify_accept(logits: torch.Tensor, drafts: Optional[torch.Tensor], toke
                                  _ptr(pending_h, torch.float32), _ptr(ws, torch.uint8), ws.numel(),
                                  _stream(stream))
     _check(st, "moe_verify_accept")
+
+
+# include/moe_kv.h: paged 4-bit key/value cache, append and attention.
+BF16, F16 = 6, 7
+_ACT_DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+KV_ROTARY_INTERLEAVED = 1
+
+
+def _act_dtype(t: torch.Tensor) -> int:
+    try:
+        return _ACT_DTYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"expected float32, bfloat16 or float16, got {t.dtype}") from None
+
+
+def _on(device: torch.device, t: Optional[torch.Tensor], dtype=None, shape=None,
+        what: str = "tensor") -> Optional[int]:
+    """The address of a contiguous tensor of `device` (None for None)."""
+    if t is None:
+        return None
+    if t.device != device:
+        raise ValueError(f"{what}: expected a tensor on {device}, got {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _rows(device: torch.device, t: torch.Tensor, dtype, shape, what: str):
+    """Address and row stride of a [rows][heads][dim] tensor whose rows may lie apart."""
+    if t.device != device:
+        raise ValueError(f"{what}: expected a tensor on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    s, row = t.stride(), shape[1] * shape[2]
+    if shape[0] == 0:
+        return t.data_ptr(), row
+    if s[2] != 1 or (s[1] != shape[2] and shape[1] != 1) or (s[0] < row and shape[0] != 1):
+        raise ValueError(f"{what}: expected whole rows of heads, got strides {s}")
+    return t.data_ptr(), (row if shape[0] == 1 else s[0])
+
+
+def _call_on(device: torch.device, stream, f, *args) -> int:
+    """f(*args, stream) with `device` current; its current stream where none is given."""
+    if device.type != "cuda":
+        raise ValueError("expected a device tensor")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"expected a stream of {device}, got one of {stream.device}")
+    if device.index == torch.cuda.current_device():
+        return f(*args, stream.cuda_stream)
+    with torch.cuda.device(device):
+        return f(*args, stream.cuda_stream)
+
+
+@dataclasses.dataclass(frozen=True)
+class KvDesc:
+    """Head layout and cache format of one attention layer (moe_kv_desc)."""
+    n_heads: int
+    n_kv_heads: int
+    head_dim: int
+    page_size: int = 64
+    window: int = 0
+    rotary_dims: int = 0
+    rotary_interleaved: bool = False
+    scale: float = 0.0  # 0: 1/sqrt(head_dim)
+    norm_eps: float = 1e-6
+
+    def c(self) -> _KvDesc:
+        return _KvDesc(self.n_heads, self.n_kv_heads, self.head_dim, self.page_size, self.window,
+                       self.rotary_dims, KV_ROTARY_INTERLEAVED if self.rotary_interleaved else 0,
+                       self.scale, self.norm_eps)
+
+    @property
+    def page_bytes(self) -> int:
+        """Bytes of one page of one key/value head."""
+        return self.page_size * (self.head_dim + self.head_dim // 16)
+
+
+@dataclasses.dataclass
+class KvBatch:
+    """New rows of a batch of sequences (moe_kv_batch): int32 device tensors
+    q_offsets [B+1], seq_lens [B] (new rows included), page_table [B][pages];
+    max_rows: no sequence has more new rows."""
+    q_offsets: torch.Tensor
+    seq_lens: torch.Tensor
+    page_table: torch.Tensor
+    max_rows: int
+
+    def c(self, n_tokens: int) -> _KvBatch:
+        i32, dev = torch.int32, self.page_table.device
+        if self.page_table.dim() != 2:
+            raise ValueError("page_table: expected [sequences][pages]")
+        B = self.page_table.shape[0]
+        return _KvBatch(B, n_tokens, self.max_rows, self.page_table.shape[1],
+                        _on(dev, self.q_offsets, i32, (B + 1,), "q_offsets"),
+                        _on(dev, self.seq_lens, i32, (B,), "seq_lens"),
+                        _on(dev, self.page_table, i32, None, "page_table"))
+
+
+def moe_kv_cache_bytes(desc: KvDesc, n_pages: int) -> int:
+    out = ctypes.c_int64()
+    _check(lib().moe_kv_cache_bytes(desc.c(), n_pages, ctypes.byref(out)), "moe_kv_cache_bytes")
+    return out.value
+
+
+def kv_cache(desc: KvDesc, n_pages: int, device="cuda") -> torch.Tensor:
+    """A cache of n_pages pages: uint8 [n_pages][n_kv_heads][page bytes], zeros."""
+    moe_kv_cache_bytes(desc, n_pages)
+    return torch.zeros((n_pages, desc.n_kv_heads, desc.page_bytes), dtype=torch.uint8, device=device)
+
+
+def _cache(desc: KvDesc, cache: torch.Tensor, device: torch.device) -> int:
+    return _on(device, cache, torch.uint8, (cache.shape[0], desc.n_kv_heads, desc.page_bytes), "cache")
+
+
+def moe_kv_append(desc: KvDesc, batch: KvBatch, q: Optional[torch.Tensor], k: torch.Tensor,
+                  v: torch.Tensor, cache: torch.Tensor, q_out: Optional[torch.Tensor],
+                  q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None,
+                  inv_freq: Optional[torch.Tensor] = None,
+                  positions: Optional[torch.Tensor] = None, stream=None):
+    """q [T][heads][D] (or None, with q_out None), k and v [T][kv_heads][D] of one
+    activation type, rows of q, k, v possibly apart (views of a fused projection);
+    q_norm, k_norm [D], inv_freq [rotary/2] float32; positions [T] int32 (None: places)."""
+    dev, dt, f32 = k.device, k.dtype, torch.float32
+    T, D = k.shape[0], desc.head_dim
+    kv = (T, desc.n_kv_heads, D)
+    qp, qs, op = None, 0, None
+    if q is not None:
+        qp, qs = _rows(dev, q, dt, (T, desc.n_heads, D), "q")
+    if q_out is not None:
+        op = _on(dev, q_out, dt, (T, desc.n_heads, D), "q_out")
+    kp, ks = _rows(dev, k, dt, kv, "k")
+    vp, vs = _rows(dev, v, dt, kv, "v")
+    st = _call_on(dev, stream, lib().moe_kv_append, desc.c(), batch.c(T), _act_dtype(k), qp, qs, kp,
+                  ks, vp, vs, _on(dev, q_norm, f32, (D,), "q_norm"),
+                  _on(dev, k_norm, f32, (D,), "k_norm"),
+                  _on(dev, inv_freq, f32, (desc.rotary_dims // 2,), "inv_freq"),
+                  _on(dev, positions, torch.int32, (T,), "positions"), _cache(desc, cache, dev),
+                  cache.shape[0], op)
+    _check(st, "moe_kv_append")
+
+
+def moe_kv_attention_workspace_bytes(desc: KvDesc, batch: KvBatch, n_tokens: int) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().moe_kv_attention_workspace_bytes(desc.c(), batch.c(n_tokens), ctypes.byref(out)),
+           "moe_kv_attention_workspace_bytes")
+    return out.value
+
+
+def kv_workspace(desc: KvDesc, batch: KvBatch, n_tokens: int) -> torch.Tensor:
+    """A device workspace for moe_kv_attention on batches of this size (n_tokens rows)."""
+    return torch.empty(moe_kv_attention_workspace_bytes(desc, batch, n_tokens), dtype=torch.uint8,
+                       device=batch.page_table.device)
+
+
+def moe_kv_attention(desc: KvDesc, batch: KvBatch, q: torch.Tensor, cache: torch.Tensor,
+                     out: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                     ws: Optional[torch.Tensor] = None, stream=None):
+    """q and out [T][heads][D] of one activation type (rows of q possibly apart);
+    lse [T][heads] float32."""
+    dev = q.device
+    T, shape = q.shape[0], (q.shape[0], desc.n_heads, desc.head_dim)
+    if ws is None:
+        ws = kv_workspace(desc, batch, T)
+    qp, qs = _rows(dev, q, q.dtype, shape, "q")
+    st = _call_on(dev, stream, lib().moe_kv_attention, desc.c(), batch.c(T), _act_dtype(q), qp, qs,
+                  _cache(desc, cache, dev), cache.shape[0], _on(dev, out, q.dtype, shape, "out"),
+                  _on(dev, lse, torch.float32, shape[:2], "lse"),
+                  _on(dev, ws, torch.uint8, None, "ws"), ws.numel())
+    _check(st, "moe_kv_attention")
+
+
+def moe_kv_read(desc: KvDesc, batch: KvBatch, cache: torch.Tensor, k_out: Optional[torch.Tensor],
+                v_out: Optional[torch.Tensor], stream=None):
+    """The stored rows of the batch as float32 [T][kv_heads][D] (either may be None)."""
+    dev = cache.device
+    some = k_out if k_out is not None else v_out
+    if some is None:
+        raise ValueError("moe_kv_read: k_out or v_out is needed")
+    shape = (some.shape[0], desc.n_kv_heads, desc.head_dim)
+    st = _call_on(dev, stream, lib().moe_kv_read, desc.c(), batch.c(shape[0]),
+                  _cache(desc, cache, dev), cache.shape[0],
+                  _on(dev, k_out, torch.float32, shape, "k_out"),
+                  _on(dev, v_out, torch.float32, shape, "v_out"))
+    _check(st, "moe_kv_read")
+
+
+# include/moe_logprobs.h: log probabilities, entropy and top alternatives.
+LOGPROBS_MAX_TOP = 64
+
+
+def moe_logprobs_workspace_bytes(max_rows: int, vocab: int, max_top: int = 0) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().moe_logprobs_workspace_bytes(max_rows, vocab, max_top, ctypes.byref(out)),
+           "moe_logprobs_workspace_bytes")
+    return out.value
+
+
+def logprobs_workspace(max_rows: int, vocab: int, max_top: int = 0, device="cuda") -> torch.Tensor:
+    """A zero-filled device workspace for moe_logprobs (its counters must start
+    at zero; calls keep them so)."""
+    return torch.zeros(moe_logprobs_workspace_bytes(max_rows, vocab, max_top), dtype=torch.uint8,
+                       device=device)
+
+
+def moe_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor],
+                 logprobs: Optional[torch.Tensor], entropy: Optional[torch.Tensor] = None,
+                 top_ids: Optional[torch.Tensor] = None,
+                 top_logprobs: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                 stream=None):
+    """logits [N][V] float32, bfloat16 or float16 (rows possibly apart); targets [N]
+    int32 and logprobs [N] float32, both or neither; entropy [N] float32; top_ids
+    int32 and top_logprobs float32 [N][k], k the number of alternatives."""
+    dev, f32 = logits.device, torch.float32
+    if logits.dim() != 2:
+        raise ValueError(f"logits: expected [rows][vocabulary], got shape {tuple(logits.shape)}")
+    N, V = logits.shape
+    if N and V and logits.stride(1) != 1 and V != 1:
+        raise ValueError(f"logits: expected whole rows, got strides {logits.stride()}")
+    stride = logits.stride(0) if N > 1 else V
+    some = top_ids if top_ids is not None else top_logprobs
+    if some is not None and some.dim() != 2:
+        raise ValueError("top_ids, top_logprobs: expected [rows][alternatives]")
+    k = some.shape[1] if some is not None else 0
+    if ws is None:
+        ws = logprobs_workspace(N, V, k, dev)
+    st = _call_on(dev, stream, lib().moe_logprobs, logits.data_ptr(), _act_dtype(logits), N, V,
+                  stride, _on(dev, targets, torch.int32, (N,), "targets"),
+                  _on(dev, logprobs, f32, (N,), "logprobs"),
+                  _on(dev, entropy, f32, (N,), "entropy"), k,
+                  _on(dev, top_ids, torch.int32, (N, k), "top_ids"),
+                  _on(dev, top_logprobs, f32, (N, k), "top_logprobs"),
+                  _on(dev, ws, torch.uint8, None, "ws"), ws.numel())
+    _check(st, "moe_logprobs")

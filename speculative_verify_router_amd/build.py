@@ -24,10 +24,14 @@ LIB = os.path.join(LIBDIR, "libsvr_moe.so")
 SOURCES = [os.path.join(CSRC, f) for f in (
     "moe_layer.hip", "launch_expert.hip", "launch_ffn.hip", "launch_ffn_q8_0.hip",
     "launch_ffn_q4_k.hip", "launch_ffn_q2_k.hip", "launch_ffn_q3_k.hip", "launch_ffn_q6_k.hip",
-    "accept.hip")]
+    "accept.hip", "kv_append.hip", "kv_attention.hip", "launch_attention_d64.hip",
+    "launch_attention_d128.hip", "launch_attention_d192.hip", "launch_attention_d256.hip",
+    "logprobs.hip")]
 HEADERS = [os.path.join(CSRC, f) for f in ("common.h", "quant.h", "route.h", "ffn.h", "phases.h", "misc.h",
-                                           "gemm.h", "launch.h", "launch_ffn.h")] + [
-    os.path.join(ROOT, "include", h) for h in ("moe_layer.h", "moe_accept.h")]
+                                           "gemm.h", "launch.h", "launch_ffn.h", "kv.h",
+                                           "kv_attention.h", "launch_attention.h")] + [
+    os.path.join(ROOT, "include", h) for h in ("moe_layer.h", "moe_accept.h", "moe_kv.h",
+                                               "moe_logprobs.h")]
 
 ARCH = "gfx950"
 

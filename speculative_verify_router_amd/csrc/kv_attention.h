@@ -1,0 +1,422 @@
+// Attention over the paged 4-bit cache (include/moe_kv.h), one kernel for
+// single tokens, verify batches and prefill rows.
+//
+// A workgroup takes one key/value head of one sequence, 16 * RT of the rows
+// that read it (row = new token x query head of the group, so four drafts of
+// sixteen heads share every key that is read) and a stretch of the tokens;
+// its waves take tiles of the stretch in turn, each with a softmax of its
+// own, joined at the end.  Scores are taken transposed, S^T = K Q^T, so that
+// a lane holds four tokens of one row: the maximum and sum of a row need no
+// exchange inside a tile, and the weights are at once the right operand of
+// O^T = V^T P^T.
+//   Keys go from memory to registers: a lane's 16 bytes are 32 channels of
+// one token under one scale, four k-steps of the 16x16x32 product (the
+// channels of a step are permuted, the same way in the query).  Values need
+// channels as rows: they are widened, staged as [token][channel] in the
+// wave's own shared memory and read back transposed.  E2M1 times a power of
+// two is exact in bf16, so keys and values enter exactly.
+//   NT terms of bf16 hold a query value and a softmax weight: one for bf16
+// activations, two for fp16, three (24 bits) for fp32.
+#pragma once
+
+#include "kv.h"
+
+namespace svr {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+
+struct AttnArgs {
+  KvArgs kv;
+  const void* q;
+  int64_t qs;
+  const uint8_t* cache;
+  void* out;
+  float* lse;
+  float* part_o;   // [row][head][split][D], sums not yet divided
+  float2* part_ml;  // [row][head][split]: maximum (base 2), sum
+  float c;         // scale * log2(e)
+  int G, tiles, splits, min_tiles, vec;
+};
+
+constexpr int kAttnWaves = 4;
+constexpr int kAttnTile = 64;  // tokens of a wave's step
+
+// The tokens [beg, end) that rows of places [first, last] see, in tiles from
+// tb on, `per` of them a split, `used` splits (at least one).
+struct KvRange {
+  int beg, end, tb, ntile, per, used;
+};
+__device__ __forceinline__ KvRange kv_range(const KvArgs& kv, int len, int first, int last,
+                                            int splits, int min_tiles) {
+  KvRange r;
+  r.end = min(min(len, kv.pages_per_seq << kv.page_shift), last + 1);
+  r.beg = kv.window ? max(0, first - kv.window + 1) : 0;
+  r.tb = r.beg & ~(kAttnTile - 1);
+  r.ntile = r.end > r.beg ? (r.end - r.tb + kAttnTile - 1) / kAttnTile : 0;
+  r.per = max(min_tiles, (r.ntile + splits - 1) / splits);
+  r.used = max(1, (r.ntile + r.per - 1) / r.per);
+  return r;
+}
+
+// A sequence's rows as the kernels use them.
+struct KvRows {
+  int off, rows, len, place0;  // place of row 0
+};
+__device__ __forceinline__ KvRows kv_rows(const KvArgs& kv, int b) {
+  KvRows s;
+  s.off = kv.offs[b];
+  const int end = kv.offs[b + 1];
+  // (Wrapping only for offsets that are not ascending from 0: then no rows.)
+  s.rows = s.off >= 0 && end > s.off && end <= kv.n_tokens ? end - s.off : 0;
+  s.len = min(max(kv.lens[b], 0), 1 << 28);
+  s.place0 = s.len - s.rows;
+  s.rows = min(s.rows, kv.max_rows);
+  return s;
+}
+
+template <int D>
+__device__ __forceinline__ constexpr int step_channel(int step, int g) {
+  constexpr int kFull = 4 * (D / 128);
+  return step < kFull ? 128 * (step / 4) + 32 * g + 8 * (step % 4)
+                      : 128 * (D / 128) + 16 * g + 8 * (step - kFull);
+}
+
+// x as a sum of NT bf16 terms (24 bits of x with three).
+template <int NT>
+__device__ __forceinline__ void split_terms(float x, bf16 (&t)[NT]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    t[n] = (bf16)x;
+    x -= (float)t[n];
+  }
+}
+
+// A lane's codes and scales of one token for D/4 channels: the full 128s in
+// 16-byte pieces, a last 64 in 8 bytes.
+template <int D>
+struct Codes {
+  uint32_t w[D / 32];
+  uint32_t e[(D + 127) / 128];
+};
+
+template <int D>
+__device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* scales, int g,
+                                           Codes<D>& x) {
+#pragma unroll
+  for (int p = 0; p < D / 128; ++p) {
+    const uint4 v = *reinterpret_cast<const uint4*>(codes + 64 * p + 16 * g);
+    x.w[4 * p] = v.x;
+    x.w[4 * p + 1] = v.y;
+    x.w[4 * p + 2] = v.z;
+    x.w[4 * p + 3] = v.w;
+    x.e[p] = scales[4 * p + g];
+  }
+  if constexpr (D % 128 != 0) {
+    constexpr int p = D / 128;
+    const uint2 v = *reinterpret_cast<const uint2*>(codes + 64 * p + 8 * g);
+    x.w[4 * p] = v.x;
+    x.w[4 * p + 1] = v.y;
+    x.e[p] = scales[4 * p + g / 2];
+  }
+}
+
+// Eight codes times 2^(e-127) as bf16 (NaN for e = 255).
+__device__ __forceinline__ bf16x8 widen(uint32_t w, uint32_t e) {
+  const float s = __builtin_bit_cast(float, e << 23);
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
+  return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// Four rows (tokens) of 16 channels, transposed: lane n of 16 gets channel n.
+__device__ __forceinline__ s16x4 read_transposed(const uint8_t* p) {
+  typedef __attribute__((address_space(3))) s16x4 lds4;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
+}
+
+template <int D, int RT, int NT, typename T>
+__global__ __launch_bounds__(kAttnWaves* kWave) void k_kv_attention(AttnArgs a) {
+  constexpr int KS = D / 32, CB = D / 16, SUB = kAttnTile / 16;
+  constexpr int kRowBytes = 2 * D + 32;            // a staged token: the pad spreads the banks
+  constexpr int kStage = 32 * kRowBytes;           // a wave's 32 staged tokens
+  constexpr int kJoinRow = D + 4;                  // floats of a joined row
+  constexpr int kJoin = kAttnWaves * 16 * kJoinRow * 4;
+  constexpr int kMem = kAttnWaves * kStage > kJoin ? kAttnWaves * kStage : kJoin;
+  __shared__ __attribute__((aligned(16))) uint8_t s_mem[kMem];
+  __shared__ float2 s_ml[kAttnWaves][RT * 16];
+
+  const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x >> 6;
+  const int l16 = lane & 15, g = lane >> 4;
+
+  // Consecutive work on one XCD: row tiles of a head share its L2.
+  int id;
+  {
+    const int n = gridDim.x, x = blockIdx.x & 7, q8 = n >> 3, r8 = n & 7;
+    id = x * q8 + min(x, r8) + (blockIdx.x >> 3);
+  }
+  const int tile = id % a.tiles;
+  id /= a.tiles;
+  const int split = id % a.splits;
+  id /= a.splits;
+  const int kvh = id % a.kv.Hk, b = id / a.kv.Hk;
+
+  const KvRows sq = kv_rows(a.kv, b);
+  const int row_total = sq.rows * a.G, r0 = tile * 16 * RT;
+  if (r0 >= row_total) return;
+  const int r_last = min(row_total, r0 + 16 * RT) - 1;
+  const int first = sq.place0 + r0 / a.G, last = sq.place0 + r_last / a.G;
+  const KvRange rg = kv_range(a.kv, sq.len, first, last, a.splits, a.min_tiles);
+  if (split >= rg.used) return;
+  const int t_end = min(rg.ntile, (split + 1) * rg.per);
+
+  // The rows' queries, and the tokens that each sees: [lo, hi].
+  bf16x8 qf[RT][KS][NT];
+  int lo[RT], hi[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int r = r0 + 16 * rt + l16;
+    const bool on = r < row_total;
+    const int m = min(r, row_total - 1) / a.G, h = kvh * a.G + min(r, row_total - 1) % a.G;
+    const int place = sq.place0 + m;
+    hi[rt] = on ? min(place, rg.end - 1) : -1;
+    lo[rt] = a.kv.window ? place - a.kv.window + 1 : 0;
+    const T* qp = (const T*)a.q + (int64_t)(sq.off + m) * a.qs + (int64_t)h * D;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      float x[8];
+      load8(qp + step_channel<D>(s, g), a.vec & 1, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        bf16 t[NT];
+        split_terms<NT>(x[e], t);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) qf[rt][s][n][e] = t[n];
+      }
+    }
+  }
+  // Tiles between these need no mask.
+  const int all_hi = min(first, rg.end - 1), all_lo = a.kv.window ? last - a.kv.window + 1 : 0;
+
+  float mx[RT], sum[RT];
+  f32x4v o[RT][CB];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    mx[rt] = -INFINITY;
+    sum[rt] = 0.f;
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) o[rt][cb] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  }
+  uint8_t* stage = s_mem + wv * kStage;
+  const int P = 1 << a.kv.page_shift;
+  const int32_t* table = a.kv.table + (int64_t)b * a.kv.pages_per_seq;
+
+  for (int t = split * rg.per + wv; t < t_end; t += kAttnWaves) {
+    const int tok0 = rg.tb + t * kAttnTile;
+    Codes<D> kc[SUB], vc[SUB];
+    unsigned hidden = 0;  // subtiles on a page that is not there
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      // Sixteen tokens lie in one page.  Lanes of tokens outside [beg, end)
+      // read a token inside, so nothing else is ever loaded.
+      const int st = min(max(tok0 + 16 * u, rg.beg & ~15), (rg.end - 1) & ~15);
+      int page = __builtin_amdgcn_readfirstlane(table[st >> a.kv.page_shift]);
+      if ((unsigned)page >= (unsigned)a.kv.n_pages) {
+        hidden |= 1u << u;
+        page = 0;
+      }
+      const uint8_t* c = a.cache + ((int64_t)page * a.kv.Hk + kvh) * a.kv.page_bytes;
+      const int i = min(max(st + l16, rg.beg), rg.end - 1) & (P - 1);
+      load_codes<D>(c + i * (D / 2), c + P * D + i * (D / 32), g, kc[u]);
+      load_codes<D>(c + (P + i) * (D / 2), c + P * D + (P + i) * (D / 32), g, vc[u]);
+    }
+
+    f32x4v s[RT][SUB];
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) s[rt][u] = f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const bf16x8 kf = widen(kc[u].w[k], kc[u].e[k / 4]);
+#pragma unroll
+        for (int n = NT - 1; n >= 0; --n)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[rt][k][n], s[rt][u], 0, 0, 0);
+      }
+    }
+
+    if (hidden || tok0 + kAttnTile - 1 > all_hi || tok0 < all_lo) {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        const int tk = tok0 + 16 * u + 4 * g;
+        const bool gone = hidden >> u & 1;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (gone || tk + i > hi[rt] || tk + i < lo[rt]) s[rt][u][i] = -INFINITY;
+        if (gone) {  // whatever lies there must not meet a weight of zero
+#pragma unroll
+          for (int k = 0; k < KS; ++k) vc[u].w[k] = 0;
+#pragma unroll
+          for (int p = 0; p < (D + 127) / 128; ++p) vc[u].e[p] = 127;
+        }
+      }
+    }
+
+    // Softmax.  The maximum in use follows only where a score passes it by
+    // 2^8: weights up to 2^8 lose nothing in 32 bits, and most tiles then
+    // need neither an exchange between lanes nor a rescaling of the sums.
+    float top[RT];
+    bool grow = false;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float v = s[rt][0][0];
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v = fmaxf(v, s[rt][u][i]);
+      top[rt] = v * a.c;
+      grow |= top[rt] > mx[rt] + 8.f;
+    }
+    if (__ballot(grow)) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        float v = top[rt];
+        v = fmaxf(v, __shfl_xor(v, 16, kWave));
+        v = fmaxf(v, __shfl_xor(v, 32, kWave));
+        v = fmaxf(v, mx[rt]);
+        const float f = v == mx[rt] ? 1.f : __builtin_amdgcn_exp2f(mx[rt] - v);
+        mx[rt] = v;
+        sum[rt] *= f;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) o[rt][cb] *= f;
+      }
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const float m0 = mx[rt] == -INFINITY ? 0.f : mx[rt];
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(s[rt][u][i], a.c, -m0));
+          s[rt][u][i] = p;
+          sum[rt] += p;
+        }
+    }
+
+    // O^T += V^T P^T, 32 tokens at a time.
+#pragma unroll
+    for (int u = 0; u < SUB; u += 2) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          *reinterpret_cast<bf16x8*>(stage + (16 * y + l16) * kRowBytes + 2 * step_channel<D>(k, g)) =
+              widen(vc[u + y].w[k], vc[u + y].e[k / 4]);
+      bf16x8 pf[RT][NT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          bf16 x[NT];
+          split_terms<NT>(s[rt][u + i / 4][i % 4], x);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) pf[rt][n][i] = x[n];
+        }
+      const uint8_t* from = stage + (4 * g + l16 / 4) * kRowBytes + 8 * (l16 % 4);
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) {
+        struct { s16x4 a, b; } v{read_transposed(from + 32 * cb),
+                                 read_transposed(from + 16 * kRowBytes + 32 * cb)};
+        const bf16x8 vf = __builtin_bit_cast(bf16x8, v);
+#pragma unroll
+        for (int n = NT - 1; n >= 0; --n)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            o[rt][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][n], o[rt][cb], 0, 0, 0);
+      }
+    }
+  }
+
+  // Join the waves.
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    sum[rt] += __shfl_xor(sum[rt], 16, kWave);
+    sum[rt] += __shfl_xor(sum[rt], 32, kWave);
+    if (g == 0) s_ml[wv][16 * rt + l16] = make_float2(mx[rt], sum[rt]);
+  }
+  __syncthreads();  // also: every wave is done with its staged values
+  float* join = reinterpret_cast<float*>(s_mem);
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) m = fmaxf(m, s_ml[w][16 * rt + l16].x);
+    const float f = mx[rt] == m ? 1.f : __builtin_amdgcn_exp2f(mx[rt] - m);
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb)
+      *reinterpret_cast<f32x4v*>(join + (wv * 16 + l16) * kJoinRow + 16 * cb + 4 * g) = o[rt][cb] * f;
+    __syncthreads();
+    const int jr = threadIdx.x >> 4, r = r0 + 16 * rt + jr;
+    if (r < row_total) {
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) M = fmaxf(M, s_ml[w][16 * rt + jr].x);
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) {
+        const float2 ml = s_ml[w][16 * rt + jr];
+        L += ml.x == M ? ml.y : ml.y * __builtin_amdgcn_exp2f(ml.x - M);
+      }
+      const int64_t at = (int64_t)(sq.off + r / a.G) * a.kv.Hq + kvh * a.G + r % a.G;
+      const bool whole = rg.used == 1;
+      const float inv = !whole ? 1.f : L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const int ch = 64 * j + 4 * (threadIdx.x & 15);
+        f32x4v v = *reinterpret_cast<f32x4v*>(join + jr * kJoinRow + ch);
+#pragma unroll
+        for (int w = 1; w < kAttnWaves; ++w)
+          v += *reinterpret_cast<f32x4v*>(join + (w * 16 + jr) * kJoinRow + ch);
+        v *= inv;
+        if (whole) {
+          T x[4] = {(T)v.x, (T)v.y, (T)v.z, (T)v.w};
+          T* out = (T*)a.out + at * D + ch;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) out[e] = x[e];
+        } else {
+          *reinterpret_cast<f32x4v*>(a.part_o + (at * a.splits + split) * D + ch) = v;
+        }
+      }
+      if ((threadIdx.x & 15) == 0) {
+        if (!whole)
+          a.part_ml[at * a.splits + split] = make_float2(M, L);
+        else if (a.lse)
+          a.lse[at] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.6931471805599453f;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <int D>
+int32_t launch_kv_attention(const AttnArgs& a, int32_t dtype, int row_tiles, int grid, hipStream_t st);
+
+// The most row tiles (of 16) a workgroup of head size D and NT terms takes:
+// a wave holds their queries (D/8 registers a term) and sums (D/4) at once.
+constexpr int attn_most_row_tiles(int D, int NT) {
+  return NT == 1 ? (D <= 128 ? 4 : 2) : D <= 192 ? 2 : 1;
+}
+// Whole verify batches in one tile where they fit: every key is widened once
+// for all rows of the tile.
+inline int attn_row_tiles(int64_t rows, int D, int32_t dtype) {
+  const int most = attn_most_row_tiles(D, dtype == MOE_BF16 ? 1 : 2);
+  return rows <= 16 || most == 1 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
+}
+
+}  // namespace svr

@@ -1,0 +1,398 @@
+"""The paged 4-bit cache (include/moe_kv.h) on the GPU against the float64
+oracle (oracle/kv_oracle.py), every call through the C ABI.
+
+Append: the whole cache has to be equal byte for byte (keys are rounded from
+64 bits, so a code next to a border falls on its own side), bytes of other
+tokens unchanged.  Attention: everything that no row may see (free pages,
+the rest of a last page, table entries without a token) holds NaN scales or
+points nowhere; tolerances are derived in kv_support.attention_tolerance.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import speculative_verify_router_amd as svr
+from gpu_common import dev, log
+from kv_support import TYPES, Plan, attention_tolerance, desc_of, rounded
+from oracle import kv_oracle as ko
+
+pytestmark = pytest.mark.gpu
+
+
+def run_append(lay, plan, cache, q, k, v, **kw):
+    """moe_kv_append on a copy of `cache`; returns it and q_out as float64."""
+    c = dev(cache)
+    out = torch.full(q.shape, float("nan"), dtype=q.dtype, device="cuda")
+    svr.moe_kv_append(desc_of(lay), plan.batch(), q, k, v, c, out, **kw)
+    torch.cuda.synchronize()
+    return c.cpu().numpy(), out.double().cpu().numpy()
+
+
+def check_append(lay, plan, dtype, rng, norm=True, view=None, positions=None, scale=1.0):
+    T, D = plan.T, lay.dim
+    x = rng.standard_normal((T, lay.heads + 2 * lay.kv_heads, D)) * scale
+    t, x64 = rounded(x, dtype)
+    if view:
+        t = view(t)
+    hq, hk = lay.heads, lay.kv_heads
+    w = [(1 + 0.1 * rng.standard_normal(D)).astype(np.float32) if norm else None for _ in "qk"]
+    f = (10000.0 ** (-np.arange(0, lay.rotary, 2) / max(lay.rotary, 1))).astype(np.float32)
+    cache = rng.integers(0, 256, plan.empty_cache().shape).astype(np.uint8)
+    up = lambda a: None if a is None else dev(a)  # noqa: E731
+    got, q_out = run_append(lay, plan, cache, t[:, :hq], t[:, hq:hq + hk], t[:, hq + hk:],
+                            q_norm=up(w[0]), k_norm=up(w[1]), inv_freq=up(f) if lay.rotary else None,
+                            positions=up(positions))
+    want = cache.copy()
+    ref = ko.append(lay, want, plan.offsets, plan.lens, plan.table, x64[:, :hq], x64[:, hq:hq + hk],
+                    x64[:, hq + hk:], *w, f, positions)
+    assert np.array_equal(got, want)
+    n = plan.offsets[-1]
+    # Norm: D + 4 roundings of the sum and the root, halved by it, then two
+    # products; rotation: two products of sine and cosine (each rounded) and a
+    # sum, of values up to |a| + |b|; then the type's own rounding.
+    big = np.max(np.abs(ref[:n]), axis=-1, keepdims=True)
+    tol = (D / 2 + 10) * 2.0 ** -24 * 2 * big + torch.finfo(TYPES[dtype]).eps / 2 * np.abs(ref[:n]) + 2.0 ** -25
+    assert np.all(np.abs(q_out[:n] - ref[:n]) <= tol)
+    assert np.all(np.isnan(q_out[n:]))  # rows behind the last sequence stay as they were
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dim,heads,kv_heads,page,rotary,interleaved", [
+    (64, 3, 1, 16, 64, False), (128, 8, 8, 32, 32, True), (192, 16, 1, 64, 64, False),
+    (192, 10, 2, 16, 192, True), (256, 5, 5, 128, 0, False), (256, 4, 2, 1024, 256, False),
+    (64, 17, 1, 16, 16, False),
+])
+def test_append_bytes(dtype, dim, heads, kv_heads, page, rotary, interleaved):
+    log(f"append {dtype} D={dim} {heads}/{kv_heads} page={page} rot={rotary}")
+    rng = np.random.default_rng(dim + heads)
+    lay = ko.Layout(heads, kv_heads, dim, page, 0, rotary, interleaved)
+    plan = Plan(lay, [3, 0, 1, 5], [3, 7, page + 1, 2 * page + 2], rng, pad_rows=2)
+    check_append(lay, plan, dtype, rng, norm=rotary != 32)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_append_rows_apart_and_unaligned(dtype):
+    rng = np.random.default_rng(5)
+    lay = ko.Layout(4, 2, 64, 16, 0, 32)
+    plan = Plan(lay, [2, 3], [20, 33], rng)
+
+    def apart(by, at):
+        def f(t):
+            buf = torch.zeros((t.shape[0], t[0].numel() + by + at), dtype=t.dtype, device="cuda")
+            r = buf[:, at:at + t[0].numel()]
+            r.copy_(t.flatten(1))
+            return r.unflatten(1, t.shape[1:])
+        return f
+    check_append(lay, plan, dtype, rng, view=apart(64, 0))
+    check_append(lay, plan, dtype, rng, view=apart(3, 0))   # rows at odd offsets
+    check_append(lay, plan, dtype, rng, view=apart(8, 1))   # one element past an aligned start
+
+
+def test_append_far_positions():
+    rng = np.random.default_rng(6)
+    lay = ko.Layout(2, 1, 128, 64, 0, 128)
+    plan = Plan(lay, [4], [70], rng)
+    pos = np.array([2 ** 30 + 7, 0, 999_983, -5], dtype=np.int32)
+    check_append(lay, plan, "f32", rng, positions=pos)
+
+
+def test_append_borders_of_the_codes():
+    """Values on every midpoint of the grid, for blocks of every exponent that a type reaches."""
+    lay = ko.Layout(1, 1, 64, 16)
+    mid = np.array([0, 0.25, 0.5, 0.75, 1.25, 1.75, 2.5, 3.5, 5, 6, 6.5, 7, -0.25, -0.75, -5, -7, -0.0])
+    exps = [0, 1, -1, 30, 100, 124, 125, -100, -126, -130, -140]
+    rows = []
+    for e in exps:
+        for top in (7.0, 7.0000005, 6.0, 4.0):
+            b = np.resize(mid, 31)
+            rows.append(np.concatenate([[top], np.clip(b, -top, top)]) * 2.0 ** e)
+    rows += [np.zeros(32), np.full(32, 3.4028234e38), np.full(32, 1e-45)]
+    if len(rows) % 2:
+        rows.append(np.ones(32))
+    v = np.array(rows, dtype=np.float32).reshape(-1, 1, 64)
+    T = len(v)
+    plan = Plan(lay, [T], [T], np.random.default_rng(0))
+    cache = plan.empty_cache()
+    got, _ = run_append(lay, plan, cache, dev(v), dev(v), dev(v))
+    want = cache.copy()
+    ko.append(lay, want, plan.offsets, plan.lens, plan.table, v, v, v)
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("what", [np.nan, np.inf, -np.inf])
+def test_a_token_that_is_not_finite_is_nan_for_those_who_see_it(where, what):
+    rng = np.random.default_rng(7)
+    lay = ko.Layout(4, 2, 64, 16, 0, 32)
+    plan = Plan(lay, [4], [20], rng)
+    q, q64 = rounded(rng.standard_normal((4, 4, 64)), "bf16")
+    kv = {n: rng.standard_normal((4, 2, 64)) for n in "kv"}
+    kv[where][2, 1, 40] = what  # the third row, the second head
+    k, k64 = rounded(kv["k"], "bf16")
+    v, v64 = rounded(kv["v"], "bf16")
+    f = np.full(16, 0.5, np.float32)
+    cache = plan.filled_cache(rng)
+    got, _ = run_append(lay, plan, cache, q, k, v, inv_freq=dev(f))
+    ko.append(lay, cache, plan.offsets, plan.lens, plan.table, q64, k64, v64, inv_freq=f)
+    assert np.array_equal(got, cache)
+    out = torch.empty_like(q)
+    svr.moe_kv_attention(desc_of(lay), plan.batch(), q, dev(got), out)
+    bad = torch.isnan(out).cpu().numpy()
+    assert bad[2:, 2:].all() and not bad[:2].any() and not bad[:, :2].any()
+
+
+def test_append_where_there_is_no_place():
+    """Negative places, places beyond the table, pages outside the cache: queries are made, nothing is stored."""
+    rng = np.random.default_rng(8)
+    lay = ko.Layout(2, 1, 64, 16, 0, 32)
+    plan = Plan(lay, [4, 3, 2], [2, 35, 18], rng, width=2)  # sequence 0: two rows before place 0; 1: beyond 32
+    plan.table[2, 1] = plan.n_pages                        # sequence 2: its second page is not there
+    check_append(lay, plan, "f32", rng)
+
+
+def test_append_without_queries_and_read():
+    rng = np.random.default_rng(9)
+    lay = ko.Layout(6, 3, 192, 32)
+    plan = Plan(lay, [3, 0, 2], [40, 5, 2], rng, pad_rows=1)
+    plan.table[0, 1] = -1  # the page of sequence 0's rows (places 37 to 39)
+    k, k64 = rounded(rng.standard_normal((6, 3, 192)), "f16")
+    v, v64 = rounded(rng.standard_normal((6, 3, 192)), "f16")
+    v[3, 1, 7] = float("nan")
+    v64[3, 1, 7] = np.nan
+    c = dev(plan.empty_cache())
+    svr.moe_kv_append(desc_of(lay), plan.batch(), None, k, v, c, None)
+    want = plan.empty_cache()
+    ko.append(lay, want, plan.offsets, plan.lens, plan.table, np.zeros((6, 6, 192)), k64, v64)
+    assert np.array_equal(c.cpu().numpy(), want)
+    ko_, vo = (torch.full((6, 3, 192), 7.0, device="cuda") for _ in "kv")
+    svr.moe_kv_read(desc_of(lay), plan.batch(), c, ko_, vo)
+    ko_, vo = ko_.cpu().numpy(), vo.cpu().numpy()
+    for h in range(3):
+        K, V, _ = ko.stored(lay, want, plan.table[2], 2, h)
+        assert np.array_equal(ko_[3:5, h], K, equal_nan=True) and np.array_equal(vo[3:5, h], V)
+    assert np.isnan(ko_[3, 1]).all() and not vo[3, 1].any()
+    assert not ko_[:3].any() and not vo[:3].any()   # not stored: zeros
+    assert (ko_[5] == 7).all() and (vo[5] == 7).all()  # no sequence: left alone
+    only = torch.empty((6, 3, 192), device="cuda")
+    svr.moe_kv_read(desc_of(lay), plan.batch(), c, None, only)
+    assert np.array_equal(only[:5].cpu().numpy(), vo[:5])
+
+
+def check_attention(lay, plan, cache, dtype, rng, scale=None, q=None, want_lse=True, ws=None):
+    T = plan.T
+    qt, q64 = rounded(rng.standard_normal((T, lay.heads, lay.dim)), dtype) if q is None else q
+    out = torch.full((T, lay.heads, lay.dim), 77.0, dtype=TYPES[dtype], device="cuda")
+    lse = torch.full((T, lay.heads), 77.0, device="cuda") if want_lse else None
+    svr.moe_kv_attention(desc_of(lay, scale or 0.0), plan.batch(), qt, dev(cache), out, lse, ws=ws)
+    torch.cuda.synchronize()
+    ref, rl, size, reach, seen = ko.attention(lay, cache, plan.offsets, plan.lens, plan.table, q64, scale)
+    n = plan.offsets[-1]
+    got = out.double().cpu().numpy()
+    assert (got[n:] == 77).all()
+    tol = attention_tolerance(dtype, ref, size, reach, seen, lay.dim)[:n]
+    err = np.abs(got[:n] - ref[:n])
+    assert np.all(err <= tol), (np.nanmax(err - tol), np.nanmax(err))
+    if want_lse:
+        g = lse.double().cpu().numpy()
+        assert (g[n:] == 77).all()
+        g, r = g[:n], rl[:n]
+        empty = np.isneginf(r)
+        assert np.array_equal(np.isneginf(g), empty)
+        # The score's roundings, the weights' sum (a rounding for each token), the logarithm and its sum.
+        u = 2.0 ** -24
+        t = (lay.dim + 4) * u * reach[:n] + (64 + seen[:n, None]) * u + 8 * u * np.abs(np.where(empty, 0, r))
+        assert np.all(np.abs(g - r)[~empty] <= t[~empty])
+    return got, ref
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("dim,heads,kv_heads,page,window", [
+    (64, 4, 4, 16, 0), (128, 8, 2, 32, 0), (192, 16, 1, 64, 0), (256, 10, 2, 16, 0),
+    (192, 32, 2, 16, 7), (128, 5, 1, 64, 100), (64, 64, 1, 128, 33), (256, 16, 1, 32, 64),
+])
+def test_attention_batches(dtype, dim, heads, kv_heads, page, window):
+    log(f"attention {dtype} D={dim} {heads}/{kv_heads} page={page} W={window}")
+    rng = np.random.default_rng(dim * heads + page)
+    lay = ko.Layout(heads, kv_heads, dim, page, window)
+    # Lengths of one token, a page, odd ones; no row; a length of zero; fewer tokens than rows.
+    plan = Plan(lay, [1, 4, 0, 3, 2, 5, 1], [1, 4, 9, 130, 257, 3, 0], rng, pad_rows=3)
+    got, _ = check_attention(lay, plan, plan.filled_cache(rng), dtype, rng)
+    i = plan.offsets[5]
+    assert not got[i:i + 2].any()             # two rows before place 0 see nothing
+    assert not got[plan.offsets[6]].any()     # an empty sequence
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 7, 33])
+def test_attention_rows_share_a_tile(rows):
+    rng = np.random.default_rng(rows)
+    for heads, kv_heads in ((16, 1), (6, 2)):
+        lay = ko.Layout(heads, kv_heads, 64, 16)
+        plan = Plan(lay, [rows, 1], [rows + 61, 200], rng)
+        check_attention(lay, plan, plan.filled_cache(rng), "bf16", rng)
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 192), ("f32", 64), ("f16", 128)])
+def test_attention_over_many_tokens(dtype, dim):
+    """Long enough for every split of the axis; a table wider than the tokens."""
+    rng = np.random.default_rng(11)
+    lay = ko.Layout(8, 1, dim, 64)
+    plan = Plan(lay, [4], [3001], rng, width=200)
+    check_attention(lay, plan, plan.filled_cache(rng), dtype, rng)
+
+
+def test_attention_where_one_score_stands_out():
+    """Peaked rows, and maxima that keep growing along the axis (every tile rescales)."""
+    rng = np.random.default_rng(12)
+    lay = ko.Layout(4, 1, 64, 16)
+    plan = Plan(lay, [2], [1500], rng)
+    cache = plan.filled_cache(rng)
+    for t in range(1500):
+        page, o = ko.slot(lay, plan.table[0], plan.n_pages, t)
+        kc, _, ks, _ = ko.page_parts(lay, cache[page, 0])
+        kc[o], ks[o] = 0x22, 110 + t // 100  # all channels alike, growing
+    q = np.zeros((2, 4, 64))
+    q[:, 0], q[:, 1], q[:, 2], q[:, 3] = 40.0, 3.0, -40.0, rng.standard_normal(64)
+    check_attention(lay, plan, cache, "f32", rng, q=rounded(q, "f32"))
+    check_attention(lay, plan, cache, "bf16", rng, q=rounded(q, "bf16"), scale=0.01)
+
+
+def test_attention_hides_pages_that_are_not_there():
+    rng = np.random.default_rng(13)
+    lay = ko.Layout(4, 2, 128, 16)
+    plan = Plan(lay, [3, 2], [100, 40], rng)
+    cache = plan.filled_cache(rng)
+    plan.table[0, 2], plan.table[0, 5], plan.table[1, 0] = -1, plan.n_pages, 2 ** 31 - 1
+    cache[0] = 0xFF  # whatever stands in a page that a hidden token could be read from
+    for b in range(2):
+        plan.table[b][plan.table[b] == 0] = -7
+    check_attention(lay, plan, cache, "bf16", rng)
+    plan.table[:] = -1
+    got, _ = check_attention(lay, plan, cache, "f32", rng)
+    assert not got[:plan.offsets[-1]].any()
+
+
+def test_attention_lengths_beyond_the_table():
+    rng = np.random.default_rng(14)
+    lay = ko.Layout(2, 1, 64, 16)
+    plan = Plan(lay, [2, 2], [30, 64], rng, width=2)
+    check_attention(lay, plan, plan.filled_cache(rng), "f32", rng)
+
+
+def test_attention_leaves_rows_beyond_max_rows():
+    rng = np.random.default_rng(15)
+    lay = ko.Layout(2, 1, 64, 16)
+    plan = Plan(lay, [5, 2], [30, 20], rng)
+    plan.max_rows = 3
+    q, q64 = rounded(rng.standard_normal((7, 2, 64)), "bf16")
+    cache = plan.filled_cache(rng)
+    out = torch.full((7, 2, 64), 77.0, dtype=torch.bfloat16, device="cuda")
+    svr.moe_kv_attention(desc_of(lay), plan.batch(), q, dev(cache), out)
+    ref, _, size, reach, seen = ko.attention(lay, cache, plan.offsets, plan.lens, plan.table, q64)
+    got = out.double().cpu().numpy()
+    assert (got[3:5] == 77).all()
+    keep = [0, 1, 2, 5, 6]
+    tol = attention_tolerance("bf16", ref, size, reach, seen, 64)
+    assert np.all(np.abs(got - ref)[keep] <= tol[keep])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_attention_queries_apart_and_unaligned(dtype):
+    rng = np.random.default_rng(16)
+    lay = ko.Layout(4, 2, 64, 16)
+    plan = Plan(lay, [2, 3], [20, 33], rng)
+    cache = plan.filled_cache(rng)
+    t, q64 = rounded(rng.standard_normal((5, 4, 64)), dtype)
+    for width, at in ((320, 32), (259, 0), (264, 1)):
+        buf = torch.zeros((5, width), dtype=t.dtype, device="cuda")
+        q = buf[:, at:at + 256]
+        q.copy_(t.flatten(1))
+        check_attention(lay, plan, cache, dtype, rng, q=(q.unflatten(1, (4, 64)), q64))
+
+
+def test_cache_beyond_four_gibibytes():
+    """The last pages of a cache of 4.6 GB: offsets that pass 32 bits."""
+    rng = np.random.default_rng(17)
+    lay = ko.Layout(8, 8, 256, 1024)
+    plan = Plan(lay, [2], [40], rng, spare=0)
+    n = 2100
+    assert n * 8 * lay.page_bytes > 4.2 * 2 ** 30
+    big = svr.kv_cache(desc_of(lay), n)
+    small = plan.empty_cache(0)
+    k, k64 = rounded(rng.standard_normal((2, 8, 256)), "bf16")
+    v, v64 = rounded(rng.standard_normal((2, 8, 256)), "bf16")
+    small[:] = plan.filled_cache(rng)
+    big[n - 1] = dev(small[plan.table[0, 0]])
+    batch = svr.KvBatch(dev(plan.offsets), dev(plan.lens), dev(np.array([[n - 1]], np.int32)), 2)
+    q, q64 = rounded(rng.standard_normal((2, 8, 256)), "bf16")
+    qo, out = torch.empty_like(q), torch.empty_like(q)
+    svr.moe_kv_append(desc_of(lay), batch, q, k, v, big, qo)
+    svr.moe_kv_attention(desc_of(lay), batch, qo, big, out)
+    ko.append(lay, small, plan.offsets, plan.lens, plan.table, q64, k64, v64)
+    assert np.array_equal(big[n - 1].cpu().numpy(), small[plan.table[0, 0]])
+    assert torch.equal(qo, q)  # neither norm nor rotation
+    ref, _, size, reach, seen = ko.attention(lay, small, plan.offsets, plan.lens, plan.table, q64)
+    err = np.abs(out.double().cpu().numpy() - ref)
+    assert np.all(err <= attention_tolerance("bf16", ref, size, reach, seen, 256))
+
+
+def test_append_and_attention_replayed_from_a_graph():
+    """Captured once, replayed with eager work between; another stream and another workspace meanwhile."""
+    rng = np.random.default_rng(18)
+    lay = ko.Layout(16, 2, 128, 16, 0, 64)
+    plan = Plan(lay, [4, 4], [300, 41], rng)
+    q, _ = rounded(rng.standard_normal((8, 16, 128)), "bf16")
+    k, _ = rounded(rng.standard_normal((8, 2, 128)), "bf16")
+    v, _ = rounded(rng.standard_normal((8, 2, 128)), "bf16")
+    f = dev((10000.0 ** (-np.arange(0, 64, 2) / 64)).astype(np.float32))
+    d, batch = desc_of(lay), plan.batch()
+    cache = dev(plan.filled_cache(rng))
+    start = cache.clone()
+    qo, out = torch.empty_like(q), torch.empty_like(q)
+    ws, ws2 = svr.kv_workspace(d, batch, 8), svr.kv_workspace(d, batch, 8)
+
+    def step(c, qo, out, ws, stream=None):
+        svr.moe_kv_append(d, batch, q, k, v, c, qo, inv_freq=f, stream=stream)
+        svr.moe_kv_attention(d, batch, qo, c, out, ws=ws, stream=stream)
+
+    step(cache, qo, out, ws)
+    torch.cuda.synchronize()
+    want, want_cache = out.clone(), cache.clone()
+    g, side, other = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        step(cache, qo, out, ws)
+    c2, qo2, out2 = start.clone(), torch.empty_like(q), torch.empty_like(q)
+    for i in range(4):
+        cache.copy_(start)
+        out.fill_(float("nan"))
+        out2.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        step(c2, qo2, out2, ws2, stream=other)  # two calls at once
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(cache, want_cache), i
+        assert torch.equal(out2, want) and torch.equal(c2, want_cache), i
+
+
+def test_rejected_drafts_are_overwritten():
+    """A verify round whose tail is rejected: lower lengths and append again gives the cache of a clean run."""
+    rng = np.random.default_rng(19)
+    lay = ko.Layout(8, 2, 64, 16)
+    first = Plan(lay, [4], [35], rng)
+    cache = first.filled_cache(rng)
+    d = desc_of(lay)
+    x = [rounded(rng.standard_normal((4, 2, 64)), "bf16")[0] for _ in range(4)]
+    q, q64 = rounded(rng.standard_normal((4, 8, 64)), "bf16")
+    c = dev(cache)
+    svr.moe_kv_append(d, first.batch(), None, x[0], x[1], c, None)
+    # One draft of three accepted: places 31 and 32 stay, the next round starts at 33.
+    second = Plan(lay, [4], [37], rng)
+    second.table, second.n_pages = first.table, first.n_pages
+    svr.moe_kv_append(d, second.batch(), None, x[2], x[3], c, None)
+    want = cache.copy()
+    a = [t.double().cpu().numpy() for t in x]
+    zq = np.zeros((2, 8, 64))
+    ko.append(lay, want, [0, 2], [33], first.table, zq, a[0][:2], a[1][:2])
+    ko.append(lay, want, [0, 4], [37], first.table, q64, a[2], a[3])
+    assert np.array_equal(c.cpu().numpy(), want)
+    check_attention(lay, second, want, "bf16", rng, q=(q, q64))
