@@ -11,12 +11,31 @@ extern template int32_t launch_kv_attention<256>(const AttnArgs&, int32_t, int, 
 
 namespace {
 
-// One wave a row and head: weighs its splits' sums by their maxima.
-template <typename T>
+constexpr int kMaxSplits = 128;
+
+// Joins the splits of one row and head: out = sum_s w_s O_s / sum_s w_s l_s
+// with w_s = 2^(m_s - max m).  One workgroup a row and head; a slot of D/4
+// lanes reads a split's sums 16 bytes a lane, the slots take the splits in
+// turn.  Bound by latency, not bytes (a row's parts are at most 128 KB): the
+// first batch of every read is issued before it is known which splits are in
+// use (the workspace holds them all, what is not in use is dropped).
+template <int D, typename T>
 __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a, int row_tiles) {
+  constexpr int L = D / 4, kSlots = kBlock / L, kBatch = 4;
+  __shared__ float s_w[kMaxSplits];
+  __shared__ f32x4v s_o[kSlots][L];
   const int lane = threadIdx.x & (kWave - 1);
-  const int64_t at = (int64_t)blockIdx.x * kWavesPerBlock + (threadIdx.x >> 6);
-  if (at >= (int64_t)a.kv.n_tokens * a.kv.Hq) return;
+  const int64_t at = blockIdx.x;
+  const int slot = threadIdx.x / L, c = threadIdx.x % L;
+  const float2* ml = a.part_ml + at * a.splits;
+  const f32x4v* part = reinterpret_cast<const f32x4v*>(a.part_o + at * a.splits * D) + c;
+  float2 x[kMaxSplits / kWave];
+#pragma unroll
+  for (int j = 0; j < kMaxSplits / kWave; ++j) x[j] = ml[min(lane + kWave * j, a.splits - 1)];
+  f32x4v v[kBatch];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) v[j] = part[(int64_t)min(slot + kSlots * j, a.splits - 1) * L];
+
   const int i = (int)(at / a.kv.Hq), h = (int)(at % a.kv.Hq);
   const int b = kv_sequence_of(a.kv, i);
   if (b < 0) return;
@@ -25,25 +44,55 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a, int row_tiles) {
   if (m >= sq.rows) return;
   const int r = m * a.G + h % a.G, r0 = r / (16 * row_tiles) * (16 * row_tiles);
   const int r_last = min(sq.rows * a.G, r0 + 16 * row_tiles) - 1;
-  const KvRange rg = kv_range(a.kv, sq.len, sq.place0 + r0 / a.G, sq.place0 + r_last / a.G, a.splits,
-                              a.min_tiles);
-  if (rg.used == 1) return;
-  const float2* ml = a.part_ml + at * a.splits;
-  float M = -INFINITY;
-  for (int s = 0; s < rg.used; ++s) M = fmaxf(M, ml[s].x);
-  float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  const int n = a.kv.D / kWave;
-  for (int s = 0; s < rg.used; ++s) {
-    const float2 x = ml[s];
-    const float w = x.x == M ? 1.f : __builtin_amdgcn_exp2f(x.x - M);
-    L += w * x.y;
-    const float* p = a.part_o + (at * a.splits + s) * a.kv.D + lane;
-    for (int j = 0; j < n; ++j) o[j] += w * p[kWave * j];
+  const int used = kv_range(a.kv, sq.len, sq.place0 + r0 / a.G, sq.place0 + r_last / a.G, a.splits,
+                            a.min_tiles).used;
+  if (used == 1) return;  // written whole
+  float M = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < kMaxSplits / kWave; ++j)
+    if (lane + kWave * j < used) M = fmaxf(M, x[j].x);
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) M = fmaxf(M, __shfl_xor(M, o, kWave));
+#pragma unroll
+  for (int j = 0; j < kMaxSplits / kWave; ++j)
+    if (lane + kWave * j < used) {
+      const float w = x[j].x == M ? 1.f : __builtin_amdgcn_exp2f(x[j].x - M);
+      sum += w * x[j].y;
+      if (threadIdx.x < kWave) s_w[lane + kWave * j] = w;
+    }
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) sum += __shfl_xor(sum, o, kWave);
+  __syncthreads();
+  f32x4v acc = {0.f, 0.f, 0.f, 0.f};
+  if (slot < kSlots) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int s = slot + kSlots * j;
+      if (s < used) acc += s_w[s] * v[j];
+    }
+#pragma unroll 4
+    for (int s = slot + kSlots * kBatch; s < used; s += kSlots) acc += s_w[s] * part[(int64_t)s * L];
+    s_o[slot][c] = acc;
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  for (int j = 0; j < n; ++j) ((T*)a.out)[at * a.kv.D + lane + kWave * j] = (T)(o[j] * inv);
-  if (a.lse && lane == 0)
-    a.lse[at] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.6931471805599453f;
+  __syncthreads();
+  if (slot != 0) return;
+#pragma unroll
+  for (int j = 1; j < kSlots; ++j) acc += s_o[j][c];
+  acc *= sum == 0.f ? 0.f : 1.f / sum;
+  T* out = (T*)a.out + at * D + 4 * c;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) out[e] = (T)acc[e];
+  if (a.lse && c == 0)
+    a.lse[at] = sum == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+}
+
+template <int D>
+void launch_kv_join(const AttnArgs& a, int32_t dtype, int row_tiles, unsigned n, hipStream_t st) {
+  switch (dtype) {
+    case MOE_F32: hipLaunchKernelGGL((k_kv_join<D, float>), dim3(n), dim3(kBlock), 0, st, a, row_tiles); break;
+    case MOE_BF16: hipLaunchKernelGGL((k_kv_join<D, bf16>), dim3(n), dim3(kBlock), 0, st, a, row_tiles); break;
+    default: hipLaunchKernelGGL((k_kv_join<D, _Float16>), dim3(n), dim3(kBlock), 0, st, a, row_tiles); break;
+  }
 }
 
 // How a batch is cut: by its sizes alone (the lengths are on the device).
@@ -65,7 +114,7 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   if (d->window && d->window + (int64_t)b->max_rows < seen) seen = d->window + (int64_t)b->max_rows;
   const int64_t most = (seen / kAttnTile + 2 + p.min_tiles - 1) / p.min_tiles;
   int64_t s = base > 0 ? 512 / base : 1;
-  s = s < 1 ? 1 : s;
+  s = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
   p.splits = (int)(s < most ? s : most);
   p.grid = base * p.splits;
   if (p.splits > 1) {
@@ -145,12 +194,12 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
     default: rc = launch_kv_attention<256>(a, dtype, p.row_tiles, (int)p.grid, st); break;
   }
   if (rc != MOE_OK || p.splits == 1) return rc;
-  const int64_t n = (int64_t)batch->n_tokens * desc->n_heads;
-  const dim3 g((unsigned)((n + kWavesPerBlock - 1) / kWavesPerBlock)), t(kBlock);
-  switch (dtype) {
-    case MOE_F32: hipLaunchKernelGGL(k_kv_join<float>, g, t, 0, st, a, p.row_tiles); break;
-    case MOE_BF16: hipLaunchKernelGGL(k_kv_join<bf16>, g, t, 0, st, a, p.row_tiles); break;
-    default: hipLaunchKernelGGL(k_kv_join<_Float16>, g, t, 0, st, a, p.row_tiles); break;
+  const unsigned n = (unsigned)batch->n_tokens * (unsigned)desc->n_heads;
+  switch (desc->head_dim) {
+    case 64: launch_kv_join<64>(a, dtype, p.row_tiles, n, st); break;
+    case 128: launch_kv_join<128>(a, dtype, p.row_tiles, n, st); break;
+    case 192: launch_kv_join<192>(a, dtype, p.row_tiles, n, st); break;
+    default: launch_kv_join<256>(a, dtype, p.row_tiles, n, st); break;
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }

@@ -202,7 +202,7 @@ def check_attention(lay, plan, cache, dtype, rng, scale=None, q=None, want_lse=T
         # The score's roundings, the weights' sum (a rounding for each token), the logarithm and its sum.
         u = 2.0 ** -24
         t = (lay.dim + 4) * u * reach[:n] + (64 + seen[:n, None]) * u + 8 * u * np.abs(np.where(empty, 0, r))
-        assert np.all(np.abs(g - r)[~empty] <= t[~empty])
+        assert np.all(np.abs(g[~empty] - r[~empty]) <= t[~empty])
     return got, ref
 
 

@@ -40,11 +40,11 @@ def check(x, targets, k, ws=None):
         r, g = ref[n], got[n].astype(np.float64)
         assert np.array_equal(np.isnan(r), np.isnan(g)) and np.array_equal(np.isinf(r), np.isinf(g)), n
         f = np.isfinite(r)
-        assert np.all(np.abs(g - r)[f] <= rel + 4 * u * np.abs(r[f])), n
+        assert np.all(np.abs(g[f] - r[f]) <= rel + 4 * u * np.abs(r[f])), n
     r, g = ref["entropy"], got["entropy"].astype(np.float64)
     assert np.array_equal(np.isnan(r), np.isnan(g))
     f = np.isfinite(r)
-    assert np.all(np.abs(g - r)[f] <= 2 * rel * (1 + np.abs(r[f])) + 8 * u * 20)
+    assert np.all(np.abs(g[f] - r[f]) <= 2 * rel * (1 + np.abs(r[f])) + 8 * u * 20)
     return got
 
 
