@@ -410,18 +410,29 @@ def _rows(device: torch.device, t: torch.Tensor, dtype, shape, what: str):
     return t.data_ptr(), (row if shape[0] == 1 else s[0])
 
 
+def _current_stream_handle(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# torch's own lookup of the handle, without the Stream object around it (2 us of a 12 us call).
+_current_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream_handle)
+
+
 def _call_on(device: torch.device, stream, f, *args) -> int:
     """f(*args, stream) with `device` current; its current stream where none is given."""
     if device.type != "cuda":
         raise ValueError("expected a device tensor")
+    index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        handle = _current_stream_handle(index)
     elif stream.device != device:
         raise ValueError(f"expected a stream of {device}, got one of {stream.device}")
-    if device.index == torch.cuda.current_device():
-        return f(*args, stream.cuda_stream)
+    else:
+        handle = stream.cuda_stream
+    if index == torch.cuda.current_device():
+        return f(*args, handle)
     with torch.cuda.device(device):
-        return f(*args, stream.cuda_stream)
+        return f(*args, handle)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -437,10 +448,15 @@ class KvDesc:
     scale: float = 0.0  # 0: 1/sqrt(head_dim)
     norm_eps: float = 1e-6
 
+    def __post_init__(self):
+        # The fields never change, so the C struct is made once.
+        object.__setattr__(self, "_c", _KvDesc(
+            self.n_heads, self.n_kv_heads, self.head_dim, self.page_size, self.window,
+            self.rotary_dims, KV_ROTARY_INTERLEAVED if self.rotary_interleaved else 0, self.scale,
+            self.norm_eps))
+
     def c(self) -> _KvDesc:
-        return _KvDesc(self.n_heads, self.n_kv_heads, self.head_dim, self.page_size, self.window,
-                       self.rotary_dims, KV_ROTARY_INTERLEAVED if self.rotary_interleaved else 0,
-                       self.scale, self.norm_eps)
+        return self._c
 
     @property
     def page_bytes(self) -> int:
@@ -448,25 +464,35 @@ class KvDesc:
         return self.page_size * (self.head_dim + self.head_dim // 16)
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True)
 class KvBatch:
     """New rows of a batch of sequences (moe_kv_batch): int32 device tensors
     q_offsets [B+1], seq_lens [B] (new rows included), page_table [B][pages];
-    max_rows: no sequence has more new rows."""
+    max_rows: no sequence has more new rows.  The tensors are captured by
+    reference, as PreparedForward does: write new lengths into them, or make
+    another KvBatch."""
     q_offsets: torch.Tensor
     seq_lens: torch.Tensor
     page_table: torch.Tensor
     max_rows: int
 
-    def c(self, n_tokens: int) -> _KvBatch:
+    def __post_init__(self):
         i32, dev = torch.int32, self.page_table.device
         if self.page_table.dim() != 2:
             raise ValueError("page_table: expected [sequences][pages]")
-        B = self.page_table.shape[0]
-        return _KvBatch(B, n_tokens, self.max_rows, self.page_table.shape[1],
-                        _on(dev, self.q_offsets, i32, (B + 1,), "q_offsets"),
-                        _on(dev, self.seq_lens, i32, (B,), "seq_lens"),
-                        _on(dev, self.page_table, i32, None, "page_table"))
+        B, width = self.page_table.shape
+        args = (width, _on(dev, self.q_offsets, i32, (B + 1,), "q_offsets"),
+                _on(dev, self.seq_lens, i32, (B,), "seq_lens"),
+                _on(dev, self.page_table, i32, None, "page_table"))
+        object.__setattr__(self, "_args", args)
+        object.__setattr__(self, "_c", None)
+
+    def c(self, n_tokens: int) -> _KvBatch:
+        c = self._c
+        if c is None or c.n_tokens != n_tokens:
+            c = _KvBatch(self.page_table.shape[0], n_tokens, self.max_rows, *self._args)
+            object.__setattr__(self, "_c", c)
+        return c
 
 
 def moe_kv_cache_bytes(desc: KvDesc, n_pages: int) -> int:

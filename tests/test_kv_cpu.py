@@ -249,8 +249,7 @@ def test_the_binding_refuses_what_it_cannot_pass_on():
     with pytest.raises(ValueError, match="inv_freq: expected shape"):
         svr.moe_kv_append(kv_desc(rotary_dims=64), batch, None, kv, kv, cache, None, inv_freq=torch.zeros(16))
     with pytest.raises(ValueError, match="seq_lens: expected shape"):
-        bad = svr.KvBatch(batch.q_offsets, torch.zeros(2, dtype=torch.int32), batch.page_table, 1)
-        svr.moe_kv_append(d, bad, None, kv, kv, cache, None)
+        svr.KvBatch(batch.q_offsets, torch.zeros(2, dtype=torch.int32), batch.page_table, 1)
     with pytest.raises(ValueError, match="out: expected shape"):
         svr.moe_kv_attention(d, batch, q, cache, q[:, :4], ws=cache.view(-1))
     with pytest.raises(ValueError, match="k_out or v_out"):
