@@ -4,11 +4,11 @@
 // A workgroup takes one key/value head of one sequence, 16 * RT of the rows
 // that read it (row = new token x query head of the group, so four drafts of
 // sixteen heads share every key that is read) and a stretch of the tokens;
-// its waves take tiles of the stretch in turn, each with a softmax of its
-// own, joined at the end.  Scores are taken transposed, S^T = K Q^T, so that
-// a lane holds four tokens of one row: the maximum and sum of a row need no
-// exchange inside a tile, and the weights are at once the right operand of
-// O^T = V^T P^T.
+// its waves take 32 tokens of the stretch in turn, each with a softmax of its
+// own, joined at the end: no wave waits for another.
+//   Scores are taken transposed, S^T = K Q^T, so that a lane holds four
+// tokens of one row: the maximum and sum of a row need no exchange inside a
+// tile, and the weights are at once the right operand of O^T = V^T P^T.
 //   Keys go from memory to registers: a lane's 16 bytes are 32 channels of
 // one token under one scale, four k-steps of the 16x16x32 product (the
 // channels of a step are permuted, the same way in the query).  Values need
@@ -40,7 +40,7 @@ struct AttnArgs {
 };
 
 constexpr int kAttnWaves = 4;
-constexpr int kAttnTile = 64;  // tokens of a wave's step
+constexpr int kAttnTile = 32;  // tokens of a wave's step
 
 // The tokens [beg, end) that rows of places [first, last] see, in tiles from
 // tb on, `per` of them a split, `used` splits (at least one).
@@ -93,37 +93,55 @@ __device__ __forceinline__ void split_terms(float x, bf16 (&t)[NT]) {
 }
 
 // A lane's codes and scales of one token for D/4 channels: the full 128s in
-// 16-byte pieces, a last 64 in 8 bytes.
+// 16-byte pieces, a last 64 in 8 bytes.  A scale is kept as the aligned dword
+// that holds it and its place there: of a byte the compiler keeps eight bits
+// from tile to tile, and widens them where it was loaded, which would wait
+// for the next tile's codes in the middle of this one.
 template <int D>
 struct Codes {
   uint32_t w[D / 32];
-  uint32_t e[(D + 127) / 128];
+  uint32_t e[(D + 127) / 128], at[(D + 127) / 128];
+
+  // The scale of word k, in the exponent of a float.
+  __device__ __forceinline__ float scale(int k) const {
+    return __builtin_bit_cast(float, __builtin_amdgcn_ubfe(e[k / 4], at[k / 4], 8) << 23);
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) w[k] = 0;
+#pragma unroll
+    for (int p = 0; p < (D + 127) / 128; ++p) e[p] = 0x7F7F7F7Fu;
+  }
 };
 
+// Token i of a page's codes and scales (the scales are 4-byte aligned).
 template <int D>
-__device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* scales, int g,
+__device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* scales, int i, int g,
                                            Codes<D>& x) {
+  codes += i * (D / 2);
 #pragma unroll
-  for (int p = 0; p < D / 128; ++p) {
-    const uint4 v = *reinterpret_cast<const uint4*>(codes + 64 * p + 16 * g);
-    x.w[4 * p] = v.x;
-    x.w[4 * p + 1] = v.y;
-    x.w[4 * p + 2] = v.z;
-    x.w[4 * p + 3] = v.w;
-    x.e[p] = scales[4 * p + g];
-  }
-  if constexpr (D % 128 != 0) {
-    constexpr int p = D / 128;
-    const uint2 v = *reinterpret_cast<const uint2*>(codes + 64 * p + 8 * g);
-    x.w[4 * p] = v.x;
-    x.w[4 * p + 1] = v.y;
-    x.e[p] = scales[4 * p + g / 2];
+  for (int p = 0; p < (D + 127) / 128; ++p) {
+    int at = i * (D / 32) + 4 * p;
+    if (64 * (2 * p + 1) < D) {
+      const uint4 v = *reinterpret_cast<const uint4*>(codes + 64 * p + 16 * g);
+      x.w[4 * p] = v.x;
+      x.w[4 * p + 1] = v.y;
+      x.w[4 * p + 2] = v.z;
+      x.w[4 * p + 3] = v.w;
+      at += g;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(codes + 64 * p + 8 * g);
+      x.w[4 * p] = v.x;
+      x.w[4 * p + 1] = v.y;
+      at += g / 2;
+    }
+    x.e[p] = *reinterpret_cast<const uint32_t*>(scales + (at & ~3));
+    x.at[p] = 8 * (at & 3);
   }
 }
 
-// Eight codes times 2^(e-127) as bf16 (NaN for e = 255).
-__device__ __forceinline__ bf16x8 widen(uint32_t w, uint32_t e) {
-  const float s = __builtin_bit_cast(float, e << 23);
+// Eight codes times s, a power of two, as bf16 (NaN where its exponent is 255).
+__device__ __forceinline__ bf16x8 widen(uint32_t w, float s) {
   const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
   const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
   const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
@@ -137,18 +155,23 @@ __device__ __forceinline__ s16x4 read_transposed(const uint8_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
 }
 
+// Waves of a SIMD that the registers are to leave room for: the queries
+// (D/8 a term) and sums (D/4) of a row tile decide.
+constexpr int attn_waves(int D, int RT, int NT) { return RT * (D / 8 * NT + D / 4) <= 160 ? 2 : 1; }
+
 template <int D, int RT, int NT, typename T>
-__global__ __launch_bounds__(kAttnWaves* kWave) void k_kv_attention(AttnArgs a) {
-  constexpr int KS = D / 32, CB = D / 16, SUB = kAttnTile / 16;
-  constexpr int kRowBytes = 2 * D + 32;            // a staged token: the pad spreads the banks
-  constexpr int kStage = 32 * kRowBytes;           // a wave's 32 staged tokens
+__global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv_attention(AttnArgs a) {
+  constexpr int KS = D / 32, CB = D / 16;
+  constexpr int kRowBytes = 2 * D + 16;            // a staged token: the pad spreads the banks
+  constexpr int kStage = kAttnTile * kRowBytes;    // a wave's staged tokens
   constexpr int kJoinRow = D + 4;                  // floats of a joined row
   constexpr int kJoin = kAttnWaves * 16 * kJoinRow * 4;
   constexpr int kMem = kAttnWaves * kStage > kJoin ? kAttnWaves * kStage : kJoin;
   __shared__ __attribute__((aligned(16))) uint8_t s_mem[kMem];
   __shared__ float2 s_ml[kAttnWaves][RT * 16];
 
-  const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x >> 6;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
 
   // Consecutive work on one XCD: row tiles of a head share its L2.
@@ -170,7 +193,45 @@ __global__ __launch_bounds__(kAttnWaves* kWave) void k_kv_attention(AttnArgs a) 
   const int first = sq.place0 + r0 / a.G, last = sq.place0 + r_last / a.G;
   const KvRange rg = kv_range(a.kv, sq.len, first, last, a.splits, a.min_tiles);
   if (split >= rg.used) return;
-  const int t_end = min(rg.ntile, (split + 1) * rg.per);
+  const int t_end = min(rg.ntile, (split + 1) * rg.per), t_last = t_end - 1;
+
+  // Sixteen tokens (a run) lie in one page.  A run outside [beg, end) becomes
+  // one inside, and so does a lane's token outside, so nothing but what some
+  // row sees is ever loaded.
+  const int P = 1 << a.kv.page_shift;
+  // Read through the scalar cache: as a plain load it would be a vector load
+  // whose wait holds up the tile.
+  const auto table = (const __attribute__((address_space(4))) int32_t*)(a.kv.table +
+                                                                        (int64_t)b * a.kv.pages_per_seq);
+  const int run_lo = rg.beg & ~15, run_hi = (rg.end - 1) & ~15;
+  auto run = [&](int t, int u) {
+    return min(max(rg.tb + min(t, t_last) * kAttnTile + 16 * u, run_lo), run_hi);
+  };
+  auto page_of = [&](int t, int u) { return table[run(t, u) >> a.kv.page_shift]; };
+  auto load_keys_or_values = [&](int t, int u, int page, int side, Codes<D>& x) {
+    page = (unsigned)page < (unsigned)a.kv.n_pages ? page : 0;
+    const uint8_t* c = a.cache + ((int64_t)page * a.kv.Hk + kvh) * a.kv.page_bytes;
+    const int i = min(max(run(t, u) + l16, rg.beg), rg.end - 1) & (P - 1);
+    load_codes<D>(c + side * (P * (D / 2)), c + P * D + side * (P * (D / 32)), i, g, x);
+  };
+
+  // One tile of codes is kept in flight: keys of the next tile are asked for
+  // as soon as this tile's are widened, values likewise, page numbers a tile
+  // before that.
+  int t = split * rg.per + wv;
+  int page[2], next_page[2];
+  Codes<D> kc[2], vc[2];
+  if (t < t_end) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      page[u] = page_of(t, u);
+      next_page[u] = page_of(t + kAttnWaves, u);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) load_keys_or_values(t, u, page[u], 0, kc[u]);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) load_keys_or_values(t, u, page[u], 1, vc[u]);
+  }
 
   // The rows' queries, and the tokens that each sees: [lo, hi].
   bf16x8 qf[RT][KS][NT];
@@ -197,7 +258,7 @@ __global__ __launch_bounds__(kAttnWaves* kWave) void k_kv_attention(AttnArgs a) 
       }
     }
   }
-  // Tiles between these need no mask.
+  // Tokens between these need no mask.
   const int all_hi = min(first, rg.end - 1), all_lo = a.kv.window ? last - a.kv.window + 1 : 0;
 
   float mx[RT], sum[RT];
@@ -210,37 +271,23 @@ __global__ __launch_bounds__(kAttnWaves* kWave) void k_kv_attention(AttnArgs a) 
     for (int cb = 0; cb < CB; ++cb) o[rt][cb] = f32x4v{0.f, 0.f, 0.f, 0.f};
   }
   uint8_t* stage = s_mem + wv * kStage;
-  const int P = 1 << a.kv.page_shift;
-  const int32_t* table = a.kv.table + (int64_t)b * a.kv.pages_per_seq;
 
-  for (int t = split * rg.per + wv; t < t_end; t += kAttnWaves) {
+  for (; t < t_end; t += kAttnWaves) {
     const int tok0 = rg.tb + t * kAttnTile;
-    Codes<D> kc[SUB], vc[SUB];
-    unsigned hidden = 0;  // subtiles on a page that is not there
+    bool gone[2];  // runs on a page that is not there
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      // Sixteen tokens lie in one page.  Lanes of tokens outside [beg, end)
-      // read a token inside, so nothing else is ever loaded.
-      const int st = min(max(tok0 + 16 * u, rg.beg & ~15), (rg.end - 1) & ~15);
-      int page = __builtin_amdgcn_readfirstlane(table[st >> a.kv.page_shift]);
-      if ((unsigned)page >= (unsigned)a.kv.n_pages) {
-        hidden |= 1u << u;
-        page = 0;
-      }
-      const uint8_t* c = a.cache + ((int64_t)page * a.kv.Hk + kvh) * a.kv.page_bytes;
-      const int i = min(max(st + l16, rg.beg), rg.end - 1) & (P - 1);
-      load_codes<D>(c + i * (D / 2), c + P * D + i * (D / 32), g, kc[u]);
-      load_codes<D>(c + (P + i) * (D / 2), c + P * D + (P + i) * (D / 32), g, vc[u]);
+    for (int u = 0; u < 2; ++u) {
+      gone[u] = (unsigned)page[u] >= (unsigned)a.kv.n_pages;
+      if (gone[u]) vc[u].clear();  // whatever lies there must not meet a weight of zero
     }
-
-    f32x4v s[RT][SUB];
+    f32x4v s[RT][2];
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
+    for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) s[rt][u] = f32x4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const bf16x8 kf = widen(kc[u].w[k], kc[u].e[k / 4]);
+        const bf16x8 kf = widen(kc[u].w[k], kc[u].scale(k));
 #pragma unroll
         for (int n = NT - 1; n >= 0; --n)
 #pragma unroll
@@ -248,26 +295,34 @@ __global__ __launch_bounds__(kAttnWaves* kWave) void k_kv_attention(AttnArgs a) 
             s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[rt][k][n], s[rt][u], 0, 0, 0);
       }
     }
-
-    if (hidden || tok0 + kAttnTile - 1 > all_hi || tok0 < all_lo) {
 #pragma unroll
-      for (int u = 0; u < SUB; ++u) {
-        const int tk = tok0 + 16 * u + 4 * g;
-        const bool gone = hidden >> u & 1;
+    for (int u = 0; u < 2; ++u) load_keys_or_values(t + kAttnWaves, u, next_page[u], 0, kc[u]);
+
+    // Values to shared memory, widened; the next ones are asked for.
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        *reinterpret_cast<bf16x8*>(stage + (16 * u + l16) * kRowBytes + 2 * step_channel<D>(k, g)) =
+            widen(vc[u].w[k], vc[u].scale(k));
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      load_keys_or_values(t + kAttnWaves, u, next_page[u], 1, vc[u]);
+      page[u] = next_page[u];
+      next_page[u] = page_of(t + 2 * kAttnWaves, u);
+    }
+
+    if (gone[0] || gone[1] || tok0 + kAttnTile - 1 > all_hi || tok0 < all_lo) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (gone || tk + i > hi[rt] || tk + i < lo[rt]) s[rt][u][i] = -INFINITY;
-        if (gone) {  // whatever lies there must not meet a weight of zero
-#pragma unroll
-          for (int k = 0; k < KS; ++k) vc[u].w[k] = 0;
-#pragma unroll
-          for (int p = 0; p < (D + 127) / 128; ++p) vc[u].e[p] = 127;
-        }
-      }
+          for (int i = 0; i < 4; ++i) {
+            const int tk = tok0 + 16 * u + 4 * g + i;
+            if (gone[u] || tk > hi[rt] || tk < lo[rt]) s[rt][u][i] = -INFINITY;
+          }
     }
-
     // Softmax.  The maximum in use follows only where a score passes it by
     // 2^8: weights up to 2^8 lose nothing in 32 bits, and most tiles then
     // need neither an exchange between lanes nor a rescaling of the sums.
@@ -277,9 +332,7 @@ __global__ __launch_bounds__(kAttnWaves* kWave) void k_kv_attention(AttnArgs a) 
     for (int rt = 0; rt < RT; ++rt) {
       float v = s[rt][0][0];
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v = fmaxf(v, s[rt][u][i]);
+      for (int i = 1; i < 8; ++i) v = fmaxf(v, s[rt][i / 4][i % 4]);
       top[rt] = v * a.c;
       grow |= top[rt] > mx[rt] + 8.f;
     }
@@ -297,50 +350,33 @@ __global__ __launch_bounds__(kAttnWaves* kWave) void k_kv_attention(AttnArgs a) 
         for (int cb = 0; cb < CB; ++cb) o[rt][cb] *= f;
       }
     }
+    bf16x8 pf[RT][NT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const float m0 = mx[rt] == -INFINITY ? 0.f : mx[rt];
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
+      for (int i = 0; i < 8; ++i) {
+        bf16 x[NT];
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[rt][i / 4][i % 4], a.c, -m0));
+        sum[rt] += p;
+        split_terms<NT>(p, x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(s[rt][u][i], a.c, -m0));
-          s[rt][u][i] = p;
-          sum[rt] += p;
-        }
+        for (int n = 0; n < NT; ++n) pf[rt][n][i] = x[n];
+      }
     }
 
-    // O^T += V^T P^T, 32 tokens at a time.
+    // O^T += V^T P^T.
+    const uint8_t* from = stage + (4 * g + l16 / 4) * kRowBytes + 8 * (l16 % 4);
 #pragma unroll
-    for (int u = 0; u < SUB; u += 2) {
+    for (int cb = 0; cb < CB; ++cb) {
+      struct { s16x4 a, b; } v{read_transposed(from + 32 * cb),
+                               read_transposed(from + 16 * kRowBytes + 32 * cb)};
+      const bf16x8 vf = __builtin_bit_cast(bf16x8, v);
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+      for (int n = NT - 1; n >= 0; --n)
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-          *reinterpret_cast<bf16x8*>(stage + (16 * y + l16) * kRowBytes + 2 * step_channel<D>(k, g)) =
-              widen(vc[u + y].w[k], vc[u + y].e[k / 4]);
-      bf16x8 pf[RT][NT];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          bf16 x[NT];
-          split_terms<NT>(s[rt][u + i / 4][i % 4], x);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) pf[rt][n][i] = x[n];
-        }
-      const uint8_t* from = stage + (4 * g + l16 / 4) * kRowBytes + 8 * (l16 % 4);
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-        struct { s16x4 a, b; } v{read_transposed(from + 32 * cb),
-                                 read_transposed(from + 16 * kRowBytes + 32 * cb)};
-        const bf16x8 vf = __builtin_bit_cast(bf16x8, v);
-#pragma unroll
-        for (int n = NT - 1; n >= 0; --n)
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-            o[rt][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][n], o[rt][cb], 0, 0, 0);
-      }
+        for (int rt = 0; rt < RT; ++rt)
+          o[rt][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][n], o[rt][cb], 0, 0, 0);
     }
   }
 
@@ -385,10 +421,9 @@ __global__ __launch_bounds__(kAttnWaves* kWave) void k_kv_attention(AttnArgs a) 
           v += *reinterpret_cast<f32x4v*>(join + (w * 16 + jr) * kJoinRow + ch);
         v *= inv;
         if (whole) {
-          T x[4] = {(T)v.x, (T)v.y, (T)v.z, (T)v.w};
           T* out = (T*)a.out + at * D + ch;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) out[e] = x[e];
+          for (int e = 0; e < 4; ++e) out[e] = (T)v[e];
         } else {
           *reinterpret_cast<f32x4v*>(a.part_o + (at * a.splits + split) * D + ch) = v;
         }
@@ -407,16 +442,12 @@ __global__ __launch_bounds__(kAttnWaves* kWave) void k_kv_attention(AttnArgs a) 
 template <int D>
 int32_t launch_kv_attention(const AttnArgs& a, int32_t dtype, int row_tiles, int grid, hipStream_t st);
 
-// The most row tiles (of 16) a workgroup of head size D and NT terms takes:
-// a wave holds their queries (D/8 registers a term) and sums (D/4) at once.
-constexpr int attn_most_row_tiles(int D, int NT) {
-  return NT == 1 ? (D <= 128 ? 4 : 2) : D <= 192 ? 2 : 1;
-}
+// The most row tiles (of 16) a workgroup of head size D and NT terms takes.
+constexpr int attn_most_row_tiles(int D, int NT) { return NT <= 2 && D <= 192 ? 2 : D <= 128 ? 2 : 1; }
 // Whole verify batches in one tile where they fit: every key is widened once
 // for all rows of the tile.
 inline int attn_row_tiles(int64_t rows, int D, int32_t dtype) {
-  const int most = attn_most_row_tiles(D, dtype == MOE_BF16 ? 1 : 2);
-  return rows <= 16 || most == 1 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
+  return rows <= 16 ? 1 : attn_most_row_tiles(D, dtype == MOE_BF16 ? 1 : dtype == MOE_F16 ? 2 : 3);
 }
 
 }  // namespace svr

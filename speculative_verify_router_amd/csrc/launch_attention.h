@@ -15,7 +15,6 @@ int32_t launch_kv_attention(const AttnArgs& a, int32_t dtype, int row_tiles, int
   if (dtype == MOE_BF16) {
     SVR_ATTN(1, 1, bf16)
     SVR_ATTN(2, 1, bf16)
-    SVR_ATTN(4, 1, bf16)
   } else if (dtype == MOE_F16) {
     SVR_ATTN(1, 2, _Float16)
     SVR_ATTN(2, 2, _Float16)
