@@ -6,11 +6,15 @@
 // the sums z = sum e^(x-m), t = sum e^(x-m)(x-m), rescaled when the maximum
 // grows, so that no exchange is needed before the end.
 //   Alternatives: a 64-bit key orders columns by value and then by lower
-// column, no two alike.  A wave keeps the keys above its threshold in a short
-// list in shared memory; when the list is full, it is cut to the top_k best
-// and the threshold follows.  Whole tiles below the threshold cost one
-// comparison of the lane's maximum, so that of 131072 random columns only a
-// few hundred are ever listed.
+// column, no two alike.  A wave holds its top_k best in order, one a lane.  A
+// wave's tiles come in ascending columns, so that with top_k held a later
+// column has to be larger in value: a tile whose lanes' maxima are not costs
+// one comparison.  Where at least top_k lanes have such a maximum (always in
+// the first tile), the top_k-th best of these is a threshold first, which all
+// but few columns fail.  One or two better keys are put in their places, each
+// pushing those below it a lane on (about 250 clocks each, one step waiting
+// for the other); more are gathered, up to 64, and placed together by how
+// many of each other and of the held ones are better (about 25 clocks each).
 //   Waves, then workgroups of a row are joined the same way; the last
 // workgroup to arrive at the row's counter joins them and returns the
 // counter to zero.
@@ -24,7 +28,6 @@ namespace {
 
 constexpr int kLpCols = 16;                // columns of a lane in a tile
 constexpr int kLpTile = kLpCols * kWave;   // columns of a wave's tile
-constexpr int kLpList = 256;               // keys a wave lists
 // Rows of several workgroups are rows of a small batch: kLpSpread workgroups
 // a call are wanted, so a row is cut only where there are at most half as many.
 constexpr int kLpSpread = 1024;
@@ -33,41 +36,34 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct LpArgs {
   const void* x;
-  int64_t stride, V;
-  int N, blocks, tiles_per_block, k, vec;
+  int64_t stride;
+  int V, blocks, tiles_per_block, k, vec;
   const int32_t* targets;
   float *logprobs, *entropy, *top_logprobs;
   int32_t* top_ids;
   unsigned* ctr;
-  uint64_t* part;  // [row][block][2 + k]: (m, z), (t, 0), keys
+  uint64_t* part;  // [row]: [block][2] of (m, z), (t, 0), then [block][k] keys
 };
 
 struct Sums {
   float m, z, t;
 };
-__device__ __forceinline__ Sums lp_join(const Sums& a, const Sums& b) {
-  Sums r;
-  r.m = fmaxf(a.m, b.m);
-  // A side at the joint maximum keeps its sums (also where both are -inf).
-  const float da = a.m == r.m ? 0.f : a.m - r.m, db = b.m == r.m ? 0.f : b.m - r.m;
-  const float fa = __builtin_amdgcn_exp2f(da * kLog2e), fb = __builtin_amdgcn_exp2f(db * kLog2e);
-  r.z = a.z * fa + b.z * fb;
-  r.t = (a.z == 0.f ? 0.f : (a.t + a.z * da) * fa) + (b.z == 0.f ? 0.f : (b.t + b.z * db) * fb);
-  // fa is 0 far below the maximum, where da may be -inf.
-  if (fa == 0.f) r.t = b.t;
-  if (fb == 0.f) r.t = a.t;
-  return r;
+// The sums of s relative to the maximum m >= s.m.
+__device__ __forceinline__ Sums lp_relative(const Sums& s, float m) {
+  if (s.m == m) return s;
+  const float d = s.m - m, f = __builtin_amdgcn_exp2f(d * kLog2e);
+  // f is 0 far below the maximum, where d may be -inf.
+  return Sums{m, s.z * f, f == 0.f ? 0.f : (s.t + s.z * d) * f};
 }
-__device__ __forceinline__ Sums lp_wave_join(Sums s) {
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    Sums b;
-    b.m = __shfl_xor(s.m, o, kWave);
-    b.z = __shfl_xor(s.z, o, kWave);
-    b.t = __shfl_xor(s.t, o, kWave);
-    s = lp_join(s, b);
-  }
-  return s;
+__device__ __forceinline__ Sums lp_join(const Sums& a, const Sums& b) {
+  const float m = fmaxf(a.m, b.m);
+  const Sums x = lp_relative(a, m), y = lp_relative(b, m);
+  return Sums{m, x.z + y.z, x.t + y.t};
+}
+// Over the wave, in every lane.
+__device__ __forceinline__ Sums lp_wave_join(const Sums& s) {
+  const Sums x = lp_relative(s, key_value(wave_max_u32(order_key(s.m))));
+  return Sums{x.m, wave_sum(x.z), wave_sum(x.t)};
 }
 
 // Columns by value, then by lower column; 0 is below every column.
@@ -75,61 +71,122 @@ __device__ __forceinline__ uint64_t lp_key(float v, uint32_t col) {
   return (uint64_t)order_key(v) << 32 | (uint32_t)~col;
 }
 
-// A wave's list of keys above a threshold.
-struct TopList {
-  uint64_t* buf;  // kLpList keys in shared memory
-  int n, k;
-  uint64_t thr;   // a key has to be above it to matter
+// A bound that at least k of the wave's words v reach (there are as many): the
+// upper 16 bits of the k-th largest, found two at a time, or less where
+// exactly k reach it.
+__device__ __forceinline__ uint32_t lp_bound(uint32_t v, int k) {
+  uint32_t low = 0;
+  for (int bit = 30; bit >= 16; bit -= 2) {
+    int n[3];
+#pragma unroll
+    for (int q = 0; q < 3; ++q) n[q] = __popcll(__ballot(v >= (low | (uint32_t)(q + 1) << bit)));
+    const int q = n[2] >= k ? 3 : n[1] >= k ? 2 : n[0] >= k ? 1 : 0;
+    low |= (uint32_t)q << bit;
+    if (q && n[q - 1] == k) break;
+  }
+  return low;
+}
 
-  __device__ __forceinline__ void fence() {
+// The k best keys that a wave has met, in order, one a lane (0: none).
+struct TopKeys {
+  uint64_t* buf;  // shared memory of the wave: 64 gathered keys, 64 placed ones
+  int k;
+  uint64_t thr;  // a key has to be above it to be held
+  uint64_t key = 0;
+  int held = 0, gathered = 0;
+
+  __device__ __forceinline__ static void fence() {
     // The wave's shared-memory operations complete in order; only the
     // compiler has to keep it.
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
-
-  // Cut to the k largest (n >= k): bisects the key of the k-th by its bits,
-  // until a bound has exactly k keys at or above it.
-  __device__ void cut() {
-    const int lane = threadIdx.x & (kWave - 1);
-    fence();
-    uint64_t v[kLpList / kWave];
-#pragma unroll
-    for (int j = 0; j < kLpList / kWave; ++j) v[j] = kWave * j + lane < n ? buf[kWave * j + lane] : 0;
-    uint64_t lowest = 0;
-    for (int bit = 63; bit >= 0; --bit) {
-      const uint64_t c = lowest | 1ull << bit;
-      int have = 0;
-#pragma unroll
-      for (int j = 0; j < kLpList / kWave; ++j) have += __popcll(__ballot(v[j] >= c));
-      if (have >= k) lowest = c;
-      if (have == k) break;
-    }
-    fence();
-    int at = 0;
-#pragma unroll
-    for (int j = 0; j < kLpList / kWave; ++j) {
-      const uint64_t keep = __ballot(v[j] >= lowest);
-      if (v[j] >= lowest) buf[at + __popcll(keep & ((1ull << lane) - 1))] = v[j];
-      at += __popcll(keep);
-    }
-    fence();
-    n = at;
-    thr = lowest - 1;
+  __device__ __forceinline__ static uint64_t of_lane(uint64_t x, int l) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), l) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, l);
+  }
+  __device__ __forceinline__ void follow() {
+    if (held < k) return;
+    const uint64_t last = of_lane(key, k - 1);
+    thr = last > thr ? last : thr;
   }
 
-  // Each lane offers one key (0: none).
-  __device__ __forceinline__ void offer(uint64_t key) {
-    uint64_t in = __ballot(key > thr);
-    if (!in) return;
-    if (n + __popcll(in) > kLpList) {
-      cut();
-      in = __ballot(key > thr);
-    }
+  // x: the same in every lane.
+  __device__ __forceinline__ void insert(uint64_t x) {
     const int lane = threadIdx.x & (kWave - 1);
-    if (key > thr) buf[n + __popcll(in & ((1ull << lane) - 1))] = key;
-    n += __popcll(in);
+    const int at = __popcll(__ballot(key > x));
+    if (at >= k) return;
+    constexpr int kDppWaveShr1 = 0x138;  // from the lane before
+    const uint64_t before = (uint64_t)dpp_u<kDppWaveShr1>(0u, (uint32_t)(key >> 32)) << 32 |
+                            dpp_u<kDppWaveShr1>(0u, (uint32_t)key);
+    key = lane < at ? key : lane == at ? x : before;
+    held = min(held + 1, k);
+    follow();
+  }
+
+  // The gathered keys take their places.
+  __device__ __forceinline__ void place() {
+    const int lane = threadIdx.x & (kWave - 1);
+    fence();
+    const uint64_t x = lane < gathered ? buf[lane] : 0;
+    int at = 0, down = 0;
+    // Eight at a time: lanes behind the last hold 0, which is above nothing.
+    for (int j = 0; j < gathered; j += 8)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t other = of_lane(x, j + i);
+        at += other > x;
+        down += other > key;
+      }
+    for (int j = 0; j < held; j += 8)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) at += of_lane(key, j + i) > x;
+    uint64_t* to = buf + kWave;
+    if (lane < gathered && at < k) to[at] = x;
+    if (lane < held && lane + down < k) to[lane + down] = key;
+    fence();
+    held = min(held + gathered, k);
+    gathered = 0;
+    key = lane < held ? to[lane] : 0;
+    follow();
+  }
+
+  // N keys a lane, key_of(e), of which pass(e) says which are to be looked at:
+  // each against the threshold that the one before left, or gathered.
+  template <int N, typename Pass, typename Key>
+  __device__ __forceinline__ void one_by_one(Pass pass, Key key_of) {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (uint64_t m = __ballot(pass(e))) {
+        const uint64_t x = key_of(e);
+        for (; m; m &= m - 1) insert(of_lane(x, __builtin_ctzll(m)));
+      }
+  }
+  template <int N, typename Pass, typename Key>
+  __device__ __forceinline__ void together(Pass pass, Key key_of) {
+    const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (uint64_t m = __ballot(pass(e))) {
+        const uint64_t x = key_of(e);
+        if (gathered + __popcll(m) > kWave) {
+          place();
+          m &= __ballot(x > thr);
+        }
+        if (m >> lane & 1) buf[gathered + __popcll(m & ((1ull << lane) - 1))] = x;
+        gathered += __popcll(m);
+      }
+    if (gathered) place();
+  }
+
+  // `best`: each lane's best value (as order_key; 0: none) of what is about
+  // to come.  Where k lanes or more are above the threshold, so is the k-th
+  // best of them.
+  __device__ __forceinline__ void raise(uint32_t best) {
+    if (__popcll(__ballot(best > (uint32_t)(thr >> 32))) < k) return;
+    const uint64_t low = (uint64_t)lp_bound(best, k) << 32;
+    if (low > thr) thr = low - 1;
   }
 };
 
@@ -142,12 +199,12 @@ struct Piece {
 // 16 columns of a lane from tile column `base`: pieces of 16 bytes, lane
 // after lane.  Columns from V on are -inf.
 template <typename T>
-__device__ __forceinline__ void lp_load(const T* row, int64_t base, int64_t V, bool vec, int lane,
+__device__ __forceinline__ void lp_load(const T* row, int base, int V, bool vec, int lane,
                                         T (&x)[kLpCols]) {
   constexpr int E = Piece<T>::kElems;
 #pragma unroll
   for (int p = 0; p < Piece<T>::kCount; ++p) {
-    const int64_t c = base + p * (E * kWave) + lane * E;
+    const int c = base + p * (E * kWave) + lane * E;
     if (vec && c + E <= V) {
       *reinterpret_cast<uint4*>(x + p * E) = *reinterpret_cast<const uint4*>(row + c);
     } else {
@@ -160,67 +217,95 @@ __device__ __forceinline__ void lp_load(const T* row, int64_t base, int64_t V, b
 template <typename T>
 __global__ __launch_bounds__(kBlock) void k_logprobs(LpArgs a) {
   constexpr int E = Piece<T>::kElems;
-  __shared__ uint64_t s_list[kWavesPerBlock][kLpList];
+  __shared__ uint64_t s_buf[kWavesPerBlock][2 * kWave];
   __shared__ Sums s_sums[kWavesPerBlock];
-  __shared__ int s_n[kWavesPerBlock], s_last;
+  __shared__ int s_last;
   const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x >> 6;
   const int row = blockIdx.x / a.blocks, blk = blockIdx.x % a.blocks;
   const T* x = (const T*)a.x + (int64_t)row * a.stride;
 
+  // Asked for now: the last workgroup of the row needs it at its end.
+  float target = 0.f;
+  bool has_target = false;
+  if (a.targets && threadIdx.x == 0) {
+    const int t = a.targets[row];
+    has_target = t >= 0 && t < a.V;
+    if (has_target) target = (float)x[t];
+  }
   Sums s{-INFINITY, 0.f, 0.f};
-  TopList top{s_list[wv], 0, a.k, a.k ? 0ull : ~0ull};
-  const int64_t c_begin = (int64_t)blk * a.tiles_per_block * kLpTile;
-  const int64_t c_end = min(c_begin + (int64_t)a.tiles_per_block * kLpTile, a.V);
-  for (int64_t base = c_begin + wv * kLpTile; base < c_end; base += kWavesPerBlock * kLpTile) {
-    T raw[kLpCols];
-    lp_load(x, base, a.V, a.vec, lane, raw);
+  TopKeys top{s_buf[wv], a.k, a.k ? 0ull : ~0ull};
+  // (Columns stay below 2^30 + a tile of each wave.)
+  const int c_begin = blk * a.tiles_per_block * kLpTile;
+  const int c_end = min(c_begin + a.tiles_per_block * kLpTile, a.V);
+  T raw[kLpCols];
+  int base = c_begin + wv * kLpTile;
+  if (base < c_end) lp_load(x, base, a.V, a.vec, lane, raw);
+  for (; base < c_end; base += kWavesPerBlock * kLpTile) {
     float v[kLpCols], mx = -INFINITY;
 #pragma unroll
     for (int e = 0; e < kLpCols; ++e) {
       v[e] = (float)raw[e];
       mx = fmaxf(mx, v[e]);
     }
+    const int next = base + kWavesPerBlock * kLpTile;
+    if (next < c_end) lp_load(x, next, a.V, a.vec, lane, raw);
     if (mx > s.m) s = lp_join(s, Sums{mx, 0.f, 0.f});
     const float m = s.m == -INFINITY ? 0.f : s.m;
+    // Four chains each, then one addition to the sums of all tiles.
+    float z[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < kLpCols; ++e) {
       const float d = v[e] - m;
       const float w = __builtin_amdgcn_exp2f(d * kLog2e);
-      s.z += w;
-      s.t = fmaf(w, fmaxf(d, -3e38f), s.t);  // a weight of zero times a finite number
+      z[e & 3] += w;
+      t[e & 3] = fmaf(w, fmaxf(d, -3e38f), t[e & 3]);  // a weight of zero times a finite number
     }
-    if (__ballot(order_key(mx) >= (uint32_t)(top.thr >> 32))) {
+    s.z += (z[0] + z[1]) + (z[2] + z[3]);
+    s.t += (t[0] + t[1]) + (t[2] + t[3]);
+    auto column = [&](int e) { return base + (e / E) * (E * kWave) + lane * E + e % E; };
+    const uint64_t in = __ballot(mx > key_value((uint32_t)(top.thr >> 32)));
+    if (top.thr == 0 || in) {
+      if (top.thr == 0 || __popcll(in) >= a.k) top.raise(column(0) < a.V ? order_key(mx) : 0u);
+      const float above = key_value((uint32_t)(top.thr >> 32));
+      if (top.held == a.k && above > -INFINITY && __popcll(in) <= 8) {
+        top.one_by_one<kLpCols>([&](int e) { return v[e] >= above; },
+                                [&](int e) { return lp_key(v[e], (uint32_t)column(e)); });
+      } else {  // -inf and NaN too, which no comparison of values tells apart
+        uint64_t key[kLpCols];
 #pragma unroll
-      for (int e = 0; e < kLpCols; ++e) {
-        const int64_t c = base + (e / E) * (E * kWave) + lane * E + e % E;
-        top.offer(c < a.V ? lp_key(v[e], (uint32_t)c) : 0ull);
+        for (int e = 0; e < kLpCols; ++e) key[e] = column(e) < a.V ? lp_key(v[e], (uint32_t)column(e)) : 0;
+        top.together<kLpCols>([&](int e) { return key[e] > top.thr; }, [&](int e) { return key[e]; });
       }
     }
   }
 
   s = lp_wave_join(s);
-  if (top.n > a.k) top.cut();
-  if (lane == 0) {
-    s_sums[wv] = s;
-    s_n[wv] = top.n;
-  }
+  if (lane == 0) s_sums[wv] = s;
+  top.fence();
+  s_buf[wv][lane] = top.key;
   __syncthreads();
-  const int stride = 2 + a.k;
+  uint64_t* sums = a.part + (int64_t)row * a.blocks * (2 + a.k);
+  uint64_t* keys = sums + 2 * a.blocks;
   if (wv == 0) {
-    for (int w = 1; w < kWavesPerBlock; ++w) {
-      s = lp_join(s, s_sums[w]);
-      top.offer(lane < s_n[w] ? s_list[w][lane] : 0ull);
-    }
-    if (top.n > a.k) top.cut();
-    top.fence();
-    if (a.blocks > 1) {
-      uint64_t* p = a.part + ((int64_t)row * a.blocks + blk) * stride;
-      if (lane == 0) {
-        store_shared<uint64_t>(p, (uint64_t)__builtin_bit_cast(uint32_t, s.z) << 32 |
-                                      __builtin_bit_cast(uint32_t, s.m));
-        store_shared<uint64_t>(p + 1, __builtin_bit_cast(uint32_t, s.t));
+    for (int w = 1; w < kWavesPerBlock; ++w) s = lp_join(s, s_sums[w]);
+    if (a.k) {
+      uint64_t v[kWavesPerBlock - 1];
+      uint32_t best = (uint32_t)(top.key >> 32);
+#pragma unroll
+      for (int w = 1; w < kWavesPerBlock; ++w) {
+        v[w - 1] = s_buf[w][lane];
+        best = max(best, (uint32_t)(v[w - 1] >> 32));
       }
-      if (lane < a.k) store_shared<uint64_t>(p + 2 + lane, lane < top.n ? top.buf[lane] : 0);
+      top.raise(best);
+      top.together<kWavesPerBlock - 1>([&](int e) { return v[e] > top.thr; }, [&](int e) { return v[e]; });
+    }
+    if (a.blocks > 1) {
+      if (lane == 0) {
+        store_shared<uint64_t>(sums + 2 * blk, (uint64_t)__builtin_bit_cast(uint32_t, s.z) << 32 |
+                                                   __builtin_bit_cast(uint32_t, s.m));
+        store_shared<uint64_t>(sums + 2 * blk + 1, __builtin_bit_cast(uint32_t, s.t));
+      }
+      if (lane < a.k) store_shared<uint64_t>(keys + blk * a.k + lane, top.key);
       wait_stores();
     }
   }
@@ -233,25 +318,31 @@ __global__ __launch_bounds__(kBlock) void k_logprobs(LpArgs a) {
   if (wv != 0) return;
 
   if (a.blocks > 1) {
+    const int n = a.blocks * a.k;
     s = Sums{-INFINITY, 0.f, 0.f};
-    top.n = 0;
-    top.thr = a.k ? 0ull : ~0ull;
-    const uint64_t* p = a.part + (int64_t)row * a.blocks * stride;
+    top = TopKeys{s_buf[0], a.k, a.k ? 0ull : ~0ull};
     for (int b = lane; b < a.blocks; b += kWave) {
-      const uint64_t mz = load_shared(p + (int64_t)b * stride);
-      const uint64_t t = load_shared(p + (int64_t)b * stride + 1);
+      const uint64_t mz = load_shared(sums + 2 * b), t = load_shared(sums + 2 * b + 1);
       s = lp_join(s, Sums{__builtin_bit_cast(float, (uint32_t)mz),
                           __builtin_bit_cast(float, (uint32_t)(mz >> 32)),
                           __builtin_bit_cast(float, (uint32_t)t)});
     }
-    s = lp_wave_join(s);
-    const int keys = a.blocks * a.k;
-    for (int i = 0; i < keys; i += kWave) {
-      const int j = i + lane;
-      top.offer(j < keys ? load_shared(p + (int64_t)(j / a.k) * stride + 2 + j % a.k) : 0ull);
+    // The blocks' keys, some a lane at a time.
+    constexpr int kAtOnce = 16;
+    for (int i = 0; i < n; i += kAtOnce * kWave) {
+      uint64_t v[kAtOnce];
+      uint32_t best = 0;
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) {
+        const int j = i + e * kWave + lane;
+        v[e] = j < n ? load_shared(keys + j) : 0;
+      }
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) best = max(best, (uint32_t)(v[e] >> 32));
+      top.raise(best);
+      top.together<kAtOnce>([&](int e) { return v[e] > top.thr; }, [&](int e) { return v[e]; });
     }
-    if (top.n > a.k) top.cut();
-    top.fence();
+    s = lp_wave_join(s);
     if (lane == 0) __hip_atomic_store(a.ctr + row, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 
@@ -259,22 +350,17 @@ __global__ __launch_bounds__(kBlock) void k_logprobs(LpArgs a) {
   const float lz = __builtin_amdgcn_logf(s.z) * kLn2;
   if (lane == 0) {
     if (a.logprobs) {
-      const int t = a.targets[row];
       float lp = NAN;
-      if (t >= 0 && t < a.V) lp = none ? -INFINITY : ((float)x[t] - s.m) - lz;
+      if (has_target) lp = none ? -INFINITY : (target - s.m) - lz;
       a.logprobs[row] = lp;
     }
     if (a.entropy) a.entropy[row] = none ? 0.f : lz - s.t / s.z;
   }
   if (lane < a.k) {
-    const uint64_t key = top.buf[lane];
-    int rank = 0;
-    for (int j = 0; j < a.k; ++j) rank += top.buf[j] > key;
-    const uint32_t c = ~(uint32_t)key;
-    const int64_t at = (int64_t)row * a.k + rank;
-    if (a.top_ids) a.top_ids[at] = (int32_t)c;
+    const int64_t at = (int64_t)row * a.k + lane;
+    if (a.top_ids) a.top_ids[at] = (int32_t)~(uint32_t)top.key;
     if (a.top_logprobs)
-      a.top_logprobs[at] = none ? -INFINITY : ((float)x[c] - s.m) - lz;
+      a.top_logprobs[at] = none ? -INFINITY : (key_value((uint32_t)(top.key >> 32)) - s.m) - lz;
   }
 }
 
@@ -349,8 +435,7 @@ int32_t moe_logprobs(const void* logits, int32_t dtype, int32_t n_rows, int64_t 
   LpArgs a{};
   a.x = logits;
   a.stride = row_stride;
-  a.V = vocab;
-  a.N = n_rows;
+  a.V = (int)vocab;
   a.blocks = p.blocks;
   a.tiles_per_block = p.tiles_per_block;
   a.k = top_k;
