@@ -100,6 +100,27 @@ __device__ __forceinline__ int kv_sequence_of(const KvArgs& a, int i) {
   return lo < a.n_seqs ? lo : -1;
 }
 
+// The sequence of row i and the place of its token there; b < 0: of none.
+struct KvToken {
+  int b;
+  int64_t place;
+};
+__device__ __forceinline__ KvToken kv_token(const KvArgs& a, int i) {
+  KvToken t{-1, 0};
+  if (a.n_seqs < kWave) {  // every offset and length at once: one wait instead of two
+    const int lane = threadIdx.x & (kWave - 1);
+    const int off = lane <= a.n_seqs ? a.offs[lane] : 0, len = lane < a.n_seqs ? a.lens[lane] : 0;
+    t.b = __popcll(__ballot(lane <= a.n_seqs && off <= i)) - 1;
+    if (t.b >= a.n_seqs) t.b = -1;
+    if (t.b >= 0)
+      t.place = (int64_t)__builtin_amdgcn_readlane(len, t.b) - __builtin_amdgcn_readlane(off, t.b + 1) + i;
+    return t;
+  }
+  t.b = kv_sequence_of(a, i);
+  if (t.b >= 0) t.place = (int64_t)a.lens[t.b] - a.offs[t.b + 1] + i;
+  return t;
+}
+
 // Byte offset in the cache of key/value head h of the page that holds place
 // p of sequence b, or -1 where there is none.
 __device__ __forceinline__ int64_t kv_page_base(const KvArgs& a, int b, int64_t p, int h) {
@@ -127,24 +148,6 @@ __device__ __forceinline__ void load8(const T* p, bool vec, float (&x)[8]) {
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = (float)raw[i];
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(T* p, bool vec, const float (&x)[8]) {
-  T raw[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) raw[i] = (T)x[i];
-  if (vec) {
-    if constexpr (sizeof(T) == 4) {
-      reinterpret_cast<uint4*>(p)[0] = *reinterpret_cast<uint4*>(raw);
-      reinterpret_cast<uint4*>(p)[1] = *reinterpret_cast<uint4*>(raw + 4);
-    } else {
-      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(raw);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = raw[i];
-  }
 }
 
 }  // namespace svr

@@ -3,17 +3,27 @@
 //
 // A unit is one head vector: a query head, or a key head with its value head
 // (together, so that a NaN or infinity in either marks the token).  A group
-// of LG lanes takes a unit, eight channels a lane: one 16-byte load of a
-// 16-bit type, a 4-bit block of 32 channels is four lanes, and a lane's
-// codes are one dword.  The pair of a rotated channel is in the same lane
-// (neighbours) or a fixed number of lanes away.
+// of LG lanes takes a unit, eight channels a lane: 16 bytes of a 16-bit type,
+// a 4-bit block of 32 channels is four lanes, and a lane's codes are one
+// dword.  The pair of a rotated channel is in the same lane (neighbours), or
+// is read from memory once more, which the cache answers.
 //
-// The pass is bound by its bytes: each of q, k, v is read once, q_out and
-// the codes written once.  A workgroup serves one token, so that the angles
-// (64-bit: at place 60000 a 32-bit angle is off by 2^-9 of a turn's radian)
-// are taken once for all heads; queries are normed and rotated in 32 bits,
-// keys in 64, because a code is a whole number and a key next to a rounding
-// border must fall on its own side whatever the order of the sum.
+// The pass is to be bound by its bytes: each of q, k, v is read once, q_out
+// and the codes written once.  A workgroup serves one token: the angles
+// (64-bit: at place 60000 a 32-bit angle is off by 2^-9) and the norms'
+// weights go into tables of factors in shared memory, once for all its heads,
+// which leaves a query's channel two products, a sum and its share of the
+// norm; the first heads are asked for before anything else.  Queries are
+// normed and rotated in 32 bits, keys in 64, because a code is a whole number
+// and a key next to a rounding border must fall on its own side whatever the
+// order of the sum.
+//
+// Measured with 64 query and 4 key/value heads of 192 channels: 31 us for
+// 1878 tokens in bf16 (98 MB, 3.2 TB/s), 15.5 us for 512 in float (52 MB,
+// 3.4 TB/s), 5 us for 4, of which the reads one after another (offsets, page,
+// heads) are most.  Angles taken anew for every head: 91 and 34 us; factors
+// in registers and one step ahead, whose copies waited for the stores: 50 and
+// 26.  Four steps at once leave three waves a SIMD: 33 and 20.
 #include "kv.h"
 
 namespace svr {
@@ -28,177 +38,289 @@ struct AppendArgs {
   uint8_t* cache;
   void* q_out;
   float eps;
-  int rotary, interleaved, units_per_block, vec;
+  int rotary, interleaved;
+  int parts, steps, steps_per_part;  // workgroups of a token; waves' steps
 };
 
 template <int D>
 struct Group {
   static constexpr int kLanes = D <= 64 ? 8 : D <= 128 ? 16 : 32;  // lanes of a unit
-  static constexpr int kUnits = kBlock / kLanes;                   // units of a pass
 };
 
-template <typename F, int LG>
-__device__ __forceinline__ F group_sum(F v) {
+// Sum over the LG lanes of a unit, in each of them.
+template <int LG>
+__device__ __forceinline__ float group_sum(float v) {
+  v += dpp<0xB1>(0.f, v);   // lanes xor 1
+  v += dpp<0x4E>(0.f, v);   // xor 2
+  v += dpp<0x141>(0.f, v);  // the other four of eight
+  if (LG >= 16) v += dpp<0x140>(0.f, v);  // the other eight of sixteen
+  // The other sixteen of thirty-two.
+  if (LG >= 32) v += __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(__builtin_bit_cast(int, v), 0x401F));
+  return v;
+}
+template <int LG>
+__device__ __forceinline__ double group_sum(double v) {
 #pragma unroll
   for (int m = 1; m < LG; m <<= 1) v += __shfl_xor(v, m, kWave);
   return v;
 }
 
-// x[8] (channels c0..c0+7 of one head) normed and rotated in F.
-template <typename F, int LG>
-__device__ __forceinline__ void norm_rotate(const AppendArgs& a, int D, int sub, bool live,
-                                            const float* w, const double2* cs, F (&x)[8]) {
-  const int c0 = 8 * sub;
-  if (w) {
-    F ss = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-    ss = group_sum<F, LG>(ss);
-    const F r = (F)1 / sqrt(ss / (F)D + (F)a.eps);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (F)(live ? w[c0 + i] : 0.f);
+// Norm and rotation of a channel x: r (x A + y B), r the norm's factor, y the
+// channel that x is turned with, A = w cos and B = -+ w' sin with the norm
+// weights w of x and w' of y.  A and B are the same for every head of a token,
+// so its workgroup puts them into shared memory first.
+template <int D>
+struct Tables {
+  double ka[D], kb[D];
+  float qa[D], qb[D];
+};
+// The pair j of a token at pos; the channels that are not turned have A = w
+// and B = 0.
+template <int D>
+__device__ __forceinline__ void fill_tables(Tables<D>& t, const AppendArgs& a, int j, double pos, bool keys,
+                                            bool queries) {
+  const int half = a.rotary / 2;
+  const bool turned = j < half;
+  const int c1 = turned && !a.interleaved ? j : 2 * j, c2 = turned && !a.interleaved ? j + half : 2 * j + 1;
+  const bool kn = keys && a.k_norm, qn = queries && a.q_norm;
+  const float k1 = kn ? a.k_norm[c1] : 1.f, k2 = kn ? a.k_norm[c2] : 1.f;
+  const float q1 = qn ? a.q_norm[c1] : 1.f, q2 = qn ? a.q_norm[c2] : 1.f;
+  double sn = 0.0, cn = 1.0;
+  if (turned) sincos(pos * (double)a.inv_freq[j], &sn, &cn);
+  if (keys) {
+    t.ka[c1] = k1 * cn;
+    t.ka[c2] = k2 * cn;
+    t.kb[c1] = -(k2 * sn);
+    t.kb[c2] = k1 * sn;
   }
-  if (a.rotary == 0) return;
-  if (a.interleaved) {
-    if (c0 < a.rotary) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const double2 t = cs[c0 / 2 + i];
-        const F p = x[2 * i], n = x[2 * i + 1];
-        x[2 * i] = p * (F)t.x - n * (F)t.y;
-        x[2 * i + 1] = n * (F)t.x + p * (F)t.y;
-      }
-    }
-    return;
-  }
-  const int half = a.rotary / 2;  // a multiple of 8: the pair is half / 8 lanes away
-  const bool first = c0 < half;
-  const int other = (int)(threadIdx.x & (kWave - 1)) + (first ? half / 8 : -(half / 8));
-  F y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], other & (kWave - 1), kWave);
-  if (c0 < a.rotary) {
-    const int j = first ? c0 : c0 - half;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const double2 t = cs[j + i];
-      x[i] = first ? x[i] * (F)t.x - y[i] * (F)t.y : x[i] * (F)t.x + y[i] * (F)t.y;
-    }
+  if (queries) {
+    t.qa[c1] = (float)(q1 * cn);
+    t.qa[c2] = (float)(q2 * cn);
+    t.qb[c1] = (float)-(q2 * sn);
+    t.qb[c2] = (float)(q1 * sn);
   }
 }
+__device__ __forceinline__ float norm_factor(float mean) {
+  // The instruction (1 ulp) takes subnormal numbers for zeros.
+  const bool tiny = mean < 1e-30f;
+  const float r = __builtin_amdgcn_rsqf(tiny ? mean * 0x1p100f : mean);
+  return tiny ? r * 0x1p50f : r;
+}
 
+// The codes of eight floats over 2^e, by the conversion instruction: the
+// nearest code, the even one between two, at most 6 in size.
+__device__ __forceinline__ uint32_t codes8(const float (&x)[8], int e) {
+  const float scale = __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], scale, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], scale, 3);
+}
+// The largest m of the four lanes of a block.
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
+  m = max(m, dpp_u<0xB1>(0u, m));
+  return max(m, dpp_u<0x4E>(0u, m));
+}
 // Least E in [-126, 125] with amax <= 7 * 2^E (0 for amax == 0): with
 // amax = f * 2^x, 1 <= f < 2, that is x - 2 for f <= 7/4 and x - 1 above.
-__device__ __forceinline__ int block_exponent(double amax) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, amax);
-  const int x = (int)(b >> 52) - 1023;
-  const int e = x - 2 + ((b & 0xFFFFFFFFFFFFFull) > 0xC000000000000ull ? 1 : 0);
-  return amax == 0 ? 0 : min(max(e, -126), 125);
-}
-__device__ __forceinline__ int block_exponent(float amax) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, amax);
-  const int x = (int)(b >> 23) - 127;
-  const int e = x - 2 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return amax == 0 ? 0 : min(max(e, -126), 125);
-}
-__device__ __forceinline__ double pow2(double, int e) {
-  return __builtin_bit_cast(double, (uint64_t)(1023 + e) << 52);
-}
-__device__ __forceinline__ float pow2(float, int e) {
-  return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
+__device__ __forceinline__ int block_exponent(bool zero, int x, bool above) {
+  return zero ? 0 : min(max(x - 2 + (above ? 1 : 0), -126), 125);
 }
 
-// Eight values as one dword of codes; the scale byte of their block of 32.
-// The thresholds are the midpoints of the code values, each open on the side
-// of the even code, so the result is exact for whatever x is.
-template <typename F>
-__device__ __forceinline__ uint32_t quantise8(const F (&x)[8], uint32_t& scale) {
-  F amax = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmax(amax, fabs(x[i]));
-  amax = fmax(amax, __shfl_xor(amax, 1, kWave));
-  amax = fmax(amax, __shfl_xor(amax, 2, kWave));
-  const int e = block_exponent(amax);
-  const F inv = pow2((F)0, -e);
-  scale = (uint32_t)(e + 127);
-  uint32_t word = 0;
+// Eight values as one dword of codes, and the scale byte of their block of 32.
+__device__ __forceinline__ uint32_t quantise8(const float (&v)[8], uint32_t& scale) {
+  uint32_t m = 0;
+  float x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const F t = fabs(x[i]) * inv;
-    uint32_t c = (t > (F)0.25) + (t >= (F)0.75) + (t > (F)1.25) + (t >= (F)1.75) +
-                 (t > (F)2.5) + (t >= (F)3.5) + (t > (F)5.0);
-    c |= x[i] < 0 ? 8u : 0u;
-    word |= c << (4 * i);
+    x[i] = v[i] + 0.f;  // no -0, whose code has no sign
+    m = max(m, __builtin_bit_cast(uint32_t, x[i]) & 0x7FFFFFFFu);
   }
-  return word;
+  m = block_max(m);
+  const int e = block_exponent(m == 0, (int)(m >> 23) - 127, (m & 0x7FFFFFu) > 0x600000u);
+  scale = (uint32_t)(e + 127);
+  return codes8(x, e);
+}
+// The same of 64-bit values, exactly: of a value's lower 32 bits it matters
+// only whether there are any (the borders have at most three bits), so that a
+// float of value / 2^e with that in its last bit falls on the same side of
+// every border.
+__device__ __forceinline__ uint32_t quantise8(const double (&v)[8], uint32_t& scale) {
+  uint32_t h[8], m = 0;  // the upper 31 bits without the sign, then "and more"
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v[i]);
+    h[i] = (uint32_t)(b >> 32) << 1 | ((uint32_t)b ? 1u : 0u);
+    m = max(m, h[i]);
+  }
+  m = block_max(m);
+  const int e = block_exponent(m == 0, (int)(m >> 21) - 1023, (m & 0x1FFFFFu) > 0x180000u);
+  scale = (uint32_t)(e + 127);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // 896 + e: from the exponent's offset of 1023 to 127, over 2^e.
+    const int r = min(max((int)(h[i] >> 1) - ((896 + e) << 20), 0), (255 << 20) - 1);
+    const uint32_t sign = h[i] ? (uint32_t)(__builtin_bit_cast(uint64_t, v[i]) >> 32) & 0x80000000u : 0u;
+    x[i] = __builtin_bit_cast(float, (uint32_t)r << 3 | (h[i] & 1u) | sign);
+  }
+  return codes8(x, 0);
 }
 
+// Eight elements as they lie in memory, aligned as one element is: the memory
+// path takes wide accesses at any address.
+template <typename T>
+struct Raw8 {
+  static constexpr int kWords = 2 * sizeof(T);
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void load(const T* p) { __builtin_memcpy(w, p, sizeof(w)); }
+  __device__ __forceinline__ void store(T* p) const { __builtin_memcpy(p, w, sizeof(w)); }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, w[i]);
+    else return (float)__builtin_bit_cast(T, (uint16_t)(i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu));
+  }
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4) w[i] = __builtin_bit_cast(uint32_t, x[i]);
+      else
+        w[i] = (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * i]) |
+               (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * i + 1]) << 16;
+    }
+  }
+  // The neighbours swapped, where mask is set; 0 elsewhere.
+  __device__ __forceinline__ void swap_of(const Raw8& x, uint32_t mask) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      w[i] = (sizeof(T) == 4 ? x.w[i ^ 1] : x.w[i] << 16 | x.w[i] >> 16) & mask;
+  }
+};
+
+// A wave takes 64 / LG units at a time (a step): first the token's key/value
+// heads, then its queries, kAhead steps at once; the workgroups of a token
+// share its steps.
 template <int D, typename T>
 __global__ __launch_bounds__(kBlock) void k_kv_append(AppendArgs a) {
-  constexpr int LG = Group<D>::kLanes;
-  __shared__ double2 s_cs[D / 2];
-  const int blocks = (a.kv.Hq * (a.q ? 1 : 0) + a.kv.Hk + a.units_per_block - 1) / a.units_per_block;
-  const int i = blockIdx.x / blocks, part = blockIdx.x % blocks;
-  const int b = kv_sequence_of(a.kv, i);
-  if (b < 0) return;
-  const int64_t place = (int64_t)a.kv.lens[b] - a.kv.offs[b + 1] + i;
-  if (a.rotary) {
-    const double pos = a.positions ? (double)a.positions[i] : (double)place;
-    for (int j = threadIdx.x; j < a.rotary / 2; j += kBlock) {
-      double sn, cn;
-      sincos(pos * (double)a.inv_freq[j], &sn, &cn);
-      s_cs[j] = make_double2(cn, sn);
+  constexpr int LG = Group<D>::kLanes, kStep = kWave / LG, kAhead = 4 / sizeof(T);
+  __shared__ __align__(16) Tables<D> tab;
+  const int i = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+  const int lane = threadIdx.x & (kWave - 1), sub = lane % LG, mine = lane / LG;
+  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int c0 = 8 * sub, half = a.rotary / 2;
+  const bool live = c0 < D, turned = c0 < a.rotary, apart = turned && !a.interleaved;
+  // Where the channels that these are turned with lie from them.
+  const int turn = c0 < half ? half : -half;
+  const uint32_t near = turned && a.interleaved ? ~0u : 0u;
+  const int k_steps = (a.kv.Hk + kStep - 1) / kStep;
+  const int s_begin = part * a.steps_per_part;
+  const int s_end = min(s_begin + a.steps_per_part, a.steps), k_end = min(k_steps, s_end);
+  int s = s_begin + wv;
+
+  Raw8<T> x[kAhead]{}, y[kAhead]{}, v8{};
+  auto load = [&](const T* row, int slot) {
+    x[slot].load(row + c0);
+    if (apart) y[slot].load(row + c0 + turn);
+  };
+  auto load_keys = [&](int s) {
+    const int u = s * kStep + mine;
+    if (!live || u >= a.kv.Hk) return;
+    load((const T*)a.k + i * a.ks + u * D, 0);
+    v8.load((const T*)a.v + i * a.vs + u * D + c0);
+  };
+  auto load_queries = [&](int s) {
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      const int at = s + n * kWavesPerBlock, u = (at - k_steps) * kStep + mine;
+      if (at < s_end && live && u < a.kv.Hq) load((const T*)a.q + i * a.qs + u * D, n);
     }
-    __syncthreads();
+  };
+  // Asked for before anything else is known.
+  if (s < k_end) load_keys(s);
+  else load_queries(s);
+
+  const KvToken tok = kv_token(a.kv, i);
+  if (tok.b < 0) return;
+  if (threadIdx.x < D / 2)
+    fill_tables(tab, a, threadIdx.x, a.positions ? (double)a.positions[i] : (double)tok.place,
+                s_begin < k_steps, s_end > k_steps);
+  __syncthreads();
+
+  while (s < k_end) {
+    const int u = s * kStep + mine;
+    const bool on = live && u < a.kv.Hk;
+    double k[8], r = 1.0;
+    float v[8];
+    if (a.interleaved) y[0].swap_of(x[0], near);
+    if (a.k_norm) {
+      double ss = 0.0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += (double)x[0][e] * (double)x[0][e];
+      r = 1.0 / sqrt(group_sum<LG>(ss) / D + (double)a.eps);
+    }
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = live ? c0 + e : e;
+      k[e] = r * ((double)x[0][e] * tab.ka[c] + (double)y[0][e] * tab.kb[c]);
+      v[e] = v8[e];
+      bad |= !(fabs(k[e]) < INFINITY) || !(fabsf(v[e]) < INFINITY);
+    }
+    s += kWavesPerBlock;
+    if (s < k_end) load_keys(s);
+    else load_queries(s);
+    const uint64_t group = (1ull << LG) - 1;
+    const bool nan_token = (__ballot(bad && on) >> (lane & ~(LG - 1))) & group;
+    uint32_t ke, ve;
+    uint32_t kc = quantise8(k, ke), vc = quantise8(v, ve);
+    if (nan_token) {
+      kc = vc = 0;
+      ke = 255;
+      ve = 127;
+    }
+    const int64_t base = on ? kv_page_base(a.kv, tok.b, tok.place, u) : -1;
+    if (base >= 0) {
+      const int P = 1 << a.kv.page_shift, o = (int)(tok.place & (P - 1));
+      uint8_t* c = a.cache + base;
+      *reinterpret_cast<uint32_t*>(c + o * (D / 2) + 4 * sub) = kc;
+      *reinterpret_cast<uint32_t*>(c + (P + o) * (D / 2) + 4 * sub) = vc;
+      if (sub % 4 == 0) {
+        c[P * D + o * (D / 32) + sub / 4] = (uint8_t)ke;
+        c[P * D + (P + o) * (D / 32) + sub / 4] = (uint8_t)ve;
+      }
+    }
   }
-  const int lane = threadIdx.x & (kWave - 1);
-  const int sub = lane % LG;
-  const bool live = 8 * sub < D;
-  const int units = a.kv.Hk + (a.q ? a.kv.Hq : 0);
-  const int u_end = min((part + 1) * a.units_per_block, units);
-  // Whole passes, so that every lane takes part in the exchanges.
-  for (int u0 = part * a.units_per_block; u0 < u_end; u0 += Group<D>::kUnits) {
-    const int u = u0 + (int)threadIdx.x / LG;
-    const bool on = live && u < u_end;
-    if (u < a.kv.Hk) {
-      float xf[8] = {}, v[8] = {};
-      if (on) {
-        load8((const T*)a.k + i * a.ks + (int64_t)u * D + 8 * sub, a.vec & 2, xf);
-        load8((const T*)a.v + i * a.vs + (int64_t)u * D + 8 * sub, a.vec & 4, v);
-      }
-      double x[8];
-      bool bad = false;
+  if (s >= s_end) return;
+
+  float qa[8], qb[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = (double)xf[e];
-      norm_rotate<double, LG>(a, D, sub, live, a.k_norm, s_cs, x);
+  for (int e = 0; e < 8; ++e) {
+    qa[e] = tab.qa[live ? c0 + e : e];
+    qb[e] = tab.qb[live ? c0 + e : e];
+  }
+  T* out = (T*)a.q_out + (int64_t)i * a.kv.Hq * D + c0;
+  for (; s < s_end; s += kAhead * kWavesPerBlock) {
+    Raw8<T> z[kAhead];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) bad |= !(fabs(x[e]) < INFINITY) || !(fabsf(v[e]) < INFINITY);
-      const uint64_t group = LG == 64 ? ~0ull : (1ull << LG) - 1;
-      const bool nan_token = (__ballot(bad) >> (lane & ~(LG - 1))) & group;
-      uint32_t ke, ve;
-      uint32_t kw = quantise8(x, ke), vw = quantise8(v, ve);
-      if (nan_token) {
-        kw = vw = 0;
-        ke = 255;
-        ve = 127;
+    for (int n = 0; n < kAhead; ++n) {
+      if (a.interleaved) y[n].swap_of(x[n], near);
+      float t[8], r = 1.f;
+      if (a.q_norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[n][e], x[n][e], ss);
+        r = norm_factor(group_sum<LG>(ss) * (1.f / D) + a.eps);
       }
-      const int64_t base = on ? kv_page_base(a.kv, b, place, u) : -1;
-      if (base >= 0) {
-        const int P = 1 << a.kv.page_shift, o = (int)(place & (P - 1));
-        uint8_t* c = a.cache + base;
-        *reinterpret_cast<uint32_t*>(c + o * (D / 2) + 4 * sub) = kw;
-        *reinterpret_cast<uint32_t*>(c + (P + o) * (D / 2) + 4 * sub) = vw;
-        if (sub % 4 == 0) {
-          c[P * D + o * (D / 32) + sub / 4] = (uint8_t)ke;
-          c[P * D + (P + o) * (D / 32) + sub / 4] = (uint8_t)ve;
-        }
-      }
-    } else {
-      const int h = u - a.kv.Hk;
-      float x[8] = {};
-      if (on) load8((const T*)a.q + i * a.qs + (int64_t)h * D + 8 * sub, a.vec & 1, x);
-      norm_rotate<float, LG>(a, D, sub, live, a.q_norm, s_cs, x);
-      if (on) store8((T*)a.q_out + ((int64_t)i * a.kv.Hq + h) * D + 8 * sub, a.vec & 8, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = r * fmaf(x[n][e], qa[e], y[n][e] * qb[e]);
+      z[n].set(t);
+    }
+    load_queries(s + kAhead * kWavesPerBlock);
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      const int at = s + n * kWavesPerBlock, u = (at - k_steps) * kStep + mine;
+      if (at < s_end && live && u < a.kv.Hq) z[n].store(out + u * D);
     }
   }
 }
@@ -215,12 +337,11 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(ReadArgs a) {
   const int blocks = (per_row + kBlock - 1) / kBlock;
   const int i = blockIdx.x / blocks;
   const int w = (blockIdx.x % blocks) * kBlock + threadIdx.x;
-  const int b = kv_sequence_of(a.kv, i);
-  if (b < 0 || w >= per_row) return;
-  const int64_t place = (int64_t)a.kv.lens[b] - a.kv.offs[b + 1] + i;
+  const KvToken tok = kv_token(a.kv, i);
+  if (tok.b < 0 || w >= per_row) return;
   const int h = w / (D / 8), sub = w % (D / 8);
-  const int64_t base = kv_page_base(a.kv, b, place, h);
-  const int P = 1 << a.kv.page_shift, o = (int)(place & (P - 1));
+  const int64_t base = kv_page_base(a.kv, tok.b, tok.place, h);
+  const int P = 1 << a.kv.page_shift, o = (int)(tok.place & (P - 1));
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
     float* out = side ? a.v_out : a.k_out;
@@ -240,7 +361,9 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(ReadArgs a) {
         x[n] = ((word >> (4 * n)) & 8 ? -mag : mag) * s;
       }
     }
-    store8(out + ((int64_t)i * a.kv.Hk + h) * D + 8 * sub, (uintptr_t)out % 16 == 0, x);
+    Raw8<float> raw;
+    raw.set(x);
+    raw.store(out + ((int64_t)i * a.kv.Hk + h) * D + 8 * sub);
   }
 }
 
@@ -309,15 +432,15 @@ int32_t moe_kv_append(const moe_kv_desc* desc, const moe_kv_batch* batch, int32_
   a.eps = desc->norm_eps;
   a.rotary = desc->rotary_dims;
   a.interleaved = desc->flags & MOE_KV_ROTARY_INTERLEAVED;
-  auto aligned = [&](const void* p, int64_t stride) {
-    return (uintptr_t)p % 16 == 0 && stride * es % 16 == 0;
-  };
-  a.vec = (aligned(q, q_stride) ? 1 : 0) | (aligned(k, k_stride) ? 2 : 0) |
-          (aligned(v, v_stride) ? 4 : 0) | (aligned(q_out, 0) ? 8 : 0);
-  const int units = desc->n_kv_heads + (q ? desc->n_heads : 0);
-  const int pass = kBlock / (D <= 64 ? 8 : D <= 128 ? 16 : 32);
-  a.units_per_block = pass;
-  const int grid = batch->n_tokens * ((units + a.units_per_block - 1) / a.units_per_block);
+  // One workgroup a token where there are tokens enough to fill the chip (five
+  // workgroups a CU), several, down to a step a wave, where there are not.
+  const int step = kWave / (D <= 64 ? 8 : D <= 128 ? 16 : 32);
+  a.steps = (desc->n_kv_heads + step - 1) / step + (q ? (desc->n_heads + step - 1) / step : 0);
+  const int want = (1280 + batch->n_tokens - 1) / batch->n_tokens;
+  const int rounds = (a.steps + want * kWavesPerBlock - 1) / (want * kWavesPerBlock);
+  a.steps_per_part = rounds * kWavesPerBlock;
+  a.parts = (a.steps + a.steps_per_part - 1) / a.steps_per_part;
+  const int grid = batch->n_tokens * a.parts;
   hipStream_t st = (hipStream_t)hip_stream;
   (void)hipGetLastError();
   switch (D) {
