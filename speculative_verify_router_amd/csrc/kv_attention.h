@@ -26,6 +26,20 @@ namespace svr {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 
+// Whole division by a number that the host knows: n / d for n < 2^31 is
+// n m >> s with s = 31 + ceil(log2 d), m = floor(2^s / d) + 1 (32 bits): m d
+// passes 2^s by at most 2^(s - 31), which is too little to count below 2^31.
+struct Divider {
+  uint32_t m, s;
+  int d;
+  __device__ __forceinline__ int of(int n) const { return (int)((uint64_t)(uint32_t)n * m >> s); }
+};
+inline Divider make_divider(int d) {
+  uint32_t s = 31;
+  while ((int64_t)1 << (s - 31) < d) ++s;
+  return Divider{(uint32_t)(((uint64_t)1 << s) / (uint64_t)d + 1), s, d};
+}
+
 struct AttnArgs {
   KvArgs kv;
   const void* q;
@@ -36,26 +50,28 @@ struct AttnArgs {
   float* part_o;   // [row][head][split][D], sums not yet divided
   float2* part_ml;  // [row][head][split]: maximum (base 2), sum
   float c;         // scale * log2(e)
-  int G, tiles, splits, min_tiles, vec;
+  int min_tiles;
+  Divider G, tiles, splits, heads;  // query heads a key/value head; of a sequence's work; Hk
 };
 
 constexpr int kAttnWaves = 4;
 constexpr int kAttnTile = 32;  // tokens of a wave's step
 
 // The tokens [beg, end) that rows of places [first, last] see, in tiles from
-// tb on, `per` of them a split, `used` splits (at least one).
+// tb on, `per` of them a split.
 struct KvRange {
-  int beg, end, tb, ntile, per, used;
+  int beg, end, tb, ntile, per;
+  __device__ __forceinline__ bool uses(int split) const { return split == 0 || split * per < ntile; }
+  __device__ __forceinline__ bool whole() const { return ntile <= per; }  // one split
 };
 __device__ __forceinline__ KvRange kv_range(const KvArgs& kv, int len, int first, int last,
-                                            int splits, int min_tiles) {
+                                            const Divider& splits, int min_tiles) {
   KvRange r;
   r.end = min(min(len, kv.pages_per_seq << kv.page_shift), last + 1);
   r.beg = kv.window ? max(0, first - kv.window + 1) : 0;
   r.tb = r.beg & ~(kAttnTile - 1);
   r.ntile = r.end > r.beg ? (r.end - r.tb + kAttnTile - 1) / kAttnTile : 0;
-  r.per = max(min_tiles, (r.ntile + splits - 1) / splits);
-  r.used = max(1, (r.ntile + r.per - 1) / r.per);
+  r.per = max(min_tiles, splits.of(r.ntile + splits.d - 1));
   return r;
 }
 
@@ -155,6 +171,15 @@ __device__ __forceinline__ s16x4 read_transposed(const uint8_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
 }
 
+// Four sums in the output's type, aligned as one element is.
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const f32x4v& v) {
+  T x[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = (T)v[e];
+  __builtin_memcpy(p, x, sizeof(x));
+}
+
 // Waves of a SIMD that the registers are to leave room for: the queries
 // (D/8 a term) and sums (D/4) of a row tile decide.
 constexpr int attn_waves(int D, int RT, int NT) { return RT * (D / 8 * NT + D / 4) <= 160 ? 2 : 1; }
@@ -168,7 +193,8 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
   constexpr int kJoin = kAttnWaves * 16 * kJoinRow * 4;
   constexpr int kMem = kAttnWaves * kStage > kJoin ? kAttnWaves * kStage : kJoin;
   __shared__ __attribute__((aligned(16))) uint8_t s_mem[kMem];
-  __shared__ float2 s_ml[kAttnWaves][RT * 16];
+  __shared__ float s_m[kAttnWaves][RT * 16];
+  __shared__ float2 s_ml[kAttnWaves][16];
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -180,19 +206,21 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
     const int n = gridDim.x, x = blockIdx.x & 7, q8 = n >> 3, r8 = n & 7;
     id = x * q8 + min(x, r8) + (blockIdx.x >> 3);
   }
-  const int tile = id % a.tiles;
-  id /= a.tiles;
-  const int split = id % a.splits;
-  id /= a.splits;
-  const int kvh = id % a.kv.Hk, b = id / a.kv.Hk;
+  const int G = a.G.d;
+  int rest = a.tiles.of(id);
+  const int tile = id - rest * a.tiles.d;
+  id = rest;
+  rest = a.splits.of(id);
+  const int split = id - rest * a.splits.d;
+  const int b = a.heads.of(rest), kvh = rest - b * a.kv.Hk;
 
   const KvRows sq = kv_rows(a.kv, b);
-  const int row_total = sq.rows * a.G, r0 = tile * 16 * RT;
+  const int row_total = sq.rows * G, r0 = tile * 16 * RT;
   if (r0 >= row_total) return;
   const int r_last = min(row_total, r0 + 16 * RT) - 1;
-  const int first = sq.place0 + r0 / a.G, last = sq.place0 + r_last / a.G;
+  const int first = sq.place0 + a.G.of(r0), last = sq.place0 + a.G.of(r_last);
   const KvRange rg = kv_range(a.kv, sq.len, first, last, a.splits, a.min_tiles);
-  if (split >= rg.used) return;
+  if (!rg.uses(split)) return;
   const int t_end = min(rg.ntile, (split + 1) * rg.per), t_last = t_end - 1;
 
   // Sixteen tokens (a run) lie in one page.  A run outside [beg, end) becomes
@@ -240,21 +268,25 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
   for (int rt = 0; rt < RT; ++rt) {
     const int r = r0 + 16 * rt + l16;
     const bool on = r < row_total;
-    const int m = min(r, row_total - 1) / a.G, h = kvh * a.G + min(r, row_total - 1) % a.G;
+    const int m = a.G.of(min(r, row_total - 1)), h = kvh * G + min(r, row_total - 1) - m * G;
     const int place = sq.place0 + m;
     hi[rt] = on ? min(place, rg.end - 1) : -1;
     lo[rt] = a.kv.window ? place - a.kv.window + 1 : 0;
     const T* qp = (const T*)a.q + (int64_t)(sq.off + m) * a.qs + (int64_t)h * D;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      float x[8];
-      load8(qp + step_channel<D>(s, g), a.vec & 1, x);
+      T x[8];
+      __builtin_memcpy(x, qp + step_channel<D>(s, g), sizeof(x));
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        bf16 t[NT];
-        split_terms<NT>(x[e], t);
+        if constexpr (NT == 1) {
+          qf[rt][s][0][e] = x[e];
+        } else {
+          bf16 t[NT];
+          split_terms<NT>((float)x[e], t);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) qf[rt][s][n][e] = t[n];
+          for (int n = 0; n < NT; ++n) qf[rt][s][n][e] = t[n];
+        }
       }
     }
   }
@@ -380,62 +412,58 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
     }
   }
 
-  // Join the waves.
+  // Join the waves: sums over the common maximum, a row tile at a time.
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     sum[rt] += __shfl_xor(sum[rt], 16, kWave);
     sum[rt] += __shfl_xor(sum[rt], 32, kWave);
-    if (g == 0) s_ml[wv][16 * rt + l16] = make_float2(mx[rt], sum[rt]);
+    if (g == 0) s_m[wv][16 * rt + l16] = mx[rt];
   }
   __syncthreads();  // also: every wave is done with its staged values
   float* join = reinterpret_cast<float*>(s_mem);
+  const int jr = threadIdx.x >> 4, jc = 4 * (threadIdx.x & 15);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    float m = -INFINITY;
+    float m = s_m[0][16 * rt + l16];
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) m = fmaxf(m, s_ml[w][16 * rt + l16].x);
+    for (int w = 1; w < kAttnWaves; ++w) m = fmaxf(m, s_m[w][16 * rt + l16]);
     const float f = mx[rt] == m ? 1.f : __builtin_amdgcn_exp2f(mx[rt] - m);
+    if (g == 0) s_ml[wv][l16] = make_float2(m, sum[rt] * f);
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb)
       *reinterpret_cast<f32x4v*>(join + (wv * 16 + l16) * kJoinRow + 16 * cb + 4 * g) = o[rt][cb] * f;
     __syncthreads();
-    const int jr = threadIdx.x >> 4, r = r0 + 16 * rt + jr;
+    const int r = r0 + 16 * rt + jr;
     if (r < row_total) {
-      float M = -INFINITY, L = 0.f;
-#pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) M = fmaxf(M, s_ml[w][16 * rt + jr].x);
+      const float M = s_ml[0][jr].x;
+      float L = 0.f;
+      f32x4v v[D / 64];
 #pragma unroll
       for (int w = 0; w < kAttnWaves; ++w) {
-        const float2 ml = s_ml[w][16 * rt + jr];
-        L += ml.x == M ? ml.y : ml.y * __builtin_amdgcn_exp2f(ml.x - M);
-      }
-      const int64_t at = (int64_t)(sq.off + r / a.G) * a.kv.Hq + kvh * a.G + r % a.G;
-      const bool whole = rg.used == 1;
-      const float inv = !whole ? 1.f : L == 0.f ? 0.f : 1.f / L;
+        L += s_ml[w][jr].y;
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        const int ch = 64 * j + 4 * (threadIdx.x & 15);
-        f32x4v v = *reinterpret_cast<f32x4v*>(join + jr * kJoinRow + ch);
-#pragma unroll
-        for (int w = 1; w < kAttnWaves; ++w)
-          v += *reinterpret_cast<f32x4v*>(join + (w * 16 + jr) * kJoinRow + ch);
-        v *= inv;
-        if (whole) {
-          T* out = (T*)a.out + at * D + ch;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) out[e] = (T)v[e];
-        } else {
-          *reinterpret_cast<f32x4v*>(a.part_o + (at * a.splits + split) * D + ch) = v;
+        for (int j = 0; j < D / 64; ++j) {
+          const f32x4v x = *reinterpret_cast<f32x4v*>(join + (w * 16 + jr) * kJoinRow + jc + 64 * j);
+          v[j] = w ? v[j] + x : x;
         }
       }
-      if ((threadIdx.x & 15) == 0) {
-        if (!whole)
-          a.part_ml[at * a.splits + split] = make_float2(M, L);
-        else if (a.lse)
+      const int rm = a.G.of(r);
+      const int64_t at = (int64_t)(sq.off + rm) * a.kv.Hq + kvh * G + r - rm * G;
+      if (rg.whole()) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        T* out = (T*)a.out + at * D + jc;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) store4(out + 64 * j, v[j] * inv);
+        if (jc == 0 && a.lse)
           a.lse[at] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.6931471805599453f;
+      } else {
+        float* part = a.part_o + (at * a.splits.d + split) * D + jc;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) *reinterpret_cast<f32x4v*>(part + 64 * j) = v[j];
+        if (jc == 0) a.part_ml[at * a.splits.d + split] = make_float2(M, L);
       }
     }
-    __syncthreads();
+    if (rt + 1 < RT) __syncthreads();
   }
 }
 

@@ -27,35 +27,37 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a, int row_tiles) {
   const int lane = threadIdx.x & (kWave - 1);
   const int64_t at = blockIdx.x;
   const int slot = threadIdx.x / L, c = threadIdx.x % L;
-  const float2* ml = a.part_ml + at * a.splits;
-  const f32x4v* part = reinterpret_cast<const f32x4v*>(a.part_o + at * a.splits * D) + c;
+  const int splits = a.splits.d;
+  const float2* ml = a.part_ml + at * splits;
+  const f32x4v* part = reinterpret_cast<const f32x4v*>(a.part_o + at * splits * D) + c;
   float2 x[kMaxSplits / kWave];
 #pragma unroll
-  for (int j = 0; j < kMaxSplits / kWave; ++j) x[j] = ml[min(lane + kWave * j, a.splits - 1)];
+  for (int j = 0; j < kMaxSplits / kWave; ++j) x[j] = ml[min(lane + kWave * j, splits - 1)];
   f32x4v v[kBatch];
 #pragma unroll
-  for (int j = 0; j < kBatch; ++j) v[j] = part[(int64_t)min(slot + kSlots * j, a.splits - 1) * L];
+  for (int j = 0; j < kBatch; ++j) v[j] = part[(int64_t)min(slot + kSlots * j, splits - 1) * L];
 
-  const int i = (int)(at / a.kv.Hq), h = (int)(at % a.kv.Hq);
+  const int kvh = a.G.of(blockIdx.x), i = a.heads.of(kvh);  // at = (i Hk + head) G + query of the head
   const int b = kv_sequence_of(a.kv, i);
   if (b < 0) return;
   const KvRows sq = kv_rows(a.kv, b);
   const int m = i - sq.off;
   if (m >= sq.rows) return;
-  const int r = m * a.G + h % a.G, r0 = r / (16 * row_tiles) * (16 * row_tiles);
-  const int r_last = min(sq.rows * a.G, r0 + 16 * row_tiles) - 1;
-  const int used = kv_range(a.kv, sq.len, sq.place0 + r0 / a.G, sq.place0 + r_last / a.G, a.splits,
-                            a.min_tiles).used;
-  if (used == 1) return;  // written whole
+  const int span = 16 * row_tiles, G = a.G.d;
+  const int r0 = (m * G + (int)blockIdx.x - kvh * G) & ~(span - 1);
+  const int r_last = min(sq.rows * G, r0 + span) - 1;
+  const KvRange rg = kv_range(a.kv, sq.len, sq.place0 + a.G.of(r0), sq.place0 + a.G.of(r_last), a.splits,
+                              a.min_tiles);
+  if (rg.whole()) return;  // written already
   float M = -INFINITY, sum = 0.f;
 #pragma unroll
   for (int j = 0; j < kMaxSplits / kWave; ++j)
-    if (lane + kWave * j < used) M = fmaxf(M, x[j].x);
+    if (rg.uses(lane + kWave * j)) M = fmaxf(M, x[j].x);
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) M = fmaxf(M, __shfl_xor(M, o, kWave));
 #pragma unroll
   for (int j = 0; j < kMaxSplits / kWave; ++j)
-    if (lane + kWave * j < used) {
+    if (rg.uses(lane + kWave * j)) {
       const float w = x[j].x == M ? 1.f : __builtin_amdgcn_exp2f(x[j].x - M);
       sum += w * x[j].y;
       if (threadIdx.x < kWave) s_w[lane + kWave * j] = w;
@@ -68,10 +70,10 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a, int row_tiles) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int s = slot + kSlots * j;
-      if (s < used) acc += s_w[s] * v[j];
+      if (rg.uses(s)) acc += s_w[s] * v[j];
     }
 #pragma unroll 4
-    for (int s = slot + kSlots * kBatch; s < used; s += kSlots) acc += s_w[s] * part[(int64_t)s * L];
+    for (int s = slot + kSlots * kBatch; rg.uses(s); s += kSlots) acc += s_w[s] * part[(int64_t)s * L];
     s_o[slot][c] = acc;
   }
   __syncthreads();
@@ -79,9 +81,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a, int row_tiles) {
 #pragma unroll
   for (int j = 1; j < kSlots; ++j) acc += s_o[j][c];
   acc *= sum == 0.f ? 0.f : 1.f / sum;
-  T* out = (T*)a.out + at * D + 4 * c;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) out[e] = (T)acc[e];
+  store4((T*)a.out + at * D + 4 * c, acc);
   if (a.lse && c == 0)
     a.lse[at] = sum == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }
@@ -180,11 +180,11 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
   a.part_o = (float*)workspace;
   a.part_ml = (float2*)((uint8_t*)workspace + p.o_bytes);
   a.c = (desc->scale > 0.f ? desc->scale : 1.f / sqrtf((float)desc->head_dim)) * 1.4426950408889634f;
-  a.G = desc->n_heads / desc->n_kv_heads;
-  a.tiles = p.tiles;
-  a.splits = p.splits;
+  a.G = make_divider(desc->n_heads / desc->n_kv_heads);
+  a.tiles = make_divider(p.tiles);
+  a.splits = make_divider(p.splits);
+  a.heads = make_divider(desc->n_kv_heads);
   a.min_tiles = p.min_tiles;
-  a.vec = (uintptr_t)q % 16 == 0 && q_stride * es % 16 == 0 ? 1 : 0;
   hipStream_t st = (hipStream_t)hip_stream;
   (void)hipGetLastError();
   switch (desc->head_dim) {
