@@ -50,30 +50,15 @@ struct AttnArgs {
   float* part_o;   // [row][head][split][D], sums not yet divided
   float2* part_ml;  // [row][head][split]: maximum (base 2), sum
   float c;         // scale * log2(e)
-  int min_tiles;
-  Divider G, tiles, splits, heads;  // query heads a key/value head; of a sequence's work; Hk
+  int row_tiles, min_tiles;
+  // Query heads a key/value head; row tiles of a sequence; splits at most;
+  // Hk; work of a head that runs at once; row tiles side by side on an XCD.
+  Divider G, tiles, splits, heads, share, group;
 };
 
 constexpr int kAttnWaves = 4;
 constexpr int kAttnTile = 32;  // tokens of a wave's step
-
-// The tokens [beg, end) that rows of places [first, last] see, in tiles from
-// tb on, `per` of them a split.
-struct KvRange {
-  int beg, end, tb, ntile, per;
-  __device__ __forceinline__ bool uses(int split) const { return split == 0 || split * per < ntile; }
-  __device__ __forceinline__ bool whole() const { return ntile <= per; }  // one split
-};
-__device__ __forceinline__ KvRange kv_range(const KvArgs& kv, int len, int first, int last,
-                                            const Divider& splits, int min_tiles) {
-  KvRange r;
-  r.end = min(min(len, kv.pages_per_seq << kv.page_shift), last + 1);
-  r.beg = kv.window ? max(0, first - kv.window + 1) : 0;
-  r.tb = r.beg & ~(kAttnTile - 1);
-  r.ntile = r.end > r.beg ? (r.end - r.tb + kAttnTile - 1) / kAttnTile : 0;
-  r.per = max(min_tiles, splits.of(r.ntile + splits.d - 1));
-  return r;
-}
+constexpr int kWholeRange = 1 << 28;  // a split of any number of tiles
 
 // A sequence's rows as the kernels use them.
 struct KvRows {
@@ -91,6 +76,86 @@ __device__ __forceinline__ KvRows kv_rows(const KvArgs& kv, int b) {
   return s;
 }
 
+// Sums, or maxima, of lanes 0 .. own.
+template <bool kMax>
+__device__ __forceinline__ int wave_scan(int v) {
+  auto join = [&](int x) { v = kMax ? max(v, x) : v + x; };
+  join(__builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false));  // 1, 2, 4, 8 lanes before, in rows
+  join(__builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false));
+  join(__builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false));
+  join(__builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false));
+  join(__builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));  // rows 0, 2 to 1, 3
+  join(__builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));  // lane 31 to the upper half
+  return v;
+}
+
+// How the tokens of a batch are cut: a split is `per` tiles, the same for
+// every sequence, so that work is even whatever the lengths are.  The
+// sequences' work (row tiles x tiles, a head) over what runs at once; no more
+// splits than there is room for.  Whole numbers, so that the kernels agree;
+// every wave finds them for itself, a lane a sequence, where there is
+// something to cut.
+struct KvCut {
+  int row_tiles, tiles;  // of a sequence: row tiles, tiles that one of them sees at most
+};
+__device__ __forceinline__ KvCut kv_cut(const AttnArgs& a, const KvRows& s) {
+  KvCut c;
+  const int span = 16 * a.row_tiles;
+  c.row_tiles = (s.rows * a.G.d + span - 1) / span;
+  int seen = min(s.len, a.kv.pages_per_seq << a.kv.page_shift);
+  // Rows of a tile: whole tokens, and one cut at either end.
+  if (a.kv.window) seen = (int)min((int64_t)seen, (int64_t)a.kv.window + a.G.of(span) + 2 + kAttnTile);
+  c.tiles = (seen + kAttnTile - 1) / kAttnTile;
+  return c;
+}
+__device__ __forceinline__ KvRows kv_lane_rows(const AttnArgs& a, int b) {
+  KvRows s{0, 0, 0, 0};
+  if (a.kv.n_seqs == 1) return kv_rows(a.kv, 0);  // in every lane
+  if (b < a.kv.n_seqs) s = kv_rows(a.kv, b);
+  return s;
+}
+// s: the lane's sequence, of the first 64.
+__device__ __forceinline__ int kv_per(const AttnArgs& a, const KvRows& s) {
+  int64_t all = 0;
+  int most = 0;
+  if (a.kv.n_seqs == 1) {
+    const KvCut c = kv_cut(a, s);
+    all = (int64_t)c.row_tiles * c.tiles;
+    most = c.tiles;
+  } else {
+    int64_t work = 0;
+    const int lane = threadIdx.x & (kWave - 1);
+    for (int b = 0; b < a.kv.n_seqs; b += kWave) {
+      const KvCut c = kv_cut(a, b ? kv_lane_rows(a, b + lane) : s);
+      work += (int64_t)c.row_tiles * c.tiles;
+      most = max(most, c.tiles);
+    }
+    most = __builtin_amdgcn_readlane(wave_scan<true>(most), kWave - 1);
+    all = __builtin_amdgcn_readlane(wave_scan<false>((int)(work >> 20)), kWave - 1);
+    all = (all << 20) + __builtin_amdgcn_readlane(wave_scan<false>((int)(work & 0xFFFFF)), kWave - 1);
+  }
+  // Rounded up, by the bits that the divider takes.
+  const int shift = max(0, 34 - (int)__builtin_clzll(all | 1));
+  const int64_t fair = (int64_t)(a.share.of((int)(all >> shift) + a.share.d - 1) + (shift ? 1 : 0)) << shift;
+  return max(a.min_tiles, max((int)min(fair, (int64_t)kWholeRange), a.splits.of(most + a.splits.d - 1)));
+}
+
+// The tokens [beg, end) that rows of places [first, last] see, in tiles from
+// tb on, `per` of them a split.
+struct KvRange {
+  int beg, end, tb, ntile, per;
+  __device__ __forceinline__ bool uses(int split) const { return split == 0 || split * per < ntile; }
+  __device__ __forceinline__ bool whole() const { return ntile <= per; }  // one split
+};
+__device__ __forceinline__ KvRange kv_range(const AttnArgs& a, int len, int first, int last, int per) {
+  KvRange r;
+  r.end = min(min(len, a.kv.pages_per_seq << a.kv.page_shift), last + 1);
+  r.beg = a.kv.window ? max(0, first - a.kv.window + 1) : 0;
+  r.tb = r.beg & ~(kAttnTile - 1);
+  r.ntile = r.end > r.beg ? (r.end - r.tb + kAttnTile - 1) / kAttnTile : 0;
+  r.per = per;
+  return r;
+}
 template <int D>
 __device__ __forceinline__ constexpr int step_channel(int step, int g) {
   constexpr int kFull = 4 * (D / 128);
@@ -180,9 +245,12 @@ __device__ __forceinline__ void store4(T* p, const f32x4v& v) {
   __builtin_memcpy(p, x, sizeof(x));
 }
 
-// Waves of a SIMD that the registers are to leave room for: the queries
-// (D/8 a term) and sums (D/4) of a row tile decide.
-constexpr int attn_waves(int D, int RT, int NT) { return RT * (D / 8 * NT + D / 4) <= 160 ? 2 : 1; }
+// Waves of a SIMD, and so workgroups of a CU, that the registers are to leave
+// room for: the queries (D/8 a term) and sums (D/4) of the row tiles decide.
+constexpr int attn_waves(int D, int RT, int NT) {
+  const int n = RT * (D / 8 * NT + D / 4);
+  return n <= 48 ? 4 : n <= 72 ? 3 : n <= 160 ? 2 : 1;
+}
 
 template <int D, int RT, int NT, typename T>
 __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv_attention(AttnArgs a) {
@@ -200,26 +268,64 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
   const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
 
-  // Consecutive work on one XCD: row tiles of a head share its L2.
-  int id;
-  {
-    const int n = gridDim.x, x = blockIdx.x & 7, q8 = n >> 3, r8 = n & 7;
-    id = x * q8 + min(x, r8) + (blockIdx.x >> 3);
-  }
+  // Work of a head is a list: sequences, their splits, the row tiles of a
+  // split.  Heads go round the XCDs, and a group of row tiles, which read the
+  // same tokens, lies eight workgroups apart, on one XCD, and shares its L2.
   const int G = a.G.d;
-  int rest = a.tiles.of(id);
-  const int tile = id - rest * a.tiles.d;
-  id = rest;
-  rest = a.splits.of(id);
-  const int split = id - rest * a.splits.d;
-  const int b = a.heads.of(rest), kvh = rest - b * a.kv.Hk;
+  int kvh, at;
+  {
+    const int v = blockIdx.x >> 3, y = a.group.of(v), u = 8 * y + (blockIdx.x & 7);
+    const int n = a.heads.of(u);
+    kvh = u - n * a.heads.d;
+    at = n * a.group.d + v - y * a.group.d;
+  }
+  int b, tile, split = 0, per = kWholeRange;
+  KvRows sq;
+  if (a.splits.d == 1) {
+    b = a.tiles.of(at);
+    tile = at - b * a.tiles.d;
+    if (b >= a.kv.n_seqs) return;
+    sq = kv_rows(a.kv, b);
+  } else if (a.kv.n_seqs == 1) {
+    sq = kv_rows(a.kv, 0);
+    per = kv_per(a, sq);
+    b = 0;
+    split = a.tiles.of(at);
+    tile = at - split * a.tiles.d;
+    if (split >= a.splits.d) return;
+  } else {
+    KvRows s = kv_lane_rows(a, lane);
+    per = kv_per(a, s);
+    for (b = 0;; b += kWave) {
+      if (b >= a.kv.n_seqs) return;
+      if (b) s = kv_lane_rows(a, b + lane);
+      const KvCut c = kv_cut(a, s);
+      const int splits = max(1, (int)((unsigned)(c.tiles + per - 1) / (unsigned)per));
+      const int n = c.row_tiles * splits, upto = wave_scan<false>(n);
+      const uint64_t past = __ballot(upto > at);
+      if (!past) {
+        at -= __builtin_amdgcn_readlane(upto, kWave - 1);
+        continue;
+      }
+      const int l = __builtin_ctzll(past);
+      b += l;
+      at -= __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l);
+      const int row_tiles = __builtin_amdgcn_readlane(c.row_tiles, l);
+      split = at / row_tiles;
+      tile = at - split * row_tiles;
+      sq.off = __builtin_amdgcn_readlane(s.off, l);
+      sq.rows = __builtin_amdgcn_readlane(s.rows, l);
+      sq.len = __builtin_amdgcn_readlane(s.len, l);
+      sq.place0 = __builtin_amdgcn_readlane(s.place0, l);
+      break;
+    }
+  }
 
-  const KvRows sq = kv_rows(a.kv, b);
   const int row_total = sq.rows * G, r0 = tile * 16 * RT;
   if (r0 >= row_total) return;
   const int r_last = min(row_total, r0 + 16 * RT) - 1;
   const int first = sq.place0 + a.G.of(r0), last = sq.place0 + a.G.of(r_last);
-  const KvRange rg = kv_range(a.kv, sq.len, first, last, a.splits, a.min_tiles);
+  const KvRange rg = kv_range(a, sq.len, first, last, per);
   if (!rg.uses(split)) return;
   const int t_end = min(rg.ntile, (split + 1) * rg.per), t_last = t_end - 1;
 
@@ -474,8 +580,9 @@ int32_t launch_kv_attention(const AttnArgs& a, int32_t dtype, int row_tiles, int
 constexpr int attn_most_row_tiles(int D, int NT) { return NT <= 2 && D <= 192 ? 2 : D <= 128 ? 2 : 1; }
 // Whole verify batches in one tile where they fit: every key is widened once
 // for all rows of the tile.
+inline int attn_terms(int32_t dtype) { return dtype == MOE_BF16 ? 1 : dtype == MOE_F16 ? 2 : 3; }
 inline int attn_row_tiles(int64_t rows, int D, int32_t dtype) {
-  return rows <= 16 ? 1 : attn_most_row_tiles(D, dtype == MOE_BF16 ? 1 : dtype == MOE_F16 ? 2 : 3);
+  return rows <= 16 ? 1 : attn_most_row_tiles(D, attn_terms(dtype));
 }
 
 }  // namespace svr

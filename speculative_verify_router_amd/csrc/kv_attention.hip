@@ -20,7 +20,7 @@ constexpr int kMaxSplits = 128;
 // first batch of every read is issued before it is known which splits are in
 // use (the workspace holds them all, what is not in use is dropped).
 template <int D, typename T>
-__global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a, int row_tiles) {
+__global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a) {
   constexpr int L = D / 4, kSlots = kBlock / L, kBatch = 4;
   __shared__ float s_w[kMaxSplits];
   __shared__ f32x4v s_o[kSlots][L];
@@ -38,16 +38,15 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a, int row_tiles) {
   for (int j = 0; j < kBatch; ++j) v[j] = part[(int64_t)min(slot + kSlots * j, splits - 1) * L];
 
   const int kvh = a.G.of(blockIdx.x), i = a.heads.of(kvh);  // at = (i Hk + head) G + query of the head
-  const int b = kv_sequence_of(a.kv, i);
+  const int per = kv_per(a, kv_lane_rows(a, lane)), b = kv_sequence_of(a.kv, i);
   if (b < 0) return;
   const KvRows sq = kv_rows(a.kv, b);
   const int m = i - sq.off;
   if (m >= sq.rows) return;
-  const int span = 16 * row_tiles, G = a.G.d;
+  const int span = 16 * a.row_tiles, G = a.G.d;
   const int r0 = (m * G + (int)blockIdx.x - kvh * G) & ~(span - 1);
   const int r_last = min(sq.rows * G, r0 + span) - 1;
-  const KvRange rg = kv_range(a.kv, sq.len, sq.place0 + a.G.of(r0), sq.place0 + a.G.of(r_last), a.splits,
-                              a.min_tiles);
+  const KvRange rg = kv_range(a, sq.len, sq.place0 + a.G.of(r0), sq.place0 + a.G.of(r_last), per);
   if (rg.whole()) return;  // written already
   float M = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -87,17 +86,17 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a, int row_tiles) {
 }
 
 template <int D>
-void launch_kv_join(const AttnArgs& a, int32_t dtype, int row_tiles, unsigned n, hipStream_t st) {
+void launch_kv_join(const AttnArgs& a, int32_t dtype, unsigned n, hipStream_t st) {
   switch (dtype) {
-    case MOE_F32: hipLaunchKernelGGL((k_kv_join<D, float>), dim3(n), dim3(kBlock), 0, st, a, row_tiles); break;
-    case MOE_BF16: hipLaunchKernelGGL((k_kv_join<D, bf16>), dim3(n), dim3(kBlock), 0, st, a, row_tiles); break;
-    default: hipLaunchKernelGGL((k_kv_join<D, _Float16>), dim3(n), dim3(kBlock), 0, st, a, row_tiles); break;
+    case MOE_F32: hipLaunchKernelGGL((k_kv_join<D, float>), dim3(n), dim3(kBlock), 0, st, a); break;
+    case MOE_BF16: hipLaunchKernelGGL((k_kv_join<D, bf16>), dim3(n), dim3(kBlock), 0, st, a); break;
+    default: hipLaunchKernelGGL((k_kv_join<D, _Float16>), dim3(n), dim3(kBlock), 0, st, a); break;
   }
 }
 
-// How a batch is cut: by its sizes alone (the lengths are on the device).
+// How a batch is cut, as far as its sizes say (the lengths are on the device).
 struct AttnPlan {
-  int row_tiles, tiles, splits, min_tiles;
+  int row_tiles, tiles, splits, min_tiles, share, group;
   int64_t grid;
   size_t o_bytes, bytes;
 };
@@ -107,16 +106,28 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   const int G = d->n_heads / d->n_kv_heads;
   const int64_t rows = (int64_t)(b->max_rows < b->n_tokens ? b->max_rows : b->n_tokens) * G;
   p.row_tiles = attn_row_tiles(rows, d->head_dim, dtype);
-  p.tiles = (int)((rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles));
+  const int span = 16 * p.row_tiles;
+  p.tiles = (int)((rows + span - 1) / span);
   p.min_tiles = kAttnWaves;  // a tile a wave
-  const int64_t base = (int64_t)b->n_seqs * d->n_kv_heads * p.tiles;
+  // Work of a head that runs at once, and its row tiles at most.
+  const int slots = 256 * attn_waves(d->head_dim, p.row_tiles, attn_terms(dtype)) / d->n_kv_heads;
+  int64_t all = (int64_t)b->n_seqs * p.tiles;
+  const int64_t dense = ((int64_t)b->n_tokens * G + span - 1) / span + b->n_seqs;
+  all = all < dense ? all : dense;
+  // Every sequence's last split is half full on the average.
+  p.share = (int)(slots - all / 2 > slots / 2 ? slots - all / 2 : slots / 2);
+  p.share = p.share > 0 ? p.share : 1;
   int64_t seen = (int64_t)b->pages_per_seq * d->page_size;
   if (d->window && d->window + (int64_t)b->max_rows < seen) seen = d->window + (int64_t)b->max_rows;
   const int64_t most = (seen / kAttnTile + 2 + p.min_tiles - 1) / p.min_tiles;
-  int64_t s = base > 0 ? 512 / base : 1;
-  s = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
+  // One sequence gets all splits, several up to four times their even part.
+  int64_t s = 2 * all > slots ? 1 : b->n_seqs == 1 ? slots / all : (4 * slots + all - 1) / all;
+  s = s > kMaxSplits ? kMaxSplits : s;
   p.splits = (int)(s < most ? s : most);
-  p.grid = base * p.splits;
+  p.group = p.tiles < 64 ? p.tiles : 64;
+  const int64_t list = p.splits == 1 ? (int64_t)b->n_seqs * p.tiles
+                       : b->n_seqs == 1 ? (int64_t)p.splits * p.tiles : p.share + all;
+  p.grid = ((list + p.group - 1) / p.group * d->n_kv_heads + 7) / 8 * 8 * p.group;
   if (p.splits > 1) {
     const size_t n = (size_t)b->n_tokens * d->n_heads * p.splits;
     p.o_bytes = (n * d->head_dim * 4 + 255) & ~(size_t)255;
@@ -184,7 +195,10 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
   a.tiles = make_divider(p.tiles);
   a.splits = make_divider(p.splits);
   a.heads = make_divider(desc->n_kv_heads);
+  a.share = make_divider(p.share);
+  a.group = make_divider(p.group);
   a.min_tiles = p.min_tiles;
+  a.row_tiles = p.row_tiles;
   hipStream_t st = (hipStream_t)hip_stream;
   (void)hipGetLastError();
   switch (desc->head_dim) {
@@ -196,10 +210,10 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
   if (rc != MOE_OK || p.splits == 1) return rc;
   const unsigned n = (unsigned)batch->n_tokens * (unsigned)desc->n_heads;
   switch (desc->head_dim) {
-    case 64: launch_kv_join<64>(a, dtype, p.row_tiles, n, st); break;
-    case 128: launch_kv_join<128>(a, dtype, p.row_tiles, n, st); break;
-    case 192: launch_kv_join<192>(a, dtype, p.row_tiles, n, st); break;
-    default: launch_kv_join<256>(a, dtype, p.row_tiles, n, st); break;
+    case 64: launch_kv_join<64>(a, dtype, n, st); break;
+    case 128: launch_kv_join<128>(a, dtype, n, st); break;
+    case 192: launch_kv_join<192>(a, dtype, n, st); break;
+    default: launch_kv_join<256>(a, dtype, n, st); break;
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }

@@ -241,6 +241,22 @@ def test_attention_over_many_tokens(dtype, dim):
     check_attention(lay, plan, plan.filled_cache(rng), dtype, rng)
 
 
+@pytest.mark.parametrize("seqs,heads,kv_heads,page,window", [(2, 8, 2, 16, 0), (64, 4, 2, 32, 0), (65, 6, 3, 16, 0),
+                                                             (150, 2, 1, 16, 0), (70, 3, 1, 16, 120)])
+def test_attention_over_uneven_sequences(seqs, heads, kv_heads, page, window):
+    """One long sequence among short and empty ones: the splits of a batch are shared out by its lengths,
+    a wave at a time (of 64 sequences)."""
+    log(f"uneven {seqs} {heads}/{kv_heads} W={window}")
+    rng = np.random.default_rng(seqs)
+    lay = ko.Layout(heads, kv_heads, 64, page, window)
+    rows = rng.integers(0, 4, seqs)
+    lens = rows + rng.integers(0, 90, seqs)
+    rows[seqs // 2], lens[seqs // 2] = 41, 2100
+    rows[-1], lens[-1] = 2, 700
+    plan = Plan(lay, list(rows), list(lens), rng, pad_rows=1)
+    check_attention(lay, plan, plan.filled_cache(rng), "bf16", rng)
+
+
 def test_attention_where_one_score_stands_out():
     """Peaked rows, and maxima that keep growing along the axis (every tile rescales)."""
     rng = np.random.default_rng(12)
