@@ -109,10 +109,17 @@ def mfma_utilisation(cfg, ids_per_instance, t_us: float) -> dict:
             "token_tile_padding": round(pad, 4)}
 
 
+# Sources of the operators beside the layer and verify/accept, which no
+# counter profile covers.
+OTHER_SOURCES = ("kv", "launch_attention", "logprobs")
+
+
 def source_hash() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "speculative_verify_router_amd", "csrc")
     for name in sorted(os.listdir(csrc)):
+        if name.startswith(OTHER_SOURCES):
+            continue
         with open(os.path.join(csrc, name), "rb") as f:
             h.update(name.encode() + f.read())
     return h.hexdigest()[:16]
@@ -344,6 +351,93 @@ def bench_accept(args) -> int:
     return 0
 
 
+def bench_step(args) -> int:
+    """A verify step's operators in the order of use: cache append, attention,
+    the layer, verify/accept, log probabilities: steps/s.
+
+    Steps rotate over layer and cache instances as the layer's own workload
+    does; a graph of one step an instance is timed as well."""
+    import torch
+    import speculative_verify_router_amd as svr
+    import synth
+
+    w = synth.STEP_WORKLOADS[args.workload]
+    cfg = synth.CONFIGS[w["layer"]]
+    dev = torch.device("cuda:0")
+    torch.cuda.set_device(dev)
+    M, D, P, V, top = cfg.n_tokens, w["dim"], w["page"], w["vocab"], w["top"]
+    ld = svr.LayerDesc(cfg.hidden, cfg.n_experts, cfg.top_k, cfg.ffn, cfg.shared_ffn,
+                       cfg.expert_type, cfg.shared_type, down_type=cfg.down_type)
+    kd = svr.KvDesc(w["heads"], w["kv_heads"], D, P, rotary_dims=w["rotary"])
+    i32, f32 = dict(dtype=torch.int32, device=dev), dict(dtype=torch.float32, device=dev)
+    pages = -(-w["length"] // P)
+    gen = torch.Generator(device=dev).manual_seed(0)
+    steps = []
+    for i in range(max(1, args.instances)):
+        inp = synth.draw_layer(cfg, instance=i)
+        x, _ = synth.draw_tokens(cfg, instance=i)
+        up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)  # noqa: E731
+        lw = svr.LayerWeights(up(inp.router), up(inp.gate), up(inp.up), up(inp.down))
+        if cfg.shared_ffn:
+            lw.shared_gate, lw.shared_up, lw.shared_down = (up(inp.shared_gate), up(inp.shared_up),
+                                                            up(inp.shared_down))
+        batch = svr.KvBatch(torch.tensor([0, M], **i32), torch.tensor([w["length"]], **i32),
+                            torch.randperm(pages, generator=gen, device=dev).int()[None].contiguous(), M)
+        cache = svr.kv_cache(kd, pages)
+        cache.random_(0, 256, generator=gen)
+        cache[..., P * D:] = 126  # scales of 1/2: codes of up to 3
+        qkv = torch.randn((M, (w["heads"] + 2 * w["kv_heads"]) * D), generator=gen, device=dev).bfloat16()
+        q, k, v = (t.unflatten(1, (-1, D)) for t in
+                   qkv.split([w["heads"] * D, w["kv_heads"] * D, w["kv_heads"] * D], 1))
+        b = synth.draw_verify_batch(M, V, 0, i % M, seed=i)
+        steps.append((lw, up(x), batch, cache, q, k, v, up(b.logits), up(b.drafts)))
+        print(f"# instance {i} resident", file=sys.stderr, flush=True)
+    norm = torch.ones(D, **f32)
+    inv_freq = 10000.0 ** (-torch.arange(0, w["rotary"], 2, **f32) / w["rotary"])
+    qo = torch.empty((M, w["heads"], D), dtype=torch.bfloat16, device=dev)
+    att, y = torch.empty_like(qo), torch.empty((M, cfg.hidden), **f32)
+    tok, acc, n = torch.empty(M, **i32), torch.empty(M, **i32), torch.empty(1, **i32)
+    lp, ent = torch.empty(M, **f32), torch.empty(M, **f32)
+    ids, tlp = torch.empty((M, top), **i32), torch.empty((M, top), **f32)
+    ws = (svr.kv_workspace(kd, steps[0][2], M), svr.workspace(ld, M), svr.accept_workspace(M, V),
+          svr.logprobs_workspace(M, V, top))
+
+    def call(i):
+        lw, x, batch, cache, q, k, v, logits, drafts = steps[i % len(steps)]
+        svr.moe_kv_append(kd, batch, q, k, v, cache, qo, q_norm=norm, k_norm=norm, inv_freq=inv_freq)
+        svr.moe_kv_attention(kd, batch, qo, cache, att, ws=ws[0])
+        svr.moe_layer_forward(ld, lw, x, y, None, None, ws=ws[1])
+        svr.moe_verify_accept(logits, drafts, tok, acc, n, ws=ws[2])
+        svr.moe_logprobs(logits, tok, lp, ent, ids, tlp, ws=ws[3])
+
+    def timed(f, count):
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        for s in range(count):
+            f(s)
+        torch.cuda.synchronize()
+        return (time.perf_counter() - t0) / count
+
+    for s in range(max(args.warmup, len(steps))):
+        call(s)
+    eager = timed(call, args.steps)
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        for s in range(len(steps)):
+            call(s)
+    g.replay()
+    rounds = max(1, args.steps // len(steps))
+    graph = timed(lambda s: g.replay(), rounds) / len(steps)
+    print(json.dumps({
+        "metric": f"verify steps/s (append, attention, layer, accept, log probabilities; M={M}), 1 MI355X",
+        "value": round(1 / eager, 1), "unit": "steps/s", "n_gpus": 1, "steps": args.steps,
+        "warmup": args.warmup, "ms_per_step": round(eager * 1e3, 5), "higher_is_better": True,
+        "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+        "config": {"workload": args.workload, **w, "rows": M, "instances": len(steps)},
+        "graph_ms_per_step": round(graph * 1e3, 5)}), flush=True)
+    return 0
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     ap.add_argument("--gpus", type=int, default=1)
@@ -387,6 +481,8 @@ def main(argv=None) -> int:
 
     if args.workload in synth.ACCEPT_WORKLOADS:
         return bench_accept(args)
+    if args.workload in synth.STEP_WORKLOADS:
+        return bench_step(args)
     cfg = synth.CONFIGS[args.workload]
     dev = torch.device("cuda:0")
     torch.cuda.set_device(dev)

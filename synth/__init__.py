@@ -32,4 +32,4 @@ from .layers import (  # noqa: F401
     quantize_q8_0,
     tensor_bytes,
 )
-from .verify import ACCEPT_WORKLOADS, VerifyBatch, draw_verify_batch  # noqa: F401,E402
+from .verify import ACCEPT_WORKLOADS, STEP_WORKLOADS, VerifyBatch, draw_verify_batch  # noqa: F401,E402

@@ -30,6 +30,14 @@ ACCEPT_WORKLOADS = {
     "accept_m4": dict(rows=4, vocab=131072, h_dim=4096),
 }
 
+# One verify step around a layer workload: attention over `length` tokens (the
+# verify rows included) of a 4-bit cache of a generic grouped-query layout, the
+# layer, verify/accept and the log probabilities of the returned tokens.
+STEP_WORKLOADS = {
+    "verify_step_m4": dict(layer="step35_verify_m4", heads=64, kv_heads=4, dim=192, page=64,
+                           rotary=64, length=60000, vocab=131072, top=20),
+}
+
 
 @dataclasses.dataclass
 class VerifyBatch:
