@@ -19,9 +19,9 @@ constexpr int kMaxSplits = 128;
 // turn.  Bound by latency, not bytes (a row's parts are at most 128 KB): the
 // first batch of every read is issued before it is known which splits are in
 // use (the workspace holds them all, what is not in use is dropped).
-template <int D, typename T>
+template <int D, int kBatch, typename T>
 __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a) {
-  constexpr int L = D / 4, kSlots = kBlock / L, kBatch = 4;
+  constexpr int L = D / 4, kSlots = kBlock / L;
   __shared__ float s_w[kMaxSplits];
   __shared__ f32x4v s_o[kSlots][L];
   const int lane = threadIdx.x & (kWave - 1);
@@ -85,13 +85,19 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a) {
     a.lse[at] = sum == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }
 
+template <int D, int kBatch>
+void launch_kv_join(const AttnArgs& a, int32_t dtype, unsigned n, hipStream_t st) {
+  const dim3 g(n), t(kBlock);
+  switch (dtype) {
+    case MOE_F32: hipLaunchKernelGGL((k_kv_join<D, kBatch, float>), g, t, 0, st, a); break;
+    case MOE_BF16: hipLaunchKernelGGL((k_kv_join<D, kBatch, bf16>), g, t, 0, st, a); break;
+    default: hipLaunchKernelGGL((k_kv_join<D, kBatch, _Float16>), g, t, 0, st, a); break;
+  }
+}
 template <int D>
 void launch_kv_join(const AttnArgs& a, int32_t dtype, unsigned n, hipStream_t st) {
-  switch (dtype) {
-    case MOE_F32: hipLaunchKernelGGL((k_kv_join<D, float>), dim3(n), dim3(kBlock), 0, st, a); break;
-    case MOE_BF16: hipLaunchKernelGGL((k_kv_join<D, bf16>), dim3(n), dim3(kBlock), 0, st, a); break;
-    default: hipLaunchKernelGGL((k_kv_join<D, _Float16>), dim3(n), dim3(kBlock), 0, st, a); break;
-  }
+  if (a.kv.n_seqs == 1) launch_kv_join<D, 13>(a, dtype, n, st);
+  else launch_kv_join<D, 1>(a, dtype, n, st);
 }
 
 // How a batch is cut, as far as its sizes say (the lengths are on the device).
