@@ -93,8 +93,7 @@ int32_t moe_kv_cache_bytes(const moe_kv_desc* desc, int64_t n_pages, int64_t* by
 /* Norms, rotation and append, ONE launch.  dtype: MOE_F32, MOE_BF16 or
  * MOE_F16, of q, k, v and q_out.  q [n_tokens][n_heads][D], k and v
  * [n_tokens][n_kv_heads][D] with rows q_stride, k_stride, v_stride elements
- * apart (views of one fused projection need no copy; 16-byte aligned rows
- * are read with 16-byte loads), q_out contiguous [n_tokens][n_heads][D].
+ * apart (views of one fused projection need no copy), q_out contiguous [n_tokens][n_heads][D].
  *   q_out = rotate(norm(q) * q_norm), k likewise with k_norm, v as it is;
  *   norm(x) = x / sqrt(mean(x^2) + norm_eps) over a head's D channels;
  *   q_norm, k_norm [D] float, NULL: no norm.
@@ -115,8 +114,10 @@ int32_t moe_kv_append(const moe_kv_desc* desc, const moe_kv_batch* batch, int32_
                       const float* inv_freq, const int32_t* positions, void* cache,
                       int32_t n_pages, void* q_out, void* hip_stream);
 
-/* Device workspace, in *bytes, of moe_kv_attention for this desc and batch
- * (its sizes only; the arrays may be NULL).  The workspace needs no
+/* Device workspace, in *bytes, of moe_kv_attention for this desc and the
+ * sizes of this batch (the arrays may be NULL).  Other sizes need their own,
+ * and smaller ones may need more (fewer rows are cut into more parts): for a
+ * range of sizes, take the largest.  The workspace needs no
  * initialisation; calls that share one must not overlap in time.  0 is
  * possible, and then workspace may be NULL. */
 int32_t moe_kv_attention_workspace_bytes(const moe_kv_desc* desc, const moe_kv_batch* batch,

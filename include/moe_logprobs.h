@@ -38,7 +38,8 @@ extern "C" {
  * vocab columns and max_top alternatives: 2048 bytes of counters, then the
  * parts of rows that several workgroups share.  The counters must be zero
  * before the first call that uses the workspace; every call leaves them
- * zero, so zero-fill a workspace once when it is allocated.  Calls that share a workspace must not overlap in time.
+ * zero, so zero-fill a workspace once when it is allocated.  Calls that
+ * share a workspace must not overlap in time.
  * MOE_ERR_NULL if bytes is NULL; MOE_ERR_SHAPE for sizes out of range. */
 int32_t moe_logprobs_workspace_bytes(int32_t max_rows, int64_t vocab, int32_t max_top,
                                      size_t* bytes);

@@ -435,6 +435,21 @@ def _call_on(device: torch.device, stream, f, *args) -> int:
         return f(*args, handle)
 
 
+def _check_int32(obj, *names):
+    """ctypes would cut a larger number off in silence."""
+    for name in names:
+        if not -2 ** 31 <= getattr(obj, name) < 2 ** 31:
+            raise ValueError(f"{name}: {getattr(obj, name)} does not fit 32 bits")
+
+
+def _default_workspace(stream, make, *args) -> torch.Tensor:
+    """A workspace of the stream that will use it: filled there, and given back there."""
+    if stream is None:
+        return make(*args)
+    with torch.cuda.stream(stream):
+        return make(*args)
+
+
 @dataclasses.dataclass(frozen=True)
 class KvDesc:
     """Head layout and cache format of one attention layer (moe_kv_desc)."""
@@ -449,6 +464,7 @@ class KvDesc:
     norm_eps: float = 1e-6
 
     def __post_init__(self):
+        _check_int32(self, "n_heads", "n_kv_heads", "head_dim", "page_size", "window", "rotary_dims")
         # The fields never change, so the C struct is made once.
         object.__setattr__(self, "_c", _KvDesc(
             self.n_heads, self.n_kv_heads, self.head_dim, self.page_size, self.window,
@@ -484,11 +500,16 @@ class KvBatch:
         args = (width, _on(dev, self.q_offsets, i32, (B + 1,), "q_offsets"),
                 _on(dev, self.seq_lens, i32, (B,), "seq_lens"),
                 _on(dev, self.page_table, i32, None, "page_table"))
+        _check_int32(self, "max_rows")
         object.__setattr__(self, "_args", args)
+        object.__setattr__(self, "_device", dev)
         object.__setattr__(self, "_c", None)
 
-    def c(self, n_tokens: int) -> _KvBatch:
+    def c(self, n_tokens: int, device: Optional[torch.device] = None) -> _KvBatch:
+        """The C struct for rows on `device` (None: sizes only)."""
         c = self._c
+        if device is not None and device != self._device:
+            raise ValueError(f"batch: expected tensors on {device}, got {self._device}")
         if c is None or c.n_tokens != n_tokens:
             c = _KvBatch(self.page_table.shape[0], n_tokens, self.max_rows, *self._args)
             object.__setattr__(self, "_c", c)
@@ -529,7 +550,7 @@ def moe_kv_append(desc: KvDesc, batch: KvBatch, q: Optional[torch.Tensor], k: to
         op = _on(dev, q_out, dt, (T, desc.n_heads, D), "q_out")
     kp, ks = _rows(dev, k, dt, kv, "k")
     vp, vs = _rows(dev, v, dt, kv, "v")
-    st = _call_on(dev, stream, lib().moe_kv_append, desc.c(), batch.c(T), _act_dtype(k), qp, qs, kp,
+    st = _call_on(dev, stream, lib().moe_kv_append, desc.c(), batch.c(T, dev), _act_dtype(k), qp, qs, kp,
                   ks, vp, vs, _on(dev, q_norm, f32, (D,), "q_norm"),
                   _on(dev, k_norm, f32, (D,), "k_norm"),
                   _on(dev, inv_freq, f32, (desc.rotary_dims // 2,), "inv_freq"),
@@ -559,9 +580,9 @@ def moe_kv_attention(desc: KvDesc, batch: KvBatch, q: torch.Tensor, cache: torch
     dev = q.device
     T, shape = q.shape[0], (q.shape[0], desc.n_heads, desc.head_dim)
     if ws is None:
-        ws = kv_workspace(desc, batch, T)
+        ws = _default_workspace(stream, kv_workspace, desc, batch, T)
     qp, qs = _rows(dev, q, q.dtype, shape, "q")
-    st = _call_on(dev, stream, lib().moe_kv_attention, desc.c(), batch.c(T), _act_dtype(q), qp, qs,
+    st = _call_on(dev, stream, lib().moe_kv_attention, desc.c(), batch.c(T, dev), _act_dtype(q), qp, qs,
                   _cache(desc, cache, dev), cache.shape[0], _on(dev, out, q.dtype, shape, "out"),
                   _on(dev, lse, torch.float32, shape[:2], "lse"),
                   _on(dev, ws, torch.uint8, None, "ws"), ws.numel())
@@ -576,7 +597,7 @@ def moe_kv_read(desc: KvDesc, batch: KvBatch, cache: torch.Tensor, k_out: Option
     if some is None:
         raise ValueError("moe_kv_read: k_out or v_out is needed")
     shape = (some.shape[0], desc.n_kv_heads, desc.head_dim)
-    st = _call_on(dev, stream, lib().moe_kv_read, desc.c(), batch.c(shape[0]),
+    st = _call_on(dev, stream, lib().moe_kv_read, desc.c(), batch.c(shape[0], dev),
                   _cache(desc, cache, dev), cache.shape[0],
                   _on(dev, k_out, torch.float32, shape, "k_out"),
                   _on(dev, v_out, torch.float32, shape, "v_out"))
@@ -621,7 +642,7 @@ def moe_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor],
         raise ValueError("top_ids, top_logprobs: expected [rows][alternatives]")
     k = some.shape[1] if some is not None else 0
     if ws is None:
-        ws = logprobs_workspace(N, V, k, dev)
+        ws = _default_workspace(stream, logprobs_workspace, N, V, k, dev)
     st = _call_on(dev, stream, lib().moe_logprobs, logits.data_ptr(), _act_dtype(logits), N, V,
                   stride, _on(dev, targets, torch.int32, (N,), "targets"),
                   _on(dev, logprobs, f32, (N,), "logprobs"),

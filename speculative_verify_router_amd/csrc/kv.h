@@ -76,7 +76,7 @@ inline KvArgs kv_args(const moe_kv_desc* d, const moe_kv_batch* b, int32_t n_pag
   a.Hk = d->n_kv_heads;
   a.D = d->head_dim;
   a.page_shift = __builtin_ctz((unsigned)d->page_size);
-  a.window = d->window;
+  a.window = d->window < 1 << 30 ? d->window : 1 << 30;  // places are below 2^28: no sum passes 32 bits
   a.n_pages = n_pages;
   a.page_bytes = kv_page_bytes(d);
   return a;

@@ -47,13 +47,17 @@ struct AttnArgs {
   const uint8_t* cache;
   void* out;
   float* lse;
-  float* part_o;   // [row][head][split][D], sums not yet divided
-  float2* part_ml;  // [row][head][split]: maximum (base 2), sum
+  // [part row][head][split][D] sums not yet divided, and [..][split]: maximum
+  // (base 2), sum.  A part row is a row of the batch, or row m of sequence b
+  // as b * max_rows + m where those are fewer (a padded batch).
+  float* part_o;
+  float2* part_ml;
   float c;         // scale * log2(e)
-  int row_tiles, min_tiles;
+  int row_tiles, min_tiles, by_seq;
   // Query heads a key/value head; row tiles of a sequence; splits at most;
-  // Hk; work of a head that runs at once; row tiles side by side on an XCD.
-  Divider G, tiles, splits, heads, share, group;
+  // Hk; work of a head that runs at once; row tiles side by side on an XCD;
+  // max_rows.
+  Divider G, tiles, splits, heads, share, group, rows;
 };
 
 constexpr int kAttnWaves = 4;
@@ -113,6 +117,17 @@ __device__ __forceinline__ KvRows kv_lane_rows(const AttnArgs& a, int b) {
   if (a.kv.n_seqs == 1) return kv_rows(a.kv, 0);  // in every lane
   if (b < a.kv.n_seqs) s = kv_rows(a.kv, b);
   return s;
+}
+// Whether workgroups look their work up in the sequences' counts: not where
+// there is one sequence, or one row tile and no split of each.  (A lookup
+// passes over 64 sequences at a time; thousands of them are not split, and
+// their missing row tiles cost less.)
+constexpr int kMostListed = 1024;
+__host__ __device__ __forceinline__ bool kv_listed(int n_seqs, int tiles, int splits) {
+  return n_seqs > 1 && (splits > 1 || (tiles > 1 && n_seqs <= kMostListed));
+}
+__device__ __forceinline__ bool kv_listed(const AttnArgs& a) {
+  return kv_listed(a.kv.n_seqs, a.tiles.d, a.splits.d);
 }
 // s: the lane's sequence, of the first 64.
 __device__ __forceinline__ int kv_per(const AttnArgs& a, const KvRows& s) {
@@ -281,21 +296,19 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
   }
   int b, tile, split = 0, per = kWholeRange;
   KvRows sq;
-  if (a.splits.d == 1) {
+  if (!kv_listed(a)) {  // as many splits, and row tiles, of each sequence
     b = a.tiles.of(at);
     tile = at - b * a.tiles.d;
-    if (b >= a.kv.n_seqs) return;
+    if (a.kv.n_seqs == 1) {
+      split = b;
+      b = 0;
+    }
+    if (b >= a.kv.n_seqs || split >= a.splits.d) return;
     sq = kv_rows(a.kv, b);
-  } else if (a.kv.n_seqs == 1) {
-    sq = kv_rows(a.kv, 0);
-    per = kv_per(a, sq);
-    b = 0;
-    split = a.tiles.of(at);
-    tile = at - split * a.tiles.d;
-    if (split >= a.splits.d) return;
+    if (a.splits.d > 1) per = kv_per(a, sq);
   } else {
     KvRows s = kv_lane_rows(a, lane);
-    per = kv_per(a, s);
+    if (a.splits.d > 1) per = kv_per(a, s);
     for (b = 0;; b += kWave) {
       if (b >= a.kv.n_seqs) return;
       if (b) s = kv_lane_rows(a, b + lane);
@@ -563,10 +576,12 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
         if (jc == 0 && a.lse)
           a.lse[at] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.6931471805599453f;
       } else {
-        float* part = a.part_o + (at * a.splits.d + split) * D + jc;
+        const int64_t row = a.by_seq ? (int64_t)b * a.kv.max_rows + rm : sq.off + rm;
+        const int64_t pt = (row * a.kv.Hq + kvh * G + r - rm * G) * a.splits.d + split;
+        float* part = a.part_o + pt * D + jc;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) *reinterpret_cast<f32x4v*>(part + 64 * j) = v[j];
-        if (jc == 0) a.part_ml[at * a.splits.d + split] = make_float2(M, L);
+        if (jc == 0) a.part_ml[pt] = make_float2(M, L);
       }
     }
     if (rt + 1 < RT) __syncthreads();

@@ -25,7 +25,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a) {
   __shared__ float s_w[kMaxSplits];
   __shared__ f32x4v s_o[kSlots][L];
   const int lane = threadIdx.x & (kWave - 1);
-  const int64_t at = blockIdx.x;
+  const int64_t at = blockIdx.x;  // of the parts
   const int slot = threadIdx.x / L, c = threadIdx.x % L;
   const int splits = a.splits.d;
   const float2* ml = a.part_ml + at * splits;
@@ -37,11 +37,11 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a) {
 #pragma unroll
   for (int j = 0; j < kBatch; ++j) v[j] = part[(int64_t)min(slot + kSlots * j, splits - 1) * L];
 
-  const int kvh = a.G.of(blockIdx.x), i = a.heads.of(kvh);  // at = (i Hk + head) G + query of the head
-  const int per = kv_per(a, kv_lane_rows(a, lane)), b = kv_sequence_of(a.kv, i);
+  const int kvh = a.G.of(blockIdx.x), row = a.heads.of(kvh);  // at = (row Hk + head) G + query of the head
+  const int per = kv_per(a, kv_lane_rows(a, lane)), b = a.by_seq ? a.rows.of(row) : kv_sequence_of(a.kv, row);
   if (b < 0) return;
   const KvRows sq = kv_rows(a.kv, b);
-  const int m = i - sq.off;
+  const int m = a.by_seq ? row - b * a.kv.max_rows : row - sq.off;
   if (m >= sq.rows) return;
   const int span = 16 * a.row_tiles, G = a.G.d;
   const int r0 = (m * G + (int)blockIdx.x - kvh * G) & ~(span - 1);
@@ -80,9 +80,10 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a) {
 #pragma unroll
   for (int j = 1; j < kSlots; ++j) acc += s_o[j][c];
   acc *= sum == 0.f ? 0.f : 1.f / sum;
-  store4((T*)a.out + at * D + 4 * c, acc);
+  const int64_t to = (int64_t)(sq.off + m) * a.kv.Hq + (at - (int64_t)row * a.kv.Hq);
+  store4((T*)a.out + to * D + 4 * c, acc);
   if (a.lse && c == 0)
-    a.lse[at] = sum == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+    a.lse[to] = sum == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }
 
 template <int D, int kBatch>
@@ -102,7 +103,8 @@ void launch_kv_join(const AttnArgs& a, int32_t dtype, unsigned n, hipStream_t st
 
 // How a batch is cut, as far as its sizes say (the lengths are on the device).
 struct AttnPlan {
-  int row_tiles, tiles, splits, min_tiles, share, group;
+  int row_tiles, tiles, splits, min_tiles, share, group, by_seq;
+  int64_t part_rows;
   int64_t grid;
   size_t o_bytes, bytes;
 };
@@ -131,11 +133,14 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   s = s > kMaxSplits ? kMaxSplits : s;
   p.splits = (int)(s < most ? s : most);
   p.group = p.tiles < 64 ? p.tiles : 64;
-  const int64_t list = p.splits == 1 ? (int64_t)b->n_seqs * p.tiles
-                       : b->n_seqs == 1 ? (int64_t)p.splits * p.tiles : p.share + all;
+  const int64_t list = !kv_listed(b->n_seqs, p.tiles, p.splits) ? (int64_t)b->n_seqs * p.splits * p.tiles
+                       : p.splits == 1 ? all : p.share + all;
   p.grid = ((list + p.group - 1) / p.group * d->n_kv_heads + 7) / 8 * 8 * p.group;
+  const int64_t most_rows = (int64_t)b->n_seqs * b->max_rows;
+  p.by_seq = most_rows < b->n_tokens;
+  p.part_rows = p.by_seq ? most_rows : b->n_tokens;
   if (p.splits > 1) {
-    const size_t n = (size_t)b->n_tokens * d->n_heads * p.splits;
+    const size_t n = (size_t)p.part_rows * d->n_heads * p.splits;
     p.o_bytes = (n * d->head_dim * 4 + 255) & ~(size_t)255;
     p.bytes = p.o_bytes + n * 8;
   }
@@ -156,7 +161,7 @@ int32_t moe_kv_attention_workspace_bytes(const moe_kv_desc* desc, const moe_kv_b
   if (rc == MOE_OK) rc = kv_check_batch(desc, batch, false);
   if (rc != MOE_OK) return rc;
   size_t most = 0;
-  for (int32_t t : {MOE_F32, MOE_BF16}) {
+  for (int32_t t : {MOE_F32, MOE_BF16, MOE_F16}) {
     const size_t n = attn_plan(desc, batch, t).bytes;
     most = n > most ? n : most;
   }
@@ -205,6 +210,8 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
   a.group = make_divider(p.group);
   a.min_tiles = p.min_tiles;
   a.row_tiles = p.row_tiles;
+  a.by_seq = p.by_seq;
+  a.rows = make_divider(batch->max_rows);
   hipStream_t st = (hipStream_t)hip_stream;
   (void)hipGetLastError();
   switch (desc->head_dim) {
@@ -214,7 +221,7 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
     default: rc = launch_kv_attention<256>(a, dtype, p.row_tiles, (int)p.grid, st); break;
   }
   if (rc != MOE_OK || p.splits == 1) return rc;
-  const unsigned n = (unsigned)batch->n_tokens * (unsigned)desc->n_heads;
+  const unsigned n = (unsigned)p.part_rows * (unsigned)desc->n_heads;
   switch (desc->head_dim) {
     case 64: launch_kv_join<64>(a, dtype, n, st); break;
     case 128: launch_kv_join<128>(a, dtype, n, st); break;

@@ -257,6 +257,59 @@ def test_attention_over_uneven_sequences(seqs, heads, kv_heads, page, window):
     check_attention(lay, plan, plan.filled_cache(rng), "bf16", rng)
 
 
+@pytest.mark.parametrize("seqs,kv_heads,rows", [(40, 8, 20), (1100, 2, 9)])
+def test_attention_over_many_sequences_of_several_row_tiles(seqs, kv_heads, rows):
+    """Rows of uneven counts, one sequence of the most, with no split; too many sequences to look up."""
+    log(f"row tiles {seqs}")
+    rng = np.random.default_rng(seqs)
+    lay = ko.Layout(4 * kv_heads, kv_heads, 64, 16)
+    r = rng.integers(0, 4, seqs)
+    r[seqs // 3], r[-1] = rows, rows - 1
+    plan = Plan(lay, list(r), list(r + rng.integers(0, 30, seqs)), rng, pad_rows=1)
+    check_attention(lay, plan, plan.filled_cache(rng), "bf16", rng)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_of_a_padded_batch(dtype):
+    """Many rows of no sequence: the workspace is that of the sequences' rows."""
+    rng = np.random.default_rng(51)
+    lay = ko.Layout(8, 2, 64, 16)
+    plan = Plan(lay, [3, 1], [1500, 700], rng, pad_rows=200)
+    check_attention(lay, plan, plan.filled_cache(rng), dtype, rng)
+    d = desc_of(lay)
+    assert svr.moe_kv_attention_workspace_bytes(d, plan.batch(), 204) == \
+        svr.moe_kv_attention_workspace_bytes(d, plan.batch(), 3000)
+
+
+def test_attention_window_as_large_as_its_type():
+    rng = np.random.default_rng(52)
+    for window in (2 ** 31 - 1, 2 ** 30, 2 ** 20):
+        lay = ko.Layout(4, 2, 64, 16, window)
+        plan = Plan(lay, [6, 2], [3, 100], rng)  # three rows before place 0
+        check_attention(lay, plan, plan.filled_cache(rng), "f32", rng)
+
+
+def test_attention_makes_its_workspace_on_the_stream_of_the_call():
+    rng = np.random.default_rng(53)
+    lay = ko.Layout(8, 1, 64, 16)
+    plan = Plan(lay, [4], [2000], rng)
+    q, _ = rounded(rng.standard_normal((4, 8, 64)), "bf16")
+    d, batch, cache = desc_of(lay), plan.batch(), dev(plan.filled_cache(rng))
+    want = torch.empty_like(q)
+    svr.moe_kv_attention(d, batch, q, cache, want)
+    torch.cuda.synchronize()
+    side, n = torch.cuda.Stream(), svr.moe_kv_attention_workspace_bytes(d, batch, 4)
+    assert n > 0
+    outs = []
+    for _ in range(20):
+        out = torch.empty_like(q)
+        svr.moe_kv_attention(d, batch, q, cache, out, stream=side)
+        outs.append(out)
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xFF)  # what this stream may be given
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
 def test_attention_where_one_score_stands_out():
     """Peaked rows, and maxima that keep growing along the axis (every tile rescales)."""
     rng = np.random.default_rng(12)

@@ -195,3 +195,21 @@ def test_replayed_from_a_graph_after_verify_accept():
         step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (tok, lp, h, ids, tl))), i
+
+
+def test_workspace_made_on_the_stream_of_the_call():
+    rng = np.random.default_rng(61)
+    x = draw(rng, 2, 131072, "f32")
+    want = run(x, [5, 6], 5)
+    side = torch.cuda.Stream()
+    got, n = [], svr.moe_logprobs_workspace_bytes(2, 131072, 5)
+    t = dev(np.array([5, 6], np.int32))
+    for _ in range(20):
+        o = {k: torch.empty_like(v) for k, v in want.items()}
+        svr.moe_logprobs(x, t, stream=side, **o)
+        got.append(o)
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xFF)  # what this stream may be given
+    torch.cuda.synchronize()
+    for o in got:
+        for k, v in want.items():
+            assert torch.equal(o[k], v), k

@@ -266,3 +266,28 @@ def test_the_binding_refuses_what_it_cannot_pass_on():
                          ws=cache.view(-1))
     with pytest.raises(ValueError, match="device tensor"):
         svr.moe_logprobs(x, None, None, ws=cache.view(-1))
+
+
+def test_the_binding_refuses_numbers_that_ctypes_would_cut_off():
+    with pytest.raises(ValueError, match="window"):
+        svr.KvDesc(4, 2, 64, window=2 ** 32 + 5)
+    z = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="max_rows"):
+        svr.KvBatch(z, z[:1], z[None], 2 ** 32 + 1)
+
+
+def test_the_binding_refuses_a_batch_on_another_device():
+    """Its addresses would be read by the wrong device."""
+    d = svr.KvDesc(4, 2, 64, 16)
+    z = torch.zeros(2, dtype=torch.int32)
+    batch = svr.KvBatch(z, z[:1], z[None, :1], 1)
+    m = dict(device="meta")
+    q, k = torch.empty((1, 4, 64), **m), torch.empty((1, 2, 64), **m)
+    cache = torch.empty((1, 2, d.page_bytes), dtype=torch.uint8, **m)
+    f = torch.empty((1, 2, 64), **m)
+    ws = torch.empty(0, dtype=torch.uint8, **m)
+    for call in (lambda: svr.moe_kv_append(d, batch, q, k, k, cache, q),
+                 lambda: svr.moe_kv_attention(d, batch, q, cache, q, ws=ws),
+                 lambda: svr.moe_kv_read(d, batch, cache, f, f)):
+        with pytest.raises(ValueError, match="batch: expected tensors on meta"):
+            call()
