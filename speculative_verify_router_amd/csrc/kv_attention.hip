@@ -17,8 +17,11 @@ constexpr int kMaxSplits = 128;
 // with w_s = 2^(m_s - max m).  One workgroup a row and head; a slot of D/4
 // lanes reads a split's sums 16 bytes a lane, the slots take the splits in
 // turn.  Bound by latency, not bytes (a row's parts are at most 128 KB): the
-// first batch of every read is issued before it is known which splits are in
-// use (the workspace holds them all, what is not in use is dropped).
+// first kBatch of a slot's reads are issued before it is known which splits
+// are in use (the workspace holds them all, what is not in use is dropped):
+// all of them for a single sequence, where all are in use, and one for
+// several, which use few.  4 rows of 64 heads with 63 splits: 5.6 us (6.4 with
+// four); 70 rows of 32 heads: 7 us (7.5 with four).
 template <int D, int kBatch, typename T>
 __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a) {
   constexpr int L = D / 4, kSlots = kBlock / L;

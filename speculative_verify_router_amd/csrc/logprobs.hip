@@ -18,6 +18,13 @@
 //   Waves, then workgroups of a row are joined the same way; the last
 // workgroup to arrive at the row's counter joins them and returns the
 // counter to zero.
+//
+// Measured at 131072 columns: 512 rows of float 56 us (4.8 TB/s: the bytes),
+// of bf16 42 us (3.2 TB/s: about nine instructions a value), with five
+// alternatives 66 and 55 us; 4 rows of float 6 us, with 20 alternatives 14
+// (placing them and joining the workgroups); 1 row 5 us.  32 columns a lane
+// leave three waves a SIMD: 83 and 58 us; keys made again instead of held, and
+// eight waves a SIMD: 39 us in bf16, but 59 in float.
 #include <hip/hip_runtime.h>
 
 #include "common.h"
