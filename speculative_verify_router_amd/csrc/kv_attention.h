@@ -76,7 +76,9 @@ struct AttnArgs {
   Divider G, tiles, splits, heads, share, group, rows;
 };
 
-constexpr int kAttnWaves = 4;
+// Waves of a workgroup, and of one that makes parts of two row tiles: half as
+// many parts to write and join (see attn_plan).
+constexpr int kAttnWaves = 4, kAttnPartWaves = 8;
 constexpr int kAttnTile = 32;  // tokens of a wave's step
 constexpr int kWholeRange = 1 << 28;  // a split of any number of tiles
 
@@ -283,17 +285,18 @@ constexpr int attn_waves(int D, int RT, int NT) {
   return n <= 48 ? 4 : n <= 72 ? 3 : n <= 160 ? 2 : 1;
 }
 
-template <int D, int RT, int NT, typename T>
-__global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv_attention(AttnArgs a) {
+template <int D, int RT, int NT, int W, typename T>
+__global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attention(AttnArgs a) {
   constexpr int KS = D / 32, CB = D / 16;
   constexpr int kRowBytes = 2 * D + 16;            // a staged token: the pad spreads the banks
   constexpr int kStage = kAttnTile * kRowBytes;    // a wave's staged tokens
   constexpr int kJoinRow = D + 4;                  // floats of a joined row
-  constexpr int kJoin = kAttnWaves * 16 * kJoinRow * 4;
-  constexpr int kMem = kAttnWaves * kStage > kJoin ? kAttnWaves * kStage : kJoin;
+  constexpr int kJoin = W * 16 * kJoinRow * 4;
+  constexpr int kBehind = kJoin + 16 * W * 4;  // the last row's reads pass its end
+  constexpr int kMem = W * kStage > kBehind ? W * kStage : kBehind;
   __shared__ __attribute__((aligned(16))) uint8_t s_mem[kMem];
-  __shared__ float s_m[kAttnWaves][RT * 16];
-  __shared__ float2 s_ml[kAttnWaves][16];
+  __shared__ float s_m[W][RT * 16];
+  __shared__ float2 s_ml[W][16];
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -388,7 +391,7 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       page[u] = page_of(t, u);
-      next_page[u] = page_of(t + kAttnWaves, u);
+      next_page[u] = page_of(t + W, u);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) load_keys_or_values(t, u, page[u], 0, kc[u]);
@@ -439,7 +442,7 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
   }
   uint8_t* stage = s_mem + wv * kStage;
 
-  for (; t < t_end; t += kAttnWaves) {
+  for (; t < t_end; t += W) {
     const int tok0 = rg.tb + t * kAttnTile;
     bool gone[2];  // runs on a page that is not there
 #pragma unroll
@@ -463,7 +466,7 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
       }
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) load_keys_or_values(t + kAttnWaves, u, next_page[u], 0, kc[u]);
+    for (int u = 0; u < 2; ++u) load_keys_or_values(t + W, u, next_page[u], 0, kc[u]);
 
     // Values to shared memory, widened; the next ones are asked for.
 #pragma unroll
@@ -474,9 +477,9 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
             widen(vc[u].w[k], vc[u].scale(k));
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      load_keys_or_values(t + kAttnWaves, u, next_page[u], 1, vc[u]);
+      load_keys_or_values(t + W, u, next_page[u], 1, vc[u]);
       page[u] = next_page[u];
-      next_page[u] = page_of(t + 2 * kAttnWaves, u);
+      next_page[u] = page_of(t + 2 * W, u);
     }
 
     if (gone[0] || gone[1] || tok0 + kAttnTile - 1 > all_hi || tok0 < all_lo) {
@@ -556,12 +559,14 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
   }
   __syncthreads();  // also: every wave is done with its staged values
   float* join = reinterpret_cast<float*>(s_mem);
-  const int jr = threadIdx.x >> 4, jc = 4 * (threadIdx.x & 15);
+  constexpr int kJoinLanes = 4 * W, kSpan = 4 * kJoinLanes, kReads = (D + kSpan - 1) / kSpan;  // of a row
+  const int jr = threadIdx.x / kJoinLanes, jc = 4 * (threadIdx.x % kJoinLanes);
+  auto has = [&](int j) { return D % kSpan == 0 || jc + kSpan * j < D; };
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     float m = s_m[0][16 * rt + l16];
 #pragma unroll
-    for (int w = 1; w < kAttnWaves; ++w) m = fmaxf(m, s_m[w][16 * rt + l16]);
+    for (int w = 1; w < W; ++w) m = fmaxf(m, s_m[w][16 * rt + l16]);
     const float f = mx[rt] == m ? 1.f : __builtin_amdgcn_exp2f(mx[rt] - m);
     if (g == 0) s_ml[wv][l16] = make_float2(m, sum[rt] * f);
 #pragma unroll
@@ -572,13 +577,14 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
     if (r < row_total) {
       const float M = s_ml[0][jr].x;
       float L = 0.f;
-      f32x4v v[D / 64];
+      f32x4v v[kReads];
 #pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) {
+      for (int w = 0; w < W; ++w) {
         L += s_ml[w][jr].y;
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          const f32x4v x = *reinterpret_cast<f32x4v*>(join + (w * 16 + jr) * kJoinRow + jc + 64 * j);
+        for (int j = 0; j < kReads; ++j) {
+          // (What lies behind the row is read, and dropped.)
+          const f32x4v x = *reinterpret_cast<f32x4v*>(join + (w * 16 + jr) * kJoinRow + jc + kSpan * j);
           v[j] = w ? v[j] + x : x;
         }
       }
@@ -588,7 +594,8 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
         const float inv = L == 0.f ? 0.f : 1.f / L;
         T* out = (T*)a.out + at * D + jc;
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) store4(out + 64 * j, v[j] * inv);
+        for (int j = 0; j < kReads; ++j)
+          if (has(j)) store4(out + kSpan * j, v[j] * inv);
         if (jc == 0 && a.lse)
           a.lse[at] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.6931471805599453f;
       } else {
@@ -596,7 +603,8 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
         const int64_t pt = (row * a.kv.Hq + kvh * G + r - rm * G) * a.splits.d + split;
         float* part = a.part_o + pt * D + jc;
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) *reinterpret_cast<f32x4v*>(part + 64 * j) = v[j];
+        for (int j = 0; j < kReads; ++j)
+          if (has(j)) *reinterpret_cast<f32x4v*>(part + kSpan * j) = v[j];
         if (jc == 0) a.part_ml[pt] = make_float2(M, L);
       }
     }
@@ -605,12 +613,16 @@ __global__ __launch_bounds__(kAttnWaves* kWave, attn_waves(D, RT, NT)) void k_kv
 }
 
 template <int D>
-int32_t launch_kv_attention(const AttnArgs& a, int32_t dtype, int row_tiles, int grid, hipStream_t st);
+int32_t launch_kv_attention(const AttnArgs& a, int32_t dtype, int row_tiles, int waves, int grid,
+                            hipStream_t st);
 
 // The most row tiles (of 16) a workgroup of head size D and NT terms takes.
 constexpr int attn_most_row_tiles(int D, int NT) { return NT <= 2 && D <= 192 ? 2 : D <= 128 ? 2 : 1; }
 // Whole verify batches in one tile where they fit: every key is widened once
 // for all rows of the tile.
+// Whether a workgroup that makes parts has kAttnPartWaves: where they leave
+// the waves of a SIMD as they are.
+constexpr bool attn_part_waves(int D, int RT, int NT) { return RT == 2 && attn_waves(D, RT, NT) >= 2; }
 inline int attn_terms(int32_t dtype) { return dtype == MOE_BF16 ? 1 : dtype == MOE_F16 ? 2 : 3; }
 inline int attn_row_tiles(int64_t rows, int D, int32_t dtype) {
   return rows <= 16 ? 1 : attn_most_row_tiles(D, attn_terms(dtype));

@@ -4,10 +4,10 @@
 
 namespace svr {
 
-extern template int32_t launch_kv_attention<64>(const AttnArgs&, int32_t, int, int, hipStream_t);
-extern template int32_t launch_kv_attention<128>(const AttnArgs&, int32_t, int, int, hipStream_t);
-extern template int32_t launch_kv_attention<192>(const AttnArgs&, int32_t, int, int, hipStream_t);
-extern template int32_t launch_kv_attention<256>(const AttnArgs&, int32_t, int, int, hipStream_t);
+extern template int32_t launch_kv_attention<64>(const AttnArgs&, int32_t, int, int, int, hipStream_t);
+extern template int32_t launch_kv_attention<128>(const AttnArgs&, int32_t, int, int, int, hipStream_t);
+extern template int32_t launch_kv_attention<192>(const AttnArgs&, int32_t, int, int, int, hipStream_t);
+extern template int32_t launch_kv_attention<256>(const AttnArgs&, int32_t, int, int, int, hipStream_t);
 
 namespace {
 
@@ -106,25 +106,20 @@ void launch_kv_join(const AttnArgs& a, int32_t dtype, unsigned n, hipStream_t st
 
 // How a batch is cut, as far as its sizes say (the lengths are on the device).
 struct AttnPlan {
-  int row_tiles, tiles, splits, min_tiles, share, group, by_seq;
+  int row_tiles, tiles, waves, splits, min_tiles, share, group, by_seq;
   int64_t part_rows;
   int64_t grid;
   size_t o_bytes, bytes;
 };
 
-AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
-  AttnPlan p{};
-  const int G = d->n_heads / d->n_kv_heads;
-  const int64_t rows = (int64_t)(b->max_rows < b->n_tokens ? b->max_rows : b->n_tokens) * G;
-  p.row_tiles = attn_row_tiles(rows, d->head_dim, dtype);
-  const int span = 16 * p.row_tiles;
-  p.tiles = (int)((rows + span - 1) / span);
-  p.min_tiles = kAttnWaves;  // a tile a wave
-  // Work of a head that runs at once, and its row tiles at most.
-  const int slots = 256 * attn_waves(d->head_dim, p.row_tiles, attn_terms(dtype)) / d->n_kv_heads;
-  int64_t all = (int64_t)b->n_seqs * p.tiles;
-  const int64_t dense = ((int64_t)b->n_tokens * G + span - 1) / span + b->n_seqs;
-  all = all < dense ? all : dense;
+// The plan for workgroups of p.waves: the splits of `all` row tiles of a head.
+// Returns whether row tiles are few, and tables long, enough for four splits
+// or more and as many as there is room for.
+bool attn_split(AttnPlan& p, const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype, int64_t all) {
+  p.min_tiles = p.waves;  // a tile a wave
+  // Work of a head that runs at once.
+  const int resident = attn_waves(d->head_dim, p.row_tiles, attn_terms(dtype)) * kAttnWaves / p.waves;
+  const int slots = 256 * resident / d->n_kv_heads;
   // Every sequence's last split is half full on the average.
   p.share = (int)(slots - all / 2 > slots / 2 ? slots - all / 2 : slots / 2);
   p.share = p.share > 0 ? p.share : 1;
@@ -135,6 +130,29 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   int64_t s = 2 * all > slots ? 1 : b->n_seqs == 1 ? slots / all : (4 * slots + all - 1) / all;
   s = s > kMaxSplits ? kMaxSplits : s;
   p.splits = (int)(s < most ? s : most);
+  return slots / all >= 4 && s <= most;
+}
+
+AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
+  AttnPlan p{};
+  if (b->n_seqs == 0 || b->n_tokens == 0 || b->max_rows == 0) return p;
+  const int G = d->n_heads / d->n_kv_heads;
+  const int64_t rows = (int64_t)(b->max_rows < b->n_tokens ? b->max_rows : b->n_tokens) * G;
+  p.row_tiles = attn_row_tiles(rows, d->head_dim, dtype);
+  const int span = 16 * p.row_tiles;
+  p.tiles = (int)((rows + span - 1) / span);
+  int64_t all = (int64_t)b->n_seqs * p.tiles;
+  const int64_t dense = ((int64_t)b->n_tokens * G + span - 1) / span + b->n_seqs;
+  all = all < dense ? all : dense;
+  // Larger workgroups make fewer parts: 4 rows over 60000 tokens 32.0 us (34.4
+  // with four waves), 15000 tokens 20.4 (21.5); but a part of 64 rows over
+  // 16384, of which there are two, takes 106 us (96), 4 rows over 4000 tokens
+  // 15.9 (15.0).
+  p.waves = kAttnPartWaves;
+  if (!attn_part_waves(d->head_dim, p.row_tiles, attn_terms(dtype)) || !attn_split(p, d, b, dtype, all)) {
+    p.waves = kAttnWaves;
+    attn_split(p, d, b, dtype, all);
+  }
   p.group = p.tiles < 64 ? p.tiles : 64;
   const int64_t list = !kv_listed(b->n_seqs, p.tiles, p.splits) ? (int64_t)b->n_seqs * p.splits * p.tiles
                        : p.splits == 1 ? all : p.share + all;
@@ -218,10 +236,10 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
   hipStream_t st = (hipStream_t)hip_stream;
   (void)hipGetLastError();
   switch (desc->head_dim) {
-    case 64: rc = launch_kv_attention<64>(a, dtype, p.row_tiles, (int)p.grid, st); break;
-    case 128: rc = launch_kv_attention<128>(a, dtype, p.row_tiles, (int)p.grid, st); break;
-    case 192: rc = launch_kv_attention<192>(a, dtype, p.row_tiles, (int)p.grid, st); break;
-    default: rc = launch_kv_attention<256>(a, dtype, p.row_tiles, (int)p.grid, st); break;
+    case 64: rc = launch_kv_attention<64>(a, dtype, p.row_tiles, p.waves, (int)p.grid, st); break;
+    case 128: rc = launch_kv_attention<128>(a, dtype, p.row_tiles, p.waves, (int)p.grid, st); break;
+    case 192: rc = launch_kv_attention<192>(a, dtype, p.row_tiles, p.waves, (int)p.grid, st); break;
+    default: rc = launch_kv_attention<256>(a, dtype, p.row_tiles, p.waves, (int)p.grid, st); break;
   }
   if (rc != MOE_OK || p.splits == 1) return rc;
   const unsigned n = (unsigned)p.part_rows * (unsigned)desc->n_heads;

@@ -2,5 +2,5 @@
 #include "launch_attention.h"
 
 namespace svr {
-template int32_t launch_kv_attention<256>(const AttnArgs&, int32_t, int, int, hipStream_t);
+template int32_t launch_kv_attention<256>(const AttnArgs&, int32_t, int, int, int, hipStream_t);
 }  // namespace svr

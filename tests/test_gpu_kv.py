@@ -241,6 +241,18 @@ def test_attention_over_many_tokens(dtype, dim):
     check_attention(lay, plan, plan.filled_cache(rng), dtype, rng)
 
 
+@pytest.mark.parametrize("dtype,dim", [("bf16", 64), ("f32", 64), ("f16", 64), ("bf16", 128), ("f16", 128),
+                                       ("f32", 128), ("bf16", 192), ("f16", 192), ("f32", 192)])
+@pytest.mark.parametrize("lens", [[2900], [1800, 333]])
+def test_attention_of_a_verify_batch_in_a_long_table(dtype, dim, lens):
+    """Tables that room for any length makes long: parts by the largest workgroups, most of them not in use."""
+    log(f"long table {dtype} D={dim} {lens}")
+    rng = np.random.default_rng(dim + len(lens))
+    lay = ko.Layout(10, 1, dim, 64)
+    plan = Plan(lay, [4] * len(lens), lens, rng, width=700)
+    check_attention(lay, plan, plan.filled_cache(rng), dtype, rng)
+
+
 @pytest.mark.parametrize("seqs,heads,kv_heads,page,window", [(2, 8, 2, 16, 0), (64, 4, 2, 32, 0), (65, 6, 3, 16, 0),
                                                              (150, 2, 1, 16, 0), (70, 3, 1, 16, 120)])
 def test_attention_over_uneven_sequences(seqs, heads, kv_heads, page, window):

@@ -291,3 +291,11 @@ def test_the_binding_refuses_a_batch_on_another_device():
                  lambda: svr.moe_kv_read(d, batch, cache, f, f)):
         with pytest.raises(ValueError, match="batch: expected tensors on meta"):
             call()
+
+
+@pytest.mark.parametrize("seqs,rows,max_rows", [(0, 0, 1), (0, 3, 1), (2, 0, 1), (2, 5, 0), (1, 5, 0)])
+def test_attention_of_nothing_needs_no_workspace(seqs, rows, max_rows):
+    i32 = dict(dtype=torch.int32)
+    batch = svr.KvBatch(torch.zeros(seqs + 1, **i32), torch.zeros(seqs, **i32),
+                        torch.zeros((seqs, 9), **i32), max_rows)
+    assert svr.moe_kv_attention_workspace_bytes(kv_desc(), batch, rows) == 0
