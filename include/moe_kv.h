@@ -117,9 +117,11 @@ int32_t moe_kv_append(const moe_kv_desc* desc, const moe_kv_batch* batch, int32_
 /* Device workspace, in *bytes, of moe_kv_attention for this desc and the
  * sizes of this batch (the arrays may be NULL).  Other sizes need their own,
  * and smaller ones may need more (fewer rows are cut into more parts): for a
- * range of sizes, take the largest.  The workspace needs no
- * initialisation; calls that share one must not overlap in time.  0 is
- * possible, and then workspace may be NULL. */
+ * range of sizes, take the largest.  It begins with 16384 bytes of counters,
+ * which must be zero before the first call that uses the workspace; every call
+ * leaves them zero, so zero-fill a workspace once when it is allocated.  Calls
+ * that share one must not overlap in time.  0 is possible, and then workspace
+ * may be NULL. */
 int32_t moe_kv_attention_workspace_bytes(const moe_kv_desc* desc, const moe_kv_batch* batch,
                                          size_t* bytes);
 

@@ -369,6 +369,7 @@ def moe_verify_accept(logits: torch.Tensor, drafts: Optional[torch.Tensor], toke
 BF16, F16 = 6, 7
 _ACT_DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 KV_ROTARY_INTERLEAVED = 1
+KV_COUNTER_BYTES = 16384
 
 
 def _act_dtype(t: torch.Tensor) -> int:
@@ -567,9 +568,12 @@ def moe_kv_attention_workspace_bytes(desc: KvDesc, batch: KvBatch, n_tokens: int
 
 
 def kv_workspace(desc: KvDesc, batch: KvBatch, n_tokens: int) -> torch.Tensor:
-    """A device workspace for moe_kv_attention on batches of this size (n_tokens rows)."""
-    return torch.empty(moe_kv_attention_workspace_bytes(desc, batch, n_tokens), dtype=torch.uint8,
-                       device=batch.page_table.device)
+    """A device workspace for moe_kv_attention on batches of this size (n_tokens rows), its
+    counters zeroed (calls keep them so)."""
+    ws = torch.empty(moe_kv_attention_workspace_bytes(desc, batch, n_tokens), dtype=torch.uint8,
+                     device=batch.page_table.device)
+    ws[:KV_COUNTER_BYTES].zero_()
+    return ws
 
 
 def moe_kv_attention(desc: KvDesc, batch: KvBatch, q: torch.Tensor, cache: torch.Tensor,

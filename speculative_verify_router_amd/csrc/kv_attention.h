@@ -68,6 +68,7 @@ struct AttnArgs {
   // as b * max_rows + m where those are fewer (a padded batch).
   float* part_o;
   float2* part_ml;
+  unsigned* ctr;  // [sequence][row tile][key/value head] parts made, or NULL: a second kernel joins
   float c;         // scale * log2(e)
   int row_tiles, min_tiles, by_seq;
   // Query heads a key/value head; row tiles of a sequence; splits at most;
@@ -80,6 +81,11 @@ struct AttnArgs {
 // many parts to write and join (see attn_plan).
 constexpr int kAttnWaves = 4, kAttnPartWaves = 8;
 constexpr int kAttnTile = 32;  // tokens of a wave's step
+// Up to so many parts the workgroup that makes the last one joins them: a
+// second launch costs 4 us, and a workgroup reads 32 rows of sixteen parts
+// (393 KB at D = 192) in about as much.
+constexpr int kJoinHere = 16;
+constexpr int kAttnCounters = 4096;
 constexpr int kWholeRange = 1 << 28;  // a split of any number of tiles
 
 // A sequence's rows as the kernels use them.
@@ -109,6 +115,33 @@ __device__ __forceinline__ int wave_scan(int v) {
   join(__builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));  // rows 0, 2 to 1, 3
   join(__builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));  // lane 31 to the upper half
   return v;
+}
+
+// Over the sixteen lanes of a row of lanes, in each of them.
+__device__ __forceinline__ float row16_max(float v) {
+  v = fmaxf(v, dpp<0xB1>(-INFINITY, v));
+  v = fmaxf(v, dpp<0x4E>(-INFINITY, v));
+  v = fmaxf(v, dpp<0x141>(-INFINITY, v));
+  return fmaxf(v, dpp<0x140>(-INFINITY, v));
+}
+__device__ __forceinline__ float row16_sum(float v) {
+  v += dpp<0xB1>(0.f, v);
+  v += dpp<0x4E>(0.f, v);
+  v += dpp<0x141>(0.f, v);
+  return v + dpp<0x140>(0.f, v);
+}
+
+// Parts that another workgroup reads in the same launch.
+__device__ __forceinline__ void store_part(float* p, const f32x4v& v) {
+  struct Two { uint64_t a, b; };
+  const Two x = __builtin_bit_cast(Two, v);
+  store_shared<uint64_t>(reinterpret_cast<uint64_t*>(p), x.a);
+  store_shared<uint64_t>(reinterpret_cast<uint64_t*>(p) + 1, x.b);
+}
+__device__ __forceinline__ f32x4v load_part(const float* p) {
+  struct { uint64_t a, b; } x{load_shared(reinterpret_cast<const uint64_t*>(p)),
+                              load_shared(reinterpret_cast<const uint64_t*>(p) + 1)};
+  return __builtin_bit_cast(f32x4v, x);
 }
 
 // How the tokens of a batch are cut: a split is `per` tiles, the same for
@@ -170,7 +203,8 @@ __device__ __forceinline__ int kv_per(const AttnArgs& a, const KvRows& s) {
   // Rounded up, by the bits that the divider takes.
   const int shift = max(0, 34 - (int)__builtin_clzll(all | 1));
   const int64_t fair = (int64_t)(a.share.of((int)(all >> shift) + a.share.d - 1) + (shift ? 1 : 0)) << shift;
-  return max(a.min_tiles, max((int)min(fair, (int64_t)kWholeRange), a.splits.of(most + a.splits.d - 1)));
+  const int per = max(a.min_tiles, max((int)min(fair, (int64_t)kWholeRange), a.splits.of(most + a.splits.d - 1)));
+  return most <= 3 * a.min_tiles ? max(per, most) : per;  // four rounds of the waves take as long as joining
 }
 
 // The tokens [beg, end) that rows of places [first, last] see, in tiles from
@@ -604,11 +638,75 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
         float* part = a.part_o + pt * D + jc;
 #pragma unroll
         for (int j = 0; j < kReads; ++j)
-          if (has(j)) *reinterpret_cast<f32x4v*>(part + kSpan * j) = v[j];
-        if (jc == 0) a.part_ml[pt] = make_float2(M, L);
+          if (has(j)) {
+            if (a.ctr) store_part(part + kSpan * j, v[j]);
+            else *reinterpret_cast<f32x4v*>(part + kSpan * j) = v[j];
+          }
+        if (jc == 0) {
+          const float2 ml = make_float2(M, L);
+          if (a.ctr) store_shared<uint64_t>((uint64_t*)a.part_ml + pt, __builtin_bit_cast(uint64_t, ml));
+          else a.part_ml[pt] = ml;
+        }
       }
     }
     if (rt + 1 < RT) __syncthreads();
+  }
+  if (rg.whole() || !a.ctr) return;
+
+  // The last workgroup of the row tiles joins the parts:
+  // out = sum_s w_s O_s / sum_s w_s l_s with w_s = 2^(m_s - max m).
+  wait_stores();
+  __syncthreads();
+  bool* s_last = reinterpret_cast<bool*>(s_ml);
+  const int used = (int)((unsigned)(rg.ntile + per - 1) / (unsigned)per);
+  unsigned* ctr = a.ctr + ((int64_t)b * a.tiles.d + tile) * a.kv.Hk + kvh;
+  if (threadIdx.x == 0) *s_last = arrive(ctr) == (unsigned)(used - 1);
+  __syncthreads();
+  if (!*s_last) return;
+  if (threadIdx.x == 0) store_shared(ctr, 0u);
+  // Where row r of the tile has its parts and its output.
+  auto places = [&](int r, int64_t& pt, int64_t& to) {
+    const int rm = a.G.of(r), h = kvh * G + r - rm * G;
+    to = (int64_t)(sq.off + rm) * a.kv.Hq + h;
+    pt = (a.by_seq ? ((int64_t)b * a.kv.max_rows + rm) * a.kv.Hq + h : to) * a.splits.d;
+  };
+  float* s_w = join;  // [row][part]: w_s / sum
+  for (int n = threadIdx.x; n < RT * 16 * kJoinHere; n += W * kWave) {
+    static_assert(kJoinHere == 16, "a row's parts are a row of lanes");
+    const int row = n / kJoinHere, part = n % kJoinHere;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    int64_t at = 0, lse_at = 0;
+    const bool on = r0 + row < row_total;
+    if (on) {
+      places(r0 + row, at, lse_at);
+      if (part < used) ml = __builtin_bit_cast(float2, load_shared((const uint64_t*)a.part_ml + at + part));
+    }
+    const float M = row16_max(ml.x), w = ml.x == M ? 1.f : __builtin_amdgcn_exp2f(ml.x - M);
+    const float L = row16_sum(w * ml.y);
+    s_w[n] = L == 0.f ? 0.f : w / L;
+    if (on && part == 0 && a.lse)
+      a.lse[lse_at] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.6931471805599453f;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int row = 16 * rt + jr;
+    if (r0 + row >= row_total) continue;
+    int64_t pt, to;
+    places(r0 + row, pt, to);
+    f32x4v v[kReads];
+#pragma unroll
+    for (int j = 0; j < kReads; ++j) v[j] = f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int part = 0; part < used; ++part) {
+      const float w = s_w[row * kJoinHere + part];
+#pragma unroll
+      for (int j = 0; j < kReads; ++j)
+        if (has(j)) v[j] += w * load_part(a.part_o + (pt + part) * D + jc + kSpan * j);
+    }
+#pragma unroll
+    for (int j = 0; j < kReads; ++j)
+      if (has(j)) store4((T*)a.out + to * D + jc + kSpan * j, v[j]);
   }
 }
 

@@ -107,6 +107,7 @@ void launch_kv_join(const AttnArgs& a, int32_t dtype, unsigned n, hipStream_t st
 // How a batch is cut, as far as its sizes say (the lengths are on the device).
 struct AttnPlan {
   int row_tiles, tiles, waves, splits, min_tiles, share, group, by_seq;
+  bool join_here;
   int64_t part_rows;
   int64_t grid;
   size_t o_bytes, bytes;
@@ -163,7 +164,8 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   if (p.splits > 1) {
     const size_t n = (size_t)p.part_rows * d->n_heads * p.splits;
     p.o_bytes = (n * d->head_dim * 4 + 255) & ~(size_t)255;
-    p.bytes = p.o_bytes + n * 8;
+    p.bytes = kAttnCounters * sizeof(unsigned) + p.o_bytes + n * 8;
+    p.join_here = p.splits <= kJoinHere && (int64_t)b->n_seqs * p.tiles * d->n_kv_heads <= kAttnCounters;
   }
   return p;
 }
@@ -220,8 +222,9 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
   a.cache = (const uint8_t*)cache;
   a.out = out;
   a.lse = lse;
-  a.part_o = (float*)workspace;
-  a.part_ml = (float2*)((uint8_t*)workspace + p.o_bytes);
+  a.ctr = p.join_here ? (unsigned*)workspace : nullptr;
+  a.part_o = (float*)workspace + kAttnCounters;
+  a.part_ml = (float2*)((uint8_t*)a.part_o + p.o_bytes);
   a.c = (desc->scale > 0.f ? desc->scale : 1.f / sqrtf((float)desc->head_dim)) * 1.4426950408889634f;
   a.G = make_divider(desc->n_heads / desc->n_kv_heads);
   a.tiles = make_divider(p.tiles);
@@ -241,7 +244,7 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
     case 192: rc = launch_kv_attention<192>(a, dtype, p.row_tiles, p.waves, (int)p.grid, st); break;
     default: rc = launch_kv_attention<256>(a, dtype, p.row_tiles, p.waves, (int)p.grid, st); break;
   }
-  if (rc != MOE_OK || p.splits == 1) return rc;
+  if (rc != MOE_OK || p.splits == 1 || p.join_here) return rc;
   const unsigned n = (unsigned)p.part_rows * (unsigned)desc->n_heads;
   switch (desc->head_dim) {
     case 64: launch_kv_join<64>(a, dtype, n, st); break;

@@ -253,6 +253,34 @@ def test_attention_of_a_verify_batch_in_a_long_table(dtype, dim, lens):
     check_attention(lay, plan, plan.filled_cache(rng), dtype, rng)
 
 
+def test_attention_calls_of_all_kinds_on_one_workspace():
+    """Parts joined by the last workgroup or by a second kernel, in turn: every call leaves the counters zero."""
+    rng = np.random.default_rng(54)
+    cases = []
+    for lay, rows, lens, dtype, width in (
+            (ko.Layout(8, 1, 192, 16), [1], [900], "bf16", None), (ko.Layout(8, 2, 64, 16), [4, 2], [700, 90], "f32", 400),
+            (ko.Layout(16, 2, 128, 32), [2] * 30, list(range(2, 32 * 40, 42))[:30], "f16", None),
+            (ko.Layout(32, 2, 64, 16), [4], [600], "bf16", 3000)):
+        plan = Plan(lay, rows, lens, rng, width=width)
+        q, _ = rounded(rng.standard_normal((plan.T, lay.heads, lay.dim)), dtype)
+        cases.append((desc_of(lay), plan.batch(), q, dev(plan.filled_cache(rng))))
+    n = [svr.moe_kv_attention_workspace_bytes(d, b, len(q)) for d, b, q, _ in cases]
+    assert all(n)
+    ws = torch.full((max(n),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:16384].zero_()
+    want = []
+    for d, b, q, c in cases:
+        out = torch.empty_like(q)
+        svr.moe_kv_attention(d, b, q, c, out)
+        want.append(out)
+    for i in (0, 1, 2, 3, 2, 0, 0, 3, 1, 2):
+        d, b, q, c = cases[i]
+        out = torch.full_like(q, float("nan"))
+        svr.moe_kv_attention(d, b, q, c, out, ws=ws)
+        assert torch.equal(out, want[i]), i
+        assert not ws[:16384].any(), i
+
+
 @pytest.mark.parametrize("seqs,heads,kv_heads,page,window", [(2, 8, 2, 16, 0), (64, 4, 2, 32, 0), (65, 6, 3, 16, 0),
                                                              (150, 2, 1, 16, 0), (70, 3, 1, 16, 120)])
 def test_attention_over_uneven_sequences(seqs, heads, kv_heads, page, window):
