@@ -3,27 +3,31 @@
 //
 // A unit is one head vector: a query head, or a key head with its value head
 // (together, so that a NaN or infinity in either marks the token).  A group
-// of LG lanes takes a unit, eight channels a lane: 16 bytes of a 16-bit type,
-// a 4-bit block of 32 channels is four lanes, and a lane's codes are one
-// dword.  The pair of a rotated channel is in the same lane (neighbours), or
-// is read from memory once more, which the cache answers.
+// of lanes takes a unit: eight channels a lane of a query (16 bytes of a
+// 16-bit type), four of a key, whose 64-bit arithmetic then fits in few
+// registers and is spread over a token's waves evenly; a 4-bit block of 32
+// channels is eight of its lanes, and two lanes' codes are a dword.  The pair
+// of a rotated channel is in the same lane (neighbours), or is read from
+// memory once more, which the cache answers.
 //
 // The pass is to be bound by its bytes: each of q, k, v is read once, q_out
 // and the codes written once.  A workgroup serves one token: the angles
 // (64-bit: at place 60000 a 32-bit angle is off by 2^-9) and the norms'
 // weights go into tables of factors in shared memory, once for all its heads,
 // which leaves a query's channel two products, a sum and its share of the
-// norm; the first heads are asked for before anything else.  Queries are
-// normed and rotated in 32 bits, keys in 64, because a code is a whole number
-// and a key next to a rounding border must fall on its own side whatever the
-// order of the sum.
+// norm; the first heads and the weights are asked for before anything else.
+// Queries are normed and rotated in 32 bits, keys in 64, because a code is a
+// whole number and a key next to a rounding border must fall on its own side
+// whatever the order of the sum.
 //
-// Measured with 64 query and 4 key/value heads of 192 channels: 31 us for
-// 1878 tokens in bf16 (98 MB, 3.2 TB/s), 15.5 us for 512 in float (52 MB,
-// 3.4 TB/s), 5 us for 4, of which the reads one after another (offsets, page,
-// heads) are most.  Angles taken anew for every head: 91 and 34 us; factors
-// in registers and one step ahead, whose copies waited for the stores: 50 and
-// 26.  Four steps at once leave three waves a SIMD: 33 and 20.
+// Measured with 64 query and 4 key/value heads of 192 channels: 1878 tokens in
+// bf16 (98 MB) 26 us, 31 from beyond the last cache, 20 without norms and
+// rotation; 512 tokens in float (52 MB) 15 us; 4 tokens 4.3 us, of which the
+// reads one after another (offsets, page, heads) are most.  Angles taken anew
+// for every head: 91, 34 and 8 us; factors in registers and one step ahead,
+// whose copies waited for the stores: 50 and 26; eight channels of a key a
+// lane: 127 registers instead of 81, 4.9 us for 4 tokens; two workgroups a
+// token: 38 us.
 #include "kv.h"
 
 namespace svr {
@@ -39,13 +43,12 @@ struct AppendArgs {
   void* q_out;
   float eps;
   int rotary, interleaved;
-  int parts, steps, steps_per_part;  // workgroups of a token; waves' steps
+  int parts, k_steps, steps, steps_per_part;  // workgroups of a token; waves' steps, keys first
 };
 
-template <int D>
-struct Group {
-  static constexpr int kLanes = D <= 64 ? 8 : D <= 128 ? 16 : 32;  // lanes of a unit
-};
+// Lanes of a query head, eight channels each, and of a key/value head, four.
+constexpr int query_lanes(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
+constexpr int key_lanes(int D) { return 2 * query_lanes(D); }
 
 // Sum over the LG lanes of a unit, in each of them.
 template <int LG>
@@ -58,10 +61,19 @@ __device__ __forceinline__ float group_sum(float v) {
   if (LG >= 32) v += __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(__builtin_bit_cast(int, v), 0x401F));
   return v;
 }
+template <int CTRL>
+__device__ __forceinline__ double dpp_double(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp_u<CTRL>(0u, (uint32_t)(u >> 32)) << 32 | dpp_u<CTRL>(0u, (uint32_t)u));
+}
 template <int LG>
 __device__ __forceinline__ double group_sum(double v) {
+  v += dpp_double<0xB1>(v);
+  v += dpp_double<0x4E>(v);
+  v += dpp_double<0x141>(v);
+  v += dpp_double<0x140>(v);
 #pragma unroll
-  for (int m = 1; m < LG; m <<= 1) v += __shfl_xor(v, m, kWave);
+  for (int m = 16; m < LG; m <<= 1) v += __shfl_xor(v, m, kWave);
   return v;
 }
 
@@ -74,32 +86,39 @@ struct Tables {
   double ka[D], kb[D];
   float qa[D], qb[D];
 };
-// The pair j of a token at pos; the channels that are not turned have A = w
-// and B = 0.
-template <int D>
-__device__ __forceinline__ void fill_tables(Tables<D>& t, const AppendArgs& a, int j, double pos, bool keys,
-                                            bool queries) {
-  const int half = a.rotary / 2;
-  const bool turned = j < half;
-  const int c1 = turned && !a.interleaved ? j : 2 * j, c2 = turned && !a.interleaved ? j + half : 2 * j + 1;
-  const bool kn = keys && a.k_norm, qn = queries && a.q_norm;
-  const float k1 = kn ? a.k_norm[c1] : 1.f, k2 = kn ? a.k_norm[c2] : 1.f;
-  const float q1 = qn ? a.q_norm[c1] : 1.f, q2 = qn ? a.q_norm[c2] : 1.f;
-  double sn = 0.0, cn = 1.0;
-  if (turned) sincos(pos * (double)a.inv_freq[j], &sn, &cn);
-  if (keys) {
-    t.ka[c1] = k1 * cn;
-    t.ka[c2] = k2 * cn;
-    t.kb[c1] = -(k2 * sn);
-    t.kb[c2] = k1 * sn;
+// Pair j of a token's channels; those that are not turned have A = w, B = 0.
+struct Pair {
+  int c1, c2;
+  float k1, k2, q1, q2, freq;
+
+  __device__ __forceinline__ Pair(const AppendArgs& a, int j) {
+    const int half = a.rotary / 2;
+    const bool turned = j < half;
+    c1 = turned && !a.interleaved ? j : 2 * j;
+    c2 = turned && !a.interleaved ? j + half : 2 * j + 1;
+    k1 = k2 = q1 = q2 = 1.f;
+    if (a.k_norm) k1 = a.k_norm[c1], k2 = a.k_norm[c2];
+    if (a.q_norm) q1 = a.q_norm[c1], q2 = a.q_norm[c2];
+    freq = turned ? a.inv_freq[j] : 0.f;
   }
-  if (queries) {
-    t.qa[c1] = (float)(q1 * cn);
-    t.qa[c2] = (float)(q2 * cn);
-    t.qb[c1] = (float)-(q2 * sn);
-    t.qb[c2] = (float)(q1 * sn);
+  template <int D>
+  __device__ __forceinline__ void fill(Tables<D>& t, double pos, bool keys, bool queries) const {
+    double sn = 0.0, cn = 1.0;
+    if (freq != 0.f) sincos(pos * (double)freq, &sn, &cn);
+    if (keys) {
+      t.ka[c1] = k1 * cn;
+      t.ka[c2] = k2 * cn;
+      t.kb[c1] = -(k2 * sn);
+      t.kb[c2] = k1 * sn;
+    }
+    if (queries) {
+      t.qa[c1] = (float)(q1 * cn);
+      t.qa[c2] = (float)(q2 * cn);
+      t.qb[c1] = (float)-(q2 * sn);
+      t.qb[c2] = (float)(q1 * sn);
+    }
   }
-}
+};
 __device__ __forceinline__ float norm_factor(float mean) {
   // The instruction (1 ulp) takes subnormal numbers for zeros.
   const bool tiny = mean < 1e-30f;
@@ -107,20 +126,18 @@ __device__ __forceinline__ float norm_factor(float mean) {
   return tiny ? r * 0x1p50f : r;
 }
 
-// The codes of eight floats over 2^e, by the conversion instruction: the
+// The codes of four floats over 2^e, by the conversion instruction: the
 // nearest code, the even one between two, at most 6 in size.
-__device__ __forceinline__ uint32_t codes8(const float (&x)[8], int e) {
+__device__ __forceinline__ uint32_t codes4(const float (&x)[4], int e) {
   const float scale = __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
-  uint32_t w = 0;
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], scale, 0);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], scale, 1);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], scale, 2);
-  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], scale, 3);
+  const uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, x[0], x[1], scale, 0);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], scale, 1);
 }
-// The largest m of the four lanes of a block.
+// The largest m of the eight lanes of a block.
 __device__ __forceinline__ uint32_t block_max(uint32_t m) {
   m = max(m, dpp_u<0xB1>(0u, m));
-  return max(m, dpp_u<0x4E>(0u, m));
+  m = max(m, dpp_u<0x4E>(0u, m));
+  return max(m, dpp_u<0x141>(0u, m));
 }
 // Least E in [-126, 125] with amax <= 7 * 2^E (0 for amax == 0): with
 // amax = f * 2^x, 1 <= f < 2, that is x - 2 for f <= 7/4 and x - 1 above.
@@ -128,29 +145,29 @@ __device__ __forceinline__ int block_exponent(bool zero, int x, bool above) {
   return zero ? 0 : min(max(x - 2 + (above ? 1 : 0), -126), 125);
 }
 
-// Eight values as one dword of codes, and the scale byte of their block of 32.
-__device__ __forceinline__ uint32_t quantise8(const float (&v)[8], uint32_t& scale) {
+// Four values as 16 bits of codes, and the scale byte of their block of 32.
+__device__ __forceinline__ uint32_t quantise4(const float (&v)[4], uint32_t& scale) {
   uint32_t m = 0;
-  float x[8];
+  float x[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     x[i] = v[i] + 0.f;  // no -0, whose code has no sign
     m = max(m, __builtin_bit_cast(uint32_t, x[i]) & 0x7FFFFFFFu);
   }
   m = block_max(m);
   const int e = block_exponent(m == 0, (int)(m >> 23) - 127, (m & 0x7FFFFFu) > 0x600000u);
   scale = (uint32_t)(e + 127);
-  return codes8(x, e);
+  return codes4(x, e);
 }
 // The same of 64-bit values, exactly: of a value's lower 32 bits it matters
 // only whether there are any (the borders have at most three bits), so that a
 // float of value / 2^e with that in its last bit falls on the same side of
 // every border.
-__device__ __forceinline__ uint32_t quantise8(const double (&v)[8], uint32_t& scale) {
-  uint32_t h[8], m = 0;  // the upper 31 bits without the sign, then "and more"
-  float x[8];
+__device__ __forceinline__ uint32_t quantise4(const double (&v)[4], uint32_t& scale) {
+  uint32_t h[4], m = 0;  // the upper 31 bits without the sign, then "and more"
+  float x[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v[i]);
     h[i] = (uint32_t)(b >> 32) << 1 | ((uint32_t)b ? 1u : 0u);
     m = max(m, h[i]);
@@ -159,20 +176,20 @@ __device__ __forceinline__ uint32_t quantise8(const double (&v)[8], uint32_t& sc
   const int e = block_exponent(m == 0, (int)(m >> 21) - 1023, (m & 0x1FFFFFu) > 0x180000u);
   scale = (uint32_t)(e + 127);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     // 896 + e: from the exponent's offset of 1023 to 127, over 2^e.
     const int r = min(max((int)(h[i] >> 1) - ((896 + e) << 20), 0), (255 << 20) - 1);
     const uint32_t sign = h[i] ? (uint32_t)(__builtin_bit_cast(uint64_t, v[i]) >> 32) & 0x80000000u : 0u;
     x[i] = __builtin_bit_cast(float, (uint32_t)r << 3 | (h[i] & 1u) | sign);
   }
-  return codes8(x, 0);
+  return codes4(x, 0);
 }
 
-// Eight elements as they lie in memory, aligned as one element is: the memory
+// N elements as they lie in memory, aligned as one element is: the memory
 // path takes wide accesses at any address.
-template <typename T>
-struct Raw8 {
-  static constexpr int kWords = 2 * sizeof(T);
+template <typename T, int N>
+struct Raw {
+  static constexpr int kWords = N * sizeof(T) / 4;
   uint32_t w[kWords];
 
   __device__ __forceinline__ void load(const T* p) { __builtin_memcpy(w, p, sizeof(w)); }
@@ -181,7 +198,7 @@ struct Raw8 {
     if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, w[i]);
     else return (float)__builtin_bit_cast(T, (uint16_t)(i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu));
   }
-  __device__ __forceinline__ void set(const float (&x)[8]) {
+  __device__ __forceinline__ void set(const float (&x)[N]) {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       if constexpr (sizeof(T) == 4) w[i] = __builtin_bit_cast(uint32_t, x[i]);
@@ -191,103 +208,113 @@ struct Raw8 {
     }
   }
   // The neighbours swapped, where mask is set; 0 elsewhere.
-  __device__ __forceinline__ void swap_of(const Raw8& x, uint32_t mask) {
+  __device__ __forceinline__ void swap_of(const Raw& x, uint32_t mask) {
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
       w[i] = (sizeof(T) == 4 ? x.w[i ^ 1] : x.w[i] << 16 | x.w[i] >> 16) & mask;
   }
 };
 
-// A wave takes 64 / LG units at a time (a step): first the token's key/value
-// heads, then its queries, kAhead steps at once; the workgroups of a token
-// share its steps.
+// A wave takes as many heads as it has room for at a time (a step): first the
+// token's key/value heads, then its queries, kAhead steps at once; the
+// workgroups of a token share its steps.
 template <int D, typename T>
 __global__ __launch_bounds__(kBlock) void k_kv_append(AppendArgs a) {
-  constexpr int LG = Group<D>::kLanes, kStep = kWave / LG, kAhead = 4 / sizeof(T);
+  constexpr int LG = query_lanes(D), kStep = kWave / LG, kAhead = 4 / sizeof(T);
+  constexpr int KG = key_lanes(D), kKeyStep = kWave / KG;
   __shared__ __align__(16) Tables<D> tab;
   const int i = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
-  const int lane = threadIdx.x & (kWave - 1), sub = lane % LG, mine = lane / LG;
+  const int lane = threadIdx.x & (kWave - 1), mine = lane / LG;
   const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int c0 = 8 * sub, half = a.rotary / 2;
-  const bool live = c0 < D, turned = c0 < a.rotary, apart = turned && !a.interleaved;
-  // Where the channels that these are turned with lie from them.
-  const int turn = c0 < half ? half : -half;
-  const uint32_t near = turned && a.interleaved ? ~0u : 0u;
-  const int k_steps = (a.kv.Hk + kStep - 1) / kStep;
+  const int c0 = 8 * (lane % LG), kc0 = 4 * (lane % KG), half = a.rotary / 2;
+  const bool live = c0 < D, key_live = kc0 < D;
+  // Whether a channel is turned with one apart, and where that lies from it.
+  auto apart = [&](int c) { return c < a.rotary && !a.interleaved; };
+  auto turn = [&](int c) { return c < half ? half : -half; };
+  auto near = [&](int c) { return c < a.rotary ? ~0u : 0u; };  // of neighbours
   const int s_begin = part * a.steps_per_part;
-  const int s_end = min(s_begin + a.steps_per_part, a.steps), k_end = min(k_steps, s_end);
-  int s = s_begin + wv;
+  const int s_end = min(s_begin + a.steps_per_part, a.steps), k_end = min(a.k_steps, s_end);
+  int sk = s_begin + wv;
+  int s = sk + (max(k_end - sk, 0) + kWavesPerBlock - 1) / kWavesPerBlock * kWavesPerBlock;  // first of queries
 
-  Raw8<T> x[kAhead]{}, y[kAhead]{}, v8{};
-  auto load = [&](const T* row, int slot) {
-    x[slot].load(row + c0);
-    if (apart) y[slot].load(row + c0 + turn);
-  };
+  Raw<T, 4> kx{}, ky{}, kv{};
+  Raw<T, 8> x[kAhead]{}, y[kAhead]{};
   auto load_keys = [&](int s) {
-    const int u = s * kStep + mine;
-    if (!live || u >= a.kv.Hk) return;
-    load((const T*)a.k + i * a.ks + u * D, 0);
-    v8.load((const T*)a.v + i * a.vs + u * D + c0);
+    const int u = s * kKeyStep + lane / KG;
+    if (!key_live || u >= a.kv.Hk) return;
+    const T* row = (const T*)a.k + i * a.ks + u * D + kc0;
+    kx.load(row);
+    if (apart(kc0)) ky.load(row + turn(kc0));
+    kv.load((const T*)a.v + i * a.vs + u * D + kc0);
   };
   auto load_queries = [&](int s) {
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) {
-      const int at = s + n * kWavesPerBlock, u = (at - k_steps) * kStep + mine;
-      if (at < s_end && live && u < a.kv.Hq) load((const T*)a.q + i * a.qs + u * D, n);
+      const int at = s + n * kWavesPerBlock, u = (at - a.k_steps) * kStep + mine;
+      if (at < s_end && live && u < a.kv.Hq) {
+        const T* row = (const T*)a.q + i * a.qs + u * D + c0;
+        x[n].load(row);
+        if (apart(c0)) y[n].load(row + turn(c0));
+      }
     }
   };
   // Asked for before anything else is known.
-  if (s < k_end) load_keys(s);
-  else load_queries(s);
+  if (sk < k_end) load_keys(sk);
+  load_queries(s);
+
+  const Pair pair(a, min((int)threadIdx.x, D / 2 - 1));
+  double pos = a.positions ? (double)a.positions[i] : 0.0;
 
   const KvToken tok = kv_token(a.kv, i);
   if (tok.b < 0) return;
-  if (threadIdx.x < D / 2)
-    fill_tables(tab, a, threadIdx.x, a.positions ? (double)a.positions[i] : (double)tok.place,
-                s_begin < k_steps, s_end > k_steps);
+  if (!a.positions) pos = (double)tok.place;
+  if (threadIdx.x < D / 2) pair.fill(tab, pos, s_begin < a.k_steps, s_end > a.k_steps);
   __syncthreads();
 
-  while (s < k_end) {
-    const int u = s * kStep + mine;
-    const bool on = live && u < a.kv.Hk;
-    double k[8], r = 1.0;
-    float v[8];
-    if (a.interleaved) y[0].swap_of(x[0], near);
+  for (; sk < k_end; sk += kWavesPerBlock) {
+    const int u = sk * kKeyStep + lane / KG, sub = lane % KG;
+    const bool on = key_live && u < a.kv.Hk;
+    double k[4], r = 1.0;
+    float v[4];
+    if (a.interleaved) ky.swap_of(kx, near(kc0));
     if (a.k_norm) {
       double ss = 0.0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss += (double)x[0][e] * (double)x[0][e];
-      r = 1.0 / sqrt(group_sum<LG>(ss) / D + (double)a.eps);
+      for (int e = 0; e < 4; ++e) ss += (double)kx[e] * (double)kx[e];
+      r = 1.0 / sqrt(group_sum<KG>(ss) / D + (double)a.eps);
     }
     bool bad = false;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = live ? c0 + e : e;
-      k[e] = r * ((double)x[0][e] * tab.ka[c] + (double)y[0][e] * tab.kb[c]);
-      v[e] = v8[e];
+    for (int e = 0; e < 4; ++e) {
+      const int c = key_live ? kc0 + e : e;
+      k[e] = r * ((double)kx[e] * tab.ka[c] + (double)ky[e] * tab.kb[c]);
+      v[e] = kv[e];
       bad |= !(fabs(k[e]) < INFINITY) || !(fabsf(v[e]) < INFINITY);
     }
-    s += kWavesPerBlock;
-    if (s < k_end) load_keys(s);
-    else load_queries(s);
-    const uint64_t group = (1ull << LG) - 1;
-    const bool nan_token = (__ballot(bad && on) >> (lane & ~(LG - 1))) & group;
+    if (sk + kWavesPerBlock < k_end) load_keys(sk + kWavesPerBlock);
+    const uint64_t unit = KG == kWave ? ~0ull : (1ull << KG) - 1;
+    const bool nan_token = (__ballot(bad && on) >> (lane & ~(KG - 1))) & unit;
     uint32_t ke, ve;
-    uint32_t kc = quantise8(k, ke), vc = quantise8(v, ve);
+    uint32_t kc = quantise4(k, ke), vc = quantise4(v, ve);
     if (nan_token) {
       kc = vc = 0;
       ke = 255;
       ve = 127;
     }
+    // Two lanes' codes are a dword.
+    kc |= dpp_u<0xB1>(0u, kc) << 16;
+    vc |= dpp_u<0xB1>(0u, vc) << 16;
     const int64_t base = on ? kv_page_base(a.kv, tok.b, tok.place, u) : -1;
     if (base >= 0) {
       const int P = 1 << a.kv.page_shift, o = (int)(tok.place & (P - 1));
       uint8_t* c = a.cache + base;
-      *reinterpret_cast<uint32_t*>(c + o * (D / 2) + 4 * sub) = kc;
-      *reinterpret_cast<uint32_t*>(c + (P + o) * (D / 2) + 4 * sub) = vc;
-      if (sub % 4 == 0) {
-        c[P * D + o * (D / 32) + sub / 4] = (uint8_t)ke;
-        c[P * D + (P + o) * (D / 32) + sub / 4] = (uint8_t)ve;
+      if (sub % 2 == 0) {
+        *reinterpret_cast<uint32_t*>(c + o * (D / 2) + 2 * sub) = kc;
+        *reinterpret_cast<uint32_t*>(c + (P + o) * (D / 2) + 2 * sub) = vc;
+      }
+      if (sub % 8 == 0) {
+        c[P * D + o * (D / 32) + sub / 8] = (uint8_t)ke;
+        c[P * D + (P + o) * (D / 32) + sub / 8] = (uint8_t)ve;
       }
     }
   }
@@ -301,10 +328,10 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(AppendArgs a) {
   }
   T* out = (T*)a.q_out + (int64_t)i * a.kv.Hq * D + c0;
   for (; s < s_end; s += kAhead * kWavesPerBlock) {
-    Raw8<T> z[kAhead];
+    Raw<T, 8> z[kAhead];
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) {
-      if (a.interleaved) y[n].swap_of(x[n], near);
+      if (a.interleaved) y[n].swap_of(x[n], near(c0));
       float t[8], r = 1.f;
       if (a.q_norm) {
         float ss = 0.f;
@@ -319,7 +346,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(AppendArgs a) {
     load_queries(s + kAhead * kWavesPerBlock);
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) {
-      const int at = s + n * kWavesPerBlock, u = (at - k_steps) * kStep + mine;
+      const int at = s + n * kWavesPerBlock, u = (at - a.k_steps) * kStep + mine;
       if (at < s_end && live && u < a.kv.Hq) z[n].store(out + u * D);
     }
   }
@@ -361,7 +388,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(ReadArgs a) {
         x[n] = ((word >> (4 * n)) & 8 ? -mag : mag) * s;
       }
     }
-    Raw8<float> raw;
+    Raw<float, 8> raw;
     raw.set(x);
     raw.store(out + ((int64_t)i * a.kv.Hk + h) * D + 8 * sub);
   }
@@ -434,8 +461,9 @@ int32_t moe_kv_append(const moe_kv_desc* desc, const moe_kv_batch* batch, int32_
   a.interleaved = desc->flags & MOE_KV_ROTARY_INTERLEAVED;
   // One workgroup a token where there are tokens enough to fill the chip (five
   // workgroups a CU), several, down to a step a wave, where there are not.
-  const int step = kWave / (D <= 64 ? 8 : D <= 128 ? 16 : 32);
-  a.steps = (desc->n_kv_heads + step - 1) / step + (q ? (desc->n_heads + step - 1) / step : 0);
+  const int step = kWave / query_lanes(D), key_step = kWave / key_lanes(D);
+  a.k_steps = (desc->n_kv_heads + key_step - 1) / key_step;
+  a.steps = a.k_steps + (q ? (desc->n_heads + step - 1) / step : 0);
   const int want = (1280 + batch->n_tokens - 1) / batch->n_tokens;
   const int rounds = (a.steps + want * kWavesPerBlock - 1) / (want * kWavesPerBlock);
   a.steps_per_part = rounds * kWavesPerBlock;
