@@ -150,7 +150,7 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   // 16384, of which there are two, takes 106 us (96), 4 rows over 4000 tokens
   // 15.9 (15.0).
   p.waves = kAttnPartWaves;
-  if (!attn_part_waves(d->head_dim, p.row_tiles, attn_terms(dtype)) || !attn_split(p, d, b, dtype, all)) {
+  if (p.row_tiles != 2 || !attn_split(p, d, b, dtype, all)) {
     p.waves = kAttnWaves;
     attn_split(p, d, b, dtype, all);
   }

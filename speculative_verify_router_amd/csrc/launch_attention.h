@@ -10,7 +10,7 @@ int32_t launch_kv_attention(const AttnArgs& a, int32_t dtype, int row_tiles, int
                             hipStream_t st) {
   const dim3 n(grid), t(waves * kWave);
 #define SVR_ATTN(RT, NT, W, T)                                                          \
-  if constexpr (RT <= attn_most_row_tiles(D, NT) && (W == kAttnWaves || attn_part_waves(D, RT, NT))) { \
+  if constexpr (RT <= attn_most_row_tiles(D, NT)) {                                     \
     if (row_tiles == RT && waves == W)                                                  \
       hipLaunchKernelGGL((k_kv_attention<D, RT, NT, W, T>), n, t, 0, st, a);            \
   }
