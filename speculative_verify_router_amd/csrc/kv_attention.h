@@ -23,16 +23,19 @@
 // Bound: instructions.  A tile of two row tiles at D = 192 issues 96
 // widenings (4.6 clocks each), 48 products (17) and about 200 others, which
 // overlap with the products only in part; two waves a SIMD pass 32 tokens in
-// 0.9 us each.  Measured with 64 query on 4 key/value heads, bf16: 512 rows
-// over 16384 tokens 453 us (896 TFLOP/s, 82% of what a large bf16 product of
-// the library reaches here), 4 rows over 60000 tokens 28 us (49 MB; 17 us of
-// tiles, the rest begins and ends the workgroups, then 5.6 us of joining), 1
-// row over 777 tokens 6 + 4 us, all latency.  29 sequences of up to 5000
-// tokens, fp16, 32 on 8 heads of 128: 22 + 7 us (82 MB, 2.8 TB/s).
-// Others that were measured, for the first two calls and the third: 64 rows a
-// wave (one wave a SIMD) 716 and 47 us; waves sharing widened tiles through
-// shared memory, with 16x16 or 32x32 products, 475 to 497, 29 to 33 and 5.6 to
-// 7.3 us; eight waves a workgroup 478, 33 and 8 us.
+// 0.9 us each.  Measured with 64 query on 4 key/value heads of 192: 512 rows
+// over 16384 tokens 453 us in bf16 (896 TFLOP/s, 82% of what a large bf16
+// product of the library reaches here), 892 in fp16 and 1060 in fp32 (384
+// TFLOP/s, three products each: the same rate); 4 rows over 60000 tokens 26 us
+// and 4.5 of joining (49 MB; 17 us of tiles, the rest begins and ends the
+// workgroups); 1 row over 777 tokens 9 us, of which 4 are one wave's tile and
+// 3.5 joining seven parts.  29 sequences of up to 5000 tokens, fp16, 32 on 8
+// heads of 128: 25 us (82 MB, 3.3 TB/s).
+// Others that were measured, for the first bf16 call, the verify batch and the
+// single row: 64 rows a wave (one wave a SIMD) 716 and 47 us; waves sharing
+// widened tiles through shared memory, with 16x16 or 32x32 products, 475 to
+// 497, 29 to 33 and 5.6 to 7.3 us (with a second kernel after the last two);
+// eight waves in every workgroup 478, 33 and 11 us.
 #pragma once
 
 #include "kv.h"
