@@ -18,13 +18,14 @@ constexpr int kMaxSplits = 128;
 // lanes reads a split's sums 16 bytes a lane, the slots take the splits in
 // turn.  Bound by latency, not bytes (a row's parts are at most 128 KB): the
 // first kBatch of a slot's reads are issued before it is known which splits
-// are in use (the workspace holds them all, what is not in use is dropped):
-// all of them for a single sequence, where all are in use, and one for
-// several, which use few.  4 rows of 64 heads with 63 splits: 5.6 us (6.4 with
-// four); 70 rows of 32 heads: 7 us (7.5 with four).
-template <int D, int kBatch, typename T>
-__global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a) {
-  constexpr int L = D / 4, kSlots = kBlock / L;
+// are in use (the workspace holds them all, what is not in use is dropped).
+// Rows for at most a workgroup a CU: all reads at once, by 512 threads (1 row
+// of 64 heads with 128 splits 5.1 us, 8.2 with 256 threads; 4 rows with 32 5.0
+// us).  More: one read, by 256 (12 rows of 64 heads with 20 of 43 splits in use
+// 5.7 us, 9.9 with all at once).
+template <int D, int kThreads, int kBatch, typename T>
+__global__ __launch_bounds__(kThreads) void k_kv_join(AttnArgs a) {
+  constexpr int L = D / 4, kSlots = kThreads / L;
   __shared__ float s_w[kMaxSplits];
   __shared__ f32x4v s_o[kSlots][L];
   const int lane = threadIdx.x & (kWave - 1);
@@ -89,19 +90,21 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(AttnArgs a) {
     a.lse[to] = sum == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }
 
-template <int D, int kBatch>
+template <int D, int kThreads, int kBatch>
 void launch_kv_join(const AttnArgs& a, int32_t dtype, unsigned n, hipStream_t st) {
-  const dim3 g(n), t(kBlock);
+  const dim3 g(n), t(kThreads);
   switch (dtype) {
-    case MOE_F32: hipLaunchKernelGGL((k_kv_join<D, kBatch, float>), g, t, 0, st, a); break;
-    case MOE_BF16: hipLaunchKernelGGL((k_kv_join<D, kBatch, bf16>), g, t, 0, st, a); break;
-    default: hipLaunchKernelGGL((k_kv_join<D, kBatch, _Float16>), g, t, 0, st, a); break;
+    case MOE_F32: hipLaunchKernelGGL((k_kv_join<D, kThreads, kBatch, float>), g, t, 0, st, a); break;
+    case MOE_BF16: hipLaunchKernelGGL((k_kv_join<D, kThreads, kBatch, bf16>), g, t, 0, st, a); break;
+    default: hipLaunchKernelGGL((k_kv_join<D, kThreads, kBatch, _Float16>), g, t, 0, st, a); break;
   }
 }
+// n: rows x heads.
 template <int D>
 void launch_kv_join(const AttnArgs& a, int32_t dtype, unsigned n, hipStream_t st) {
-  if (a.kv.n_seqs == 1) launch_kv_join<D, 13>(a, dtype, n, st);
-  else launch_kv_join<D, 1>(a, dtype, n, st);
+  constexpr int kFew = 512, kSlots = kFew / (D / 4);
+  if (n <= 256) launch_kv_join<D, kFew, (kMaxSplits + kSlots - 1) / kSlots>(a, dtype, n, st);
+  else launch_kv_join<D, 256, 1>(a, dtype, n, st);
 }
 
 // How a batch is cut, as far as its sizes say (the lengths are on the device).
