@@ -21,16 +21,17 @@
 // independent, and average out over the tokens that matter.
 //
 // Bound: instructions.  A tile of two row tiles at D = 192 issues 96
-// widenings (4.6 clocks each), 48 products (17) and about 200 others, which
+// widenings (4.6 clocks each), 48 products (17) and about 130 others, which
 // overlap with the products only in part; two waves a SIMD pass 32 tokens in
 // 0.9 us each.  Measured with 64 query on 4 key/value heads of 192: 512 rows
-// over 16384 tokens 453 us in bf16 (896 TFLOP/s, 82% of what a large bf16
-// product of the library reaches here), 892 in fp16 and 1060 in fp32 (384
-// TFLOP/s, three products each: the same rate); 4 rows over 60000 tokens 26 us
-// and 4.5 of joining (49 MB; 17 us of tiles, the rest begins and ends the
+// over 16384 tokens 455 to 475 us in bf16 (850 to 890 TFLOP/s, 80% of what a
+// large bf16 product of the library reaches here), 859 in fp16 and 1036 in
+// fp32 (392 TFLOP/s, three products each); 4 rows over 60000 tokens 26 us and
+// 4.6 of joining (49 MB; 17 us of tiles, the rest begins and ends the
 // workgroups); 1 row over 777 tokens 9 us, of which 4 are one wave's tile and
 // 3.5 joining seven parts.  29 sequences of up to 5000 tokens, fp16, 32 on 8
-// heads of 128: 25 us (82 MB, 3.3 TB/s).
+// heads of 128: 25 us (82 MB, 3.3 TB/s).  Addresses by vector arithmetic in
+// every tile instead of once: 892 and 1056 in fp16 and fp32, 1 us for 4 rows.
 // Others that were measured, for the first bf16 call, the verify batch and the
 // single row: 64 rows a wave (one wave a SIMD) 716 and 47 us; waves sharing
 // widened tiles through shared memory, with 16x16 or 32x32 products, 475 to
@@ -243,53 +244,68 @@ __device__ __forceinline__ void split_terms(float x, bf16 (&t)[NT]) {
   }
 }
 
-// A lane's codes and scales of one token for D/4 channels: the full 128s in
-// 16-byte pieces, a last 64 in 8 bytes.  A scale is kept as the aligned dword
-// that holds it and its place there: of a byte the compiler keeps eight bits
-// from tile to tile, and widens them where it was loaded, which would wait
-// for the next tile's codes in the middle of this one.
+// Where a lane finds its part of a token l of sixteen (a run): 32 channels in
+// 16 bytes of codes for each full 128 channels, 16 in 8 bytes for a last 64,
+// and the aligned dword that holds their scale, with its place there.  Runs
+// begin at multiples of sixteen tokens, whose scales are whole dwords, so all
+// of this is the same for every tile, and a load takes no vector arithmetic.
+template <int D>
+struct LanePart {
+  static constexpr int kParts = (D + 127) / 128;
+  uint32_t code, half, scale[kParts], at[kParts];
+
+  __device__ __forceinline__ LanePart(int l, int g) {
+    code = l * (D / 2) + 16 * g;
+    half = l * (D / 2) + 8 * g;
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      const uint32_t n = l * (D / 32) + 4 * p + (full(p) ? g : g / 2);
+      scale[p] = n & ~3u;
+      at[p] = 8 * (n & 3);
+    }
+  }
+  __device__ __forceinline__ static constexpr bool full(int p) { return 64 * (2 * p + 1) < D; }
+};
+
+// A lane's codes and scales of one token for D/4 channels.  A scale is kept
+// as the dword around it: of a byte the compiler keeps eight bits from tile to
+// tile, and widens them where it was loaded, which would wait for the next
+// tile's codes in the middle of this one.
 template <int D>
 struct Codes {
+  static constexpr int kParts = LanePart<D>::kParts;
   uint32_t w[D / 32];
-  uint32_t e[(D + 127) / 128], at[(D + 127) / 128];
+  uint32_t e[kParts];
 
+  // codes, scales: of the run.
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, const LanePart<D>& at) {
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      if (LanePart<D>::full(p)) {
+        const uint4 v = *reinterpret_cast<const uint4*>(codes + 64 * p + at.code);
+        w[4 * p] = v.x;
+        w[4 * p + 1] = v.y;
+        w[4 * p + 2] = v.z;
+        w[4 * p + 3] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(codes + 64 * p + at.half);
+        w[4 * p] = v.x;
+        w[4 * p + 1] = v.y;
+      }
+      e[p] = *reinterpret_cast<const uint32_t*>(scales + at.scale[p]);
+    }
+  }
   // The scale of word k, in the exponent of a float.
-  __device__ __forceinline__ float scale(int k) const {
-    return __builtin_bit_cast(float, __builtin_amdgcn_ubfe(e[k / 4], at[k / 4], 8) << 23);
+  __device__ __forceinline__ float scale(int k, const LanePart<D>& at) const {
+    return __builtin_bit_cast(float, __builtin_amdgcn_ubfe(e[k / 4], at.at[k / 4], 8) << 23);
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) w[k] = 0;
 #pragma unroll
-    for (int p = 0; p < (D + 127) / 128; ++p) e[p] = 0x7F7F7F7Fu;
+    for (int p = 0; p < kParts; ++p) e[p] = 0x7F7F7F7Fu;
   }
 };
-
-// Token i of a page's codes and scales (the scales are 4-byte aligned).
-template <int D>
-__device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* scales, int i, int g,
-                                           Codes<D>& x) {
-  codes += i * (D / 2);
-#pragma unroll
-  for (int p = 0; p < (D + 127) / 128; ++p) {
-    int at = i * (D / 32) + 4 * p;
-    if (64 * (2 * p + 1) < D) {
-      const uint4 v = *reinterpret_cast<const uint4*>(codes + 64 * p + 16 * g);
-      x.w[4 * p] = v.x;
-      x.w[4 * p + 1] = v.y;
-      x.w[4 * p + 2] = v.z;
-      x.w[4 * p + 3] = v.w;
-      at += g;
-    } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(codes + 64 * p + 8 * g);
-      x.w[4 * p] = v.x;
-      x.w[4 * p + 1] = v.y;
-      at += g / 2;
-    }
-    x.e[p] = *reinterpret_cast<const uint32_t*>(scales + (at & ~3));
-    x.at[p] = 8 * (at & 3);
-  }
-}
 
 // Eight codes times s, a power of two, as bf16 (NaN where its exponent is 255).
 __device__ __forceinline__ bf16x8 widen(uint32_t w, float s) {
@@ -399,8 +415,7 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
   const int t_end = min(rg.ntile, (split + 1) * rg.per), t_last = t_end - 1;
 
   // Sixteen tokens (a run) lie in one page.  A run outside [beg, end) becomes
-  // one inside, and so does a lane's token outside, so nothing but what some
-  // row sees is ever loaded.
+  // one inside; what lies in a run outside of it is dropped.
   const int P = 1 << a.kv.page_shift;
   // Read through the scalar cache: as a plain load it would be a vector load
   // whose wait holds up the tile.
@@ -411,11 +426,12 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
     return min(max(rg.tb + min(t, t_last) * kAttnTile + 16 * u, run_lo), run_hi);
   };
   auto page_of = [&](int t, int u) { return table[run(t, u) >> a.kv.page_shift]; };
+  const LanePart<D> part(l16, g);
   auto load_keys_or_values = [&](int t, int u, int page, int side, Codes<D>& x) {
     page = (unsigned)page < (unsigned)a.kv.n_pages ? page : 0;
     const uint8_t* c = a.cache + ((int64_t)page * a.kv.Hk + kvh) * a.kv.page_bytes;
-    const int i = min(max(run(t, u) + l16, rg.beg), rg.end - 1) & (P - 1);
-    load_codes<D>(c + side * (P * (D / 2)), c + P * D + side * (P * (D / 32)), i, g, x);
+    const int i = run(t, u) & (P - 1);
+    x.load(c + (side * P + i) * (D / 2), c + P * D + (side * P + i) * (D / 32), part);
   };
 
   // One tile of codes is kept in flight: keys of the next tile are asked for
@@ -487,6 +503,13 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
       gone[u] = (unsigned)page[u] >= (unsigned)a.kv.n_pages;
       if (gone[u]) vc[u].clear();  // whatever lies there must not meet a weight of zero
     }
+    if (tok0 < rg.beg || tok0 + kAttnTile > rg.end) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int tk = tok0 + 16 * u + l16;
+        if (tk < rg.beg || tk >= rg.end) vc[u].clear();
+      }
+    }
     f32x4v s[RT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -494,7 +517,7 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
       for (int rt = 0; rt < RT; ++rt) s[rt][u] = f32x4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const bf16x8 kf = widen(kc[u].w[k], kc[u].scale(k));
+        const bf16x8 kf = widen(kc[u].w[k], kc[u].scale(k, part));
 #pragma unroll
         for (int n = NT - 1; n >= 0; --n)
 #pragma unroll
@@ -511,7 +534,7 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
 #pragma unroll
       for (int k = 0; k < KS; ++k)
         *reinterpret_cast<bf16x8*>(stage + (16 * u + l16) * kRowBytes + 2 * step_channel<D>(k, g)) =
-            widen(vc[u].w[k], vc[u].scale(k));
+            widen(vc[u].w[k], vc[u].scale(k, part));
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       load_keys_or_values(t + W, u, next_page[u], 1, vc[u]);
