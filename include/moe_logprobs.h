@@ -46,8 +46,7 @@ int32_t moe_logprobs_workspace_bytes(int32_t max_rows, int64_t vocab, int32_t ma
 
 /* ONE launch.  All pointers are device pointers of the caller.
  *   logits  [n_rows][vocab] of dtype (MOE_F32, MOE_BF16, MOE_F16), rows
- *           row_stride elements apart (16-byte aligned rows are read with
- *           16-byte loads).
+ *           row_stride elements apart.
  *   targets [n_rows] int32, and logprobs [n_rows] float out; both or neither NULL.
  *   entropy [n_rows] float out, may be NULL.
  *   top_ids [n_rows][top_k] int32 out and top_logprobs [n_rows][top_k] float

@@ -19,12 +19,13 @@
 // workgroup to arrive at the row's counter joins them and returns the
 // counter to zero.
 //
-// Measured at 131072 columns: 512 rows of float 56 us (4.8 TB/s: the bytes),
-// of bf16 42 us (3.2 TB/s: about nine instructions a value), with five
-// alternatives 66 and 55 us; 4 rows of float 6 us, with 20 alternatives 14
-// (placing them and joining the workgroups); 1 row 5 us.  32 columns a lane
-// leave three waves a SIMD: 83 and 58 us; keys made again instead of held, and
-// eight waves a SIMD: 39 us in bf16, but 59 in float.
+// Measured at 131072 columns: 512 rows of float 51 us (5.3 TB/s: the bytes),
+// of bf16 40 us (3.4 TB/s: about eight instructions a value, and a tile ahead
+// is 2 KB a wave), with five alternatives 56 and 53 us; 4 rows of float 6 us,
+// with 20 alternatives 14 (placing them and joining the workgroups); 1 row 5
+// us.  32 columns a lane leave three waves a SIMD: 83 and 58 us; three
+// workgroups a row 50 and 34 us, but 59 and 53 with alternatives, whose joins
+// are more.
 #include <hip/hip_runtime.h>
 
 #include "common.h"
@@ -44,7 +45,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 struct LpArgs {
   const void* x;
   int64_t stride;
-  int V, blocks, tiles_per_block, k, vec;
+  int V, blocks, tiles_per_block, k;
   const int32_t* targets;
   float *logprobs, *entropy, *top_logprobs;
   int32_t* top_ids;
@@ -197,37 +198,54 @@ struct TopKeys {
   }
 };
 
+// 16 columns of a lane: pieces of 16 bytes, lane after lane.  Kept as the
+// words they come in: as elements, the compiler takes 16-bit ones apart where
+// they are loaded, and waits for them there.
 template <typename T>
-struct Piece {
-  static constexpr int kElems = 16 / sizeof(T);
-  static constexpr int kCount = kLpCols / kElems;
-};
+struct LpTile {
+  static constexpr int kElems = 16 / sizeof(T);  // of a piece
+  static constexpr int kPieces = kLpCols / kElems;
+  uint32_t w[4 * kPieces];
 
-// 16 columns of a lane from tile column `base`: pieces of 16 bytes, lane
-// after lane.  Columns from V on are -inf.
-template <typename T>
-__device__ __forceinline__ void lp_load(const T* row, int base, int V, bool vec, int lane,
-                                        T (&x)[kLpCols]) {
-  constexpr int E = Piece<T>::kElems;
+  // Of the tile at column base; columns from V on are -inf.  (The memory path
+  // takes 16 bytes at any address.)
+  __device__ __forceinline__ void load(const T* row, int base, int V, int lane) {
+    const T* at = row + base + lane * kElems;
+    if (base + kLpTile <= V) {
 #pragma unroll
-  for (int p = 0; p < Piece<T>::kCount; ++p) {
-    const int c = base + p * (E * kWave) + lane * E;
-    if (vec && c + E <= V) {
-      *reinterpret_cast<uint4*>(x + p * E) = *reinterpret_cast<const uint4*>(row + c);
+      for (int p = 0; p < kPieces; ++p) __builtin_memcpy(w + 4 * p, at + p * (kElems * kWave), 16);
     } else {
+      T x[kLpCols];
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[p * E + e] = c + e < V ? row[c + e] : (T)-INFINITY;
+      for (int e = 0; e < kLpCols; ++e) {
+        const int c = (e / kElems) * (kElems * kWave) + e % kElems;
+        x[e] = base + lane * kElems + c < V ? at[c] : (T)-INFINITY;
+      }
+      __builtin_memcpy(w, x, sizeof(x));
     }
   }
-}
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 4 * kPieces; ++i) w[i] = 0;
+  }
+  // Whole words up to here, and waited for here.
+  __device__ __forceinline__ void arrive() {
+#pragma unroll
+    for (int i = 0; i < 4 * kPieces; ++i) asm("" : "+v"(w[i]));
+  }
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, w[e]);
+    else return (float)__builtin_bit_cast(T, (uint16_t)(e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu));
+  }
+};
 
 template <typename T>
 __global__ __launch_bounds__(kBlock) void k_logprobs(LpArgs a) {
-  constexpr int E = Piece<T>::kElems;
+  constexpr int E = LpTile<T>::kElems;
   __shared__ uint64_t s_buf[kWavesPerBlock][2 * kWave];
   __shared__ Sums s_sums[kWavesPerBlock];
   __shared__ int s_last;
-  const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x >> 6;
+  const int lane = threadIdx.x & (kWave - 1), wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int row = blockIdx.x / a.blocks, blk = blockIdx.x % a.blocks;
   const T* x = (const T*)a.x + (int64_t)row * a.stride;
 
@@ -244,18 +262,20 @@ __global__ __launch_bounds__(kBlock) void k_logprobs(LpArgs a) {
   // (Columns stay below 2^30 + a tile of each wave.)
   const int c_begin = blk * a.tiles_per_block * kLpTile;
   const int c_end = min(c_begin + a.tiles_per_block * kLpTile, a.V);
-  T raw[kLpCols];
+  LpTile<T> raw;
   int base = c_begin + wv * kLpTile;
-  if (base < c_end) lp_load(x, base, a.V, a.vec, lane, raw);
+  if (base < c_end) raw.load(x, base, a.V, lane);
   for (; base < c_end; base += kWavesPerBlock * kLpTile) {
     float v[kLpCols], mx = -INFINITY;
+    raw.arrive();
 #pragma unroll
     for (int e = 0; e < kLpCols; ++e) {
-      v[e] = (float)raw[e];
+      v[e] = raw[e];
       mx = fmaxf(mx, v[e]);
     }
     const int next = base + kWavesPerBlock * kLpTile;
-    if (next < c_end) lp_load(x, next, a.V, a.vec, lane, raw);
+    if (next < c_end) raw.load(x, next, a.V, lane);
+    else raw.clear();  // nothing kept, which would be copied in every tile
     if (mx > s.m) s = lp_join(s, Sums{mx, 0.f, 0.f});
     const float m = s.m == -INFINITY ? 0.f : s.m;
     // Four chains each, then one addition to the sums of all tiles.
@@ -446,7 +466,6 @@ int32_t moe_logprobs(const void* logits, int32_t dtype, int32_t n_rows, int64_t 
   a.blocks = p.blocks;
   a.tiles_per_block = p.tiles_per_block;
   a.k = top_k;
-  a.vec = (uintptr_t)logits % 16 == 0 && row_stride * es % 16 == 0;
   a.targets = targets;
   a.logprobs = logprobs;
   a.entropy = entropy;
