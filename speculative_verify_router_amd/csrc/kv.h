@@ -130,24 +130,4 @@ __device__ __forceinline__ int64_t kv_page_base(const KvArgs& a, int b, int64_t 
   return ((int64_t)page * a.Hk + h) * a.page_bytes;
 }
 
-// Eight consecutive elements of type T as float.  vec: the address is 16-byte
-// aligned.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool vec, float (&x)[8]) {
-  T raw[8];
-  if (vec) {
-    if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<uint4*>(raw) = reinterpret_cast<const uint4*>(p)[0];
-      *reinterpret_cast<uint4*>(raw + 4) = reinterpret_cast<const uint4*>(p)[1];
-    } else {
-      *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(p);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) raw[i] = p[i];
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = (float)raw[i];
-}
-
 }  // namespace svr
