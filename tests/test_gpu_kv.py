@@ -483,6 +483,40 @@ def test_append_and_attention_replayed_from_a_graph():
         assert torch.equal(out2, want) and torch.equal(c2, want_cache), i
 
 
+def test_two_graphs_that_share_a_workspace():
+    """Replayed in turn, with eager calls on the same workspace between, at lengths that change."""
+    rng = np.random.default_rng(55)
+    lay = ko.Layout(8, 2, 128, 16)
+    plan = Plan(lay, [2, 1, 3], [900, 200, 500], rng)
+    d, batch, cache = desc_of(lay), plan.batch(), dev(plan.filled_cache(rng))
+    one = svr.KvBatch(dev(np.array([0, 2], np.int32)), batch.seq_lens[:1].clone(), batch.page_table[:1].contiguous(), 2)
+    q, _ = rounded(rng.standard_normal((6, 8, 128)), "f16")
+    q1 = q[:2].clone()
+    ws = torch.zeros(max(svr.moe_kv_attention_workspace_bytes(d, batch, 6),
+                         svr.moe_kv_attention_workspace_bytes(d, one, 2)), dtype=torch.uint8, device="cuda")
+    calls = ((batch, q, torch.empty_like(q)), (one, q1, torch.empty_like(q1)))
+    graphs = [torch.cuda.CUDAGraph() for _ in calls]
+    for g, (b, x, out) in zip(graphs, calls):
+        svr.moe_kv_attention(d, b, x, cache, out, ws=ws)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+            svr.moe_kv_attention(d, b, x, cache, out, ws=ws)
+    for lens in ([900, 200, 500], [40, 200, 3], [899, 1, 77]):
+        batch.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        one.seq_lens.fill_(lens[0])
+        want = []
+        for b, x, out in calls:
+            svr.moe_kv_attention(d, b, x, cache, out)
+            want.append(out.clone())
+        for i in (0, 1, 1, 0, 0, 1):
+            calls[i][2].fill_(float("nan"))
+            graphs[i].replay()
+            assert torch.equal(calls[i][2], want[i]), (lens, i)
+            eager = torch.empty_like(calls[1 - i][2])
+            svr.moe_kv_attention(d, calls[1 - i][0], calls[1 - i][1], cache, eager, ws=ws)
+            assert torch.equal(eager, want[1 - i]), (lens, i)
+
+
 def test_rejected_drafts_are_overwritten():
     """A verify round whose tail is rejected: lower lengths and append again gives the cache of a clean run."""
     rng = np.random.default_rng(19)
