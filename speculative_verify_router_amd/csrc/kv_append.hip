@@ -20,14 +20,17 @@
 // whole number and a key next to a rounding border must fall on its own side
 // whatever the order of the sum.
 //
+// q_out goes past the caches: what reads it next runs on all dies, of which
+// one wrote a row, and a prefill's does not stay; through them, 1878 tokens
+// take 31 us and not 25, and a call with the attention behind it the same.
+//
 // Measured with 64 query and 4 key/value heads of 192 channels: 1878 tokens in
-// bf16 (98 MB) 26 us, 31 from beyond the last cache, 20 without norms and
-// rotation; 512 tokens in float (52 MB) 15 us; 4 tokens 4.3 us, of which the
-// reads one after another (offsets, page, heads) are most.  Angles taken anew
-// for every head: 91, 34 and 8 us; factors in registers and one step ahead,
-// whose copies waited for the stores: 50 and 26; eight channels of a key a
-// lane: 127 registers instead of 81, 4.9 us for 4 tokens; two workgroups a
-// token: 38 us.
+// bf16 (98 MB) 25 us (3.9 TB/s; 20 without norms and rotation), 512 tokens in
+// float (52 MB) 14 us; 4 tokens 4.3 us, of which the reads one after another
+// (offsets, page, heads) are most.  Angles taken anew for every head: 91, 34
+// and 8 us; factors in registers and one step ahead, whose copies waited for
+// the stores: 50 and 26; eight channels of a key a lane: 127 registers instead
+// of 81, 4.9 us for 4 tokens; two workgroups a token: 38 us.
 #include "kv.h"
 
 namespace svr {
@@ -194,6 +197,14 @@ struct Raw {
 
   __device__ __forceinline__ void load(const T* p) { __builtin_memcpy(w, p, sizeof(w)); }
   __device__ __forceinline__ void store(T* p) const { __builtin_memcpy(p, w, sizeof(w)); }
+  // Past the caches (non-temporal).
+  __device__ __forceinline__ void stream(T* p) const {
+    typedef uint32_t Piece __attribute__((ext_vector_type(4), aligned(2)));
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i)
+      __builtin_nontemporal_store(Piece{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]},
+                                  reinterpret_cast<Piece*>(p) + i);
+  }
   __device__ __forceinline__ float operator[](int i) const {
     if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, w[i]);
     else return (float)__builtin_bit_cast(T, (uint16_t)(i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu));
@@ -347,7 +358,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(AppendArgs a) {
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) {
       const int at = s + n * kWavesPerBlock, u = (at - a.k_steps) * kStep + mine;
-      if (at < s_end && live && u < a.kv.Hq) z[n].store(out + u * D);
+      if (at < s_end && live && u < a.kv.Hq) z[n].stream(out + u * D);
     }
   }
 }
