@@ -401,7 +401,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(ReadArgs a) {
     }
     Raw<float, 8> raw;
     raw.set(x);
-    raw.store(out + ((int64_t)i * a.kv.Hk + h) * D + 8 * sub);
+    raw.stream(out + ((int64_t)i * a.kv.Hk + h) * D + 8 * sub);
   }
 }
 

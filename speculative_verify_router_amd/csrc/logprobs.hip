@@ -19,13 +19,12 @@
 // workgroup to arrive at the row's counter joins them and returns the
 // counter to zero.
 //
-// Measured at 131072 columns: 512 rows of float 51 us (5.3 TB/s: the bytes),
-// of bf16 40 us (3.4 TB/s: about eight instructions a value, and a tile ahead
-// is 2 KB a wave), with five alternatives 56 and 53 us; 4 rows of float 6 us,
-// with 20 alternatives 14 (placing them and joining the workgroups); 1 row 5
-// us.  32 columns a lane leave three waves a SIMD: 83 and 58 us; three
-// workgroups a row 50 and 34 us, but 59 and 53 with alternatives, whose joins
-// are more.
+// Measured at 131072 columns: 512 rows of float 45 us (5.9 TB/s: the bytes),
+// of bf16 31 us (4.3 TB/s: about eight instructions a value), with five
+// alternatives 50 and 45 us; 4 rows of float 6 us, with 20 alternatives 14
+// (placing them and joining the workgroups); 1 row 5 us.  Loads through the
+// caches, which nothing is read from twice: 51 and 40 us.  Two tiles of 16-bit
+// columns in flight: the same.
 #include <hip/hip_runtime.h>
 
 #include "common.h"
@@ -207,13 +206,17 @@ struct LpTile {
   static constexpr int kPieces = kLpCols / kElems;
   uint32_t w[4 * kPieces];
 
-  // Of the tile at column base; columns from V on are -inf.  (The memory path
-  // takes 16 bytes at any address.)
+  // Of the tile at column base, past the caches; columns from V on are -inf.
+  // (The memory path takes 16 bytes at any address.)
   __device__ __forceinline__ void load(const T* row, int base, int V, int lane) {
     const T* at = row + base + lane * kElems;
     if (base + kLpTile <= V) {
 #pragma unroll
-      for (int p = 0; p < kPieces; ++p) __builtin_memcpy(w + 4 * p, at + p * (kElems * kWave), 16);
+      for (int p = 0; p < kPieces; ++p) {
+        typedef uint32_t Four __attribute__((ext_vector_type(4), aligned(2)));
+        const Four q = __builtin_nontemporal_load(reinterpret_cast<const Four*>(at + p * (kElems * kWave)));
+        __builtin_memcpy(w + 4 * p, &q, 16);
+      }
     } else {
       T x[kLpCols];
 #pragma unroll
