@@ -135,9 +135,9 @@ int32_t moe_kv_attention_workspace_bytes(const moe_kv_desc* desc, const moe_kv_b
  * the natural log of sum_t e^(s_t) (-inf for a row that sees nothing), with
  * which parts of one attention can be joined.  Rows of a sequence from
  * max_rows on are left unwritten.
- * Keys and values enter exactly; sums are 32-bit; the query and the softmax
- * weights enter as one 16-bit term for MOE_BF16 (the weights rounded once),
- * two for MOE_F16, three for MOE_F32 (24 bits).
+ * Keys and values enter exactly; sums are 32-bit; the query enters exactly for
+ * MOE_BF16, with 16 bits or more for MOE_F16, 24 for MOE_F32; the softmax weights
+ * with 16 bits, 24 for MOE_F32.
  * Errors as moe_kv_append, and MOE_ERR_WORKSPACE for a workspace that is
  * too small, MOE_ERR_ARG for one that is not 256-byte aligned. */
 int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int32_t dtype,

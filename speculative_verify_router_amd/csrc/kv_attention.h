@@ -15,25 +15,27 @@
 // channels as rows: they are widened, staged as [token][channel] in the
 // wave's own shared memory and read back transposed.  E2M1 times a power of
 // two is exact in bf16, so keys and values enter exactly.
-//   NT terms of bf16 hold a query value and a softmax weight: one for bf16
-// activations, two for fp16, three (24 bits) for fp32.  The one rounding of a
-// weight to 8 bits stays below that of a bf16 result: weights' errors are
-// independent, and average out over the tokens that matter.
+//   Terms of bf16, of 8 bits each, hold a query value and a softmax weight: a
+// query value as many as its type needs (one for bf16, two for fp16, three for
+// fp32), a weight two (16 bits), three for fp32.  One term a weight would
+// not do for bf16 either: the weights' roundings are independent, so they
+// shrink with the number of tokens, but so does the result, and its error
+// becomes as large as its own rounding (60000 tokens: 0.0023 of the result
+// instead of the 0.0016 that the rounding alone makes; two terms: 0.0016).  It
+// would save a third of the products: 458 and 581 us for the first call below.
 //
 // Bound: instructions.  A tile of two row tiles at D = 192 issues 96
-// widenings (4.6 clocks each), 48 products (17) and about 130 others, which
-// overlap with the products only in part; two waves a SIMD pass 32 tokens in
-// 0.9 us each.  Measured with 64 query on 4 key/value heads of 192: 512 rows
-// over 16384 tokens 455 to 475 us in bf16 (850 to 890 TFLOP/s, 80% of what a
-// large bf16 product of the library reaches here), 859 in fp16 and 1036 in
-// fp32 (392 TFLOP/s, three products each); 4 rows over 60000 tokens 26 us and
-// 4.6 of joining (49 MB; 17 us of tiles, the rest begins and ends the
-// workgroups); 1 row over 777 tokens 9 us, of which 4 are one wave's tile and
-// 3.5 joining seven parts.  29 sequences of up to 5000 tokens, fp16, 32 on 8
+// widenings, 72 products and about 150 others, which overlap with the
+// products only in part; two waves a SIMD pass 32 tokens in 1.1 us each.
+// Measured with 64 query on 4 key/value heads of 192: 512 rows over 16384
+// tokens 581 us in bf16 (698 TFLOP/s, 64% of what a large bf16 product of the
+// library reaches here, with a half more products than that counts), 847 in
+// fp16 and 1027 in fp32 (396 TFLOP/s, three products each); 4 rows over 60000
+// tokens 32 us with the joining (49 MB); 1 row over 777 tokens 10 us.  29 sequences of up to 5000 tokens, fp16, 32 on 8
 // heads of 128: 25 us (82 MB, 3.3 TB/s).  Addresses by vector arithmetic in
 // every tile instead of once: 892 and 1056 in fp16 and fp32, 1 us for 4 rows.
 // Others that were measured, for the first bf16 call, the verify batch and the
-// single row: 64 rows a wave (one wave a SIMD) 716 and 47 us; waves sharing
+// single row, with one term a weight (458, 28.6 and 9.6 us as it is): 64 rows a wave (one wave a SIMD) 716 and 47 us; waves sharing
 // widened tiles through shared memory, with 16x16 or 32x32 products, 475 to
 // 497, 29 to 33 and 5.6 to 7.3 us (with a second kernel after the last two);
 // eight waves in every workgroup 478, 33 and 11 us.
@@ -338,9 +340,12 @@ constexpr int attn_waves(int D, int RT, int NT) {
   return n <= 48 ? 4 : n <= 72 ? 3 : n <= 160 ? 2 : 1;
 }
 
+// Terms of a softmax weight, for NT of a query value: never one, see above.
+constexpr int attn_weight_terms(int NT) { return NT < 2 ? 2 : NT; }
+
 template <int D, int RT, int NT, int W, typename T>
 __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attention(AttnArgs a) {
-  constexpr int KS = D / 32, CB = D / 16;
+  constexpr int KS = D / 32, CB = D / 16, NP = attn_weight_terms(NT);
   constexpr int kRowBytes = 2 * D + 16;            // a staged token: the pad spreads the banks
   constexpr int kStage = kAttnTile * kRowBytes;    // a wave's staged tokens
   constexpr int kJoinRow = D + 4;                  // floats of a joined row
@@ -580,18 +585,18 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
         for (int cb = 0; cb < CB; ++cb) o[rt][cb] *= f;
       }
     }
-    bf16x8 pf[RT][NT];
+    bf16x8 pf[RT][NP];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const float m0 = mx[rt] == -INFINITY ? 0.f : mx[rt];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        bf16 x[NT];
+        bf16 x[NP];
         const float p = __builtin_amdgcn_exp2f(fmaf(s[rt][i / 4][i % 4], a.c, -m0));
         sum[rt] += p;
-        split_terms<NT>(p, x);
+        split_terms<NP>(p, x);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) pf[rt][n][i] = x[n];
+        for (int n = 0; n < NP; ++n) pf[rt][n][i] = x[n];
       }
     }
 
@@ -603,7 +608,7 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
                                read_transposed(from + 16 * kRowBytes + 32 * cb)};
       const bf16x8 vf = __builtin_bit_cast(bf16x8, v);
 #pragma unroll
-      for (int n = NT - 1; n >= 0; --n)
+      for (int n = NP - 1; n >= 0; --n)
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
           o[rt][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][n], o[rt][cb], 0, 0, 0);

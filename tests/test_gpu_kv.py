@@ -539,3 +539,26 @@ def test_rejected_drafts_are_overwritten():
     ko.append(lay, want, [0, 4], [37], first.table, q64, a[2], a[3])
     assert np.array_equal(c.cpu().numpy(), want)
     check_attention(lay, second, want, "bf16", rng, q=(q, q64))
+
+
+@pytest.mark.parametrize("dim,heads,kv_heads,rows,length,width", [
+    (64, 8, 2, 1, 1500, None), (128, 16, 1, 4, 3001, None), (192, 16, 1, 4, 2500, 700), (256, 8, 1, 2, 1200, None),
+    (192, 6, 1, 33, 900, None)])
+def test_bf16_attention_adds_no_error_to_the_rounding_of_its_result(dim, heads, kv_heads, rows, length, width):
+    """The error of a weight shrinks with the tokens as the result does, so what counts is its share: with 16
+    bits at most 2^-16 of a weight, and about sqrt(dim) 2^-24 of the scores' sizes, which is below 2^-13 here, it is a
+    32nd of the rounding's 2^-8, and a thousandth of the sum of squares.  5% are allowed; weights of 8 bits make 40%."""
+    log(f"bf16 precision D={dim} {rows} rows over {length}")
+    rng = np.random.default_rng(dim + rows)
+    lay = ko.Layout(heads, kv_heads, dim, 32)
+    plan = Plan(lay, [rows], [length], rng, width=width)
+    cache = plan.filled_cache(rng)
+    q, q64 = rounded(rng.standard_normal((rows, heads, dim)), "bf16")
+    out = torch.empty_like(q)
+    svr.moe_kv_attention(desc_of(lay), plan.batch(), q, dev(cache), out)
+    ref, *_ = ko.attention(lay, cache, plan.offsets, plan.lens, plan.table, q64)
+    rounding = torch.from_numpy(ref).bfloat16().double().numpy() - ref
+    err = out.double().cpu().numpy() - ref
+    share = np.sqrt(np.mean(err ** 2) / np.mean(rounding ** 2))
+    log(f"  error over rounding {share:.4f}")
+    assert share <= 1.05
