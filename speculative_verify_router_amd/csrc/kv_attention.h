@@ -76,7 +76,7 @@ struct AttnArgs {
   float2* part_ml;
   unsigned* ctr;  // [sequence][row tile][key/value head] parts made, or NULL: a second kernel joins
   float c;         // scale * log2(e)
-  int row_tiles, min_tiles, by_seq;
+  int row_tiles, min_tiles, by_seq, search;
   // Query heads a key/value head; row tiles of a sequence; splits at most;
   // Hk; work of a head that runs at once; row tiles side by side on an XCD;
   // max_rows.
@@ -175,16 +175,31 @@ __device__ __forceinline__ KvRows kv_lane_rows(const AttnArgs& a, int b) {
   if (b < a.kv.n_seqs) s = kv_rows(a.kv, b);
   return s;
 }
-// Whether workgroups look their work up in the sequences' counts: not where
-// there is one sequence, or one row tile and no split of each.  (A lookup
-// passes over 64 sequences at a time; thousands of them are not split, and
-// their missing row tiles cost less.)
-constexpr int kMostListed = 1024;
-__host__ __device__ __forceinline__ bool kv_listed(int n_seqs, int tiles, int splits) {
-  return n_seqs > 1 && (splits > 1 || (tiles > 1 && n_seqs <= kMostListed));
+// Whether workgroups look their work up in the sequences' counts, 64 at a
+// time: where a batch of several is split.
+__host__ __device__ __forceinline__ bool kv_listed(int n_seqs, int splits) { return n_seqs > 1 && splits > 1; }
+__device__ __forceinline__ bool kv_listed(const AttnArgs& a) { return kv_listed(a.kv.n_seqs, a.splits.d); }
+
+// Row tiles of all sequences in one row, with no counting: those of sequence b
+// begin at floor(offs[b] G / span) + b, which leaves room for all of them (and
+// for one more at most), so there are n_tokens G / span + n_seqs at most, and
+// the sequence of one is found among the offsets alone, by a search that probes
+// 64 at a time.  With max_rows row tiles for each sequence instead, one prompt
+// of 2048 rows among 1024 single ones (200 to 3000 tokens) takes 4.8 ms, not 0.8.
+__device__ __forceinline__ int kv_first_tile(const AttnArgs& a, int off, int b) {
+  return (int)((uint32_t)off * (uint32_t)a.G.d >> (a.row_tiles == 2 ? 5 : 4)) + b;
 }
-__device__ __forceinline__ bool kv_listed(const AttnArgs& a) {
-  return kv_listed(a.kv.n_seqs, a.tiles.d, a.splits.d);
+__device__ __forceinline__ int kv_sequence_of_tile(const AttnArgs& a, int at) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int lo = 0, n = a.kv.n_seqs;
+  while (n > 1) {
+    const int step = (n + kWave - 1) / kWave, i = lane * step;
+    const bool below = i < n && kv_first_tile(a, a.kv.offs[lo + i], lo + i) <= at;
+    const int last = max(__popcll(__ballot(below)) - 1, 0);
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
 }
 // s: the lane's sequence, of the first 64.
 __device__ __forceinline__ int kv_per(const AttnArgs& a, const KvRows& s) {
@@ -373,7 +388,12 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
   }
   int b, tile, split = 0, per = kWholeRange;
   KvRows sq;
-  if (!kv_listed(a)) {  // as many splits, and row tiles, of each sequence
+  if (a.search) {
+    b = kv_sequence_of_tile(a, at);
+    sq = kv_rows(a.kv, b);
+    tile = at - kv_first_tile(a, sq.off, b);
+    if (tile < 0) return;  // offsets that are not ascending
+  } else if (!kv_listed(a)) {  // as many splits, and row tiles, of each sequence
     b = a.tiles.of(at);
     tile = at - b * a.tiles.d;
     if (a.kv.n_seqs == 1) {

@@ -109,7 +109,7 @@ void launch_kv_join(const AttnArgs& a, int32_t dtype, unsigned n, hipStream_t st
 
 // How a batch is cut, as far as its sizes say (the lengths are on the device).
 struct AttnPlan {
-  int row_tiles, tiles, waves, splits, min_tiles, share, group, by_seq;
+  int row_tiles, tiles, waves, splits, min_tiles, share, group, by_seq, search;
   bool join_here;
   int64_t part_rows;
   int64_t grid;
@@ -146,8 +146,9 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   const int span = 16 * p.row_tiles;
   p.tiles = (int)((rows + span - 1) / span);
   int64_t all = (int64_t)b->n_seqs * p.tiles;
-  const int64_t dense = ((int64_t)b->n_tokens * G + span - 1) / span + b->n_seqs;
-  all = all < dense ? all : dense;
+  const int64_t dense = (int64_t)b->n_tokens * G / span + b->n_seqs;  // see kv_first_tile
+  const bool uneven = all > dense;
+  all = uneven ? dense : all;
   // Larger workgroups make fewer parts: 4 rows over 60000 tokens 32.0 us (34.4
   // with four waves), 15000 tokens 20.4 (21.5); but a part of 64 rows over
   // 16384, of which there are two, takes 106 us (96), 4 rows over 4000 tokens
@@ -158,8 +159,9 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
     attn_split(p, d, b, dtype, all);
   }
   p.group = p.tiles < 64 ? p.tiles : 64;
-  const int64_t list = !kv_listed(b->n_seqs, p.tiles, p.splits) ? (int64_t)b->n_seqs * p.splits * p.tiles
-                       : p.splits == 1 ? all : p.share + all;
+  const bool listed = kv_listed(b->n_seqs, p.splits);
+  p.search = uneven && !listed && b->n_seqs > 1;
+  const int64_t list = listed ? p.share + all : all * p.splits;
   p.grid = ((list + p.group - 1) / p.group * d->n_kv_heads + 7) / 8 * 8 * p.group;
   const int64_t most_rows = (int64_t)b->n_seqs * b->max_rows;
   p.by_seq = most_rows < b->n_tokens;
@@ -238,6 +240,7 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
   a.min_tiles = p.min_tiles;
   a.row_tiles = p.row_tiles;
   a.by_seq = p.by_seq;
+  a.search = p.search;
   a.rows = make_divider(batch->max_rows);
   hipStream_t st = (hipStream_t)hip_stream;
   (void)hipGetLastError();

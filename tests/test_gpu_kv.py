@@ -562,3 +562,46 @@ def test_bf16_attention_adds_no_error_to_the_rounding_of_its_result(dim, heads, 
     share = np.sqrt(np.mean(err ** 2) / np.mean(rounding ** 2))
     log(f"  error over rounding {share:.4f}")
     assert share <= 1.05
+
+
+def check_attention_of(lay, plan, cache, dtype, rng, picks, ws=None):
+    """check_attention of a large batch, with the oracle on the sequences `picks` only."""
+    q, q64 = rounded(rng.standard_normal((plan.T, lay.heads, lay.dim)), dtype)
+    out = torch.full_like(q, 77.0)
+    svr.moe_kv_attention(desc_of(lay), plan.batch(), q, dev(cache), out, ws=ws)
+    got = out.double().cpu().numpy()
+    assert (got[plan.offsets[-1]:] == 77).all() and not (got[:plan.offsets[-1]] == 77).any()
+    for b in picks:
+        r = slice(plan.offsets[b], plan.offsets[b + 1])
+        ref, _, size, reach, seen = ko.attention(lay, cache, [0, r.stop - r.start], plan.lens[b:b + 1],
+                                                 plan.table[b:b + 1], q64[r])
+        err = np.abs(got[r] - ref)
+        assert np.all(err <= attention_tolerance(dtype, ref, size, reach, seen, lay.dim)), (b, np.nanmax(err))
+
+
+@pytest.mark.parametrize("seqs,heads,kv_heads,rows", [(1100, 6, 3, 500), (1024, 8, 1, 700), (300, 10, 2, 900),
+                                                      (5, 15, 3, 500)])
+def test_attention_of_a_prompt_among_many_sequences(seqs, heads, kv_heads, rows):
+    """More row tiles than lie side by side (64), of one sequence or two; heads that do not divide the dies."""
+    log(f"prompt of {rows} rows among {seqs}, {heads}/{kv_heads}")
+    rng = np.random.default_rng(seqs + rows)
+    lay = ko.Layout(heads, kv_heads, 64, 16)
+    r = rng.integers(0, 3, seqs)
+    r[seqs // 2], r[-1] = rows, rows // 3
+    plan = Plan(lay, list(r), list(r + rng.integers(0, 30, seqs)), rng, pad_rows=1)
+    picks = [seqs // 2, seqs - 1, 0, 1] + list(rng.integers(0, seqs, 40))
+    check_attention_of(lay, plan, plan.filled_cache(rng), "bf16", rng, picks)
+
+
+def test_attention_of_a_prompt_among_thousands_of_sequences():
+    """Row tiles of as many rows for every sequence would be more workgroups than a launch can have."""
+    rng = np.random.default_rng(61)
+    lay = ko.Layout(64, 4, 64, 16)
+    seqs, rows = 4100, 2048
+    assert seqs * (rows * 16 // 32) * 4 * 256 >= 2 ** 32
+    r, lens = np.ones(seqs, int), 1 + rng.integers(0, 4, seqs)
+    r[777], lens[777] = rows, rows + 20
+    plan = Plan(lay, list(r), list(lens), rng)
+    cache = rng.integers(0, 256, plan.empty_cache().shape).astype(np.uint8)
+    cache[..., 16 * 64:] = 126  # scales
+    check_attention_of(lay, plan, cache, "bf16", rng, [777, 0, 776, 778, seqs - 1] + list(rng.integers(0, seqs, 40)))
