@@ -139,7 +139,9 @@ int32_t moe_kv_attention_workspace_bytes(const moe_kv_desc* desc, const moe_kv_b
  * MOE_BF16, with 16 bits or more for MOE_F16, 24 for MOE_F32; the softmax weights
  * with 16 bits, 24 for MOE_F32.
  * Errors as moe_kv_append, and MOE_ERR_WORKSPACE for a workspace that is
- * too small, MOE_ERR_ARG for one that is not 256-byte aligned. */
+ * too small, MOE_ERR_ARG for one that is not 256-byte aligned, MOE_ERR_SHAPE
+ * for more work than a launch can take: a batch is always served where
+ * n_tokens * n_heads / 16 + n_seqs * n_kv_heads is at most 16 million. */
 int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int32_t dtype,
                          const void* q, int64_t q_stride, const void* cache, int32_t n_pages,
                          void* out, float* lse, void* workspace, size_t workspace_bytes,
@@ -147,7 +149,8 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
 
 /* The stored keys and values of the batch's rows as float
  * [n_tokens][n_kv_heads][D] (key NaN for a token stored as NaN; zeros where
- * nothing is stored).  k_out or v_out may be NULL. */
+ * nothing is stored).  k_out or v_out may be NULL.  MOE_ERR_SHAPE where
+ * n_tokens * ceil(n_kv_heads * D / 2048) is 2^24 or more. */
 int32_t moe_kv_read(const moe_kv_desc* desc, const moe_kv_batch* batch, const void* cache,
                     int32_t n_pages, float* k_out, float* v_out, void* hip_stream);
 

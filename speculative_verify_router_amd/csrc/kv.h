@@ -59,6 +59,9 @@ inline int32_t kv_check_batch(const moe_kv_desc* d, const moe_kv_batch* b, bool 
   return MOE_OK;
 }
 
+// A launch has fewer than 2^32 threads.
+inline bool kv_grid_fits(int64_t workgroups, int threads) { return workgroups < ((int64_t)1 << 32) / threads; }
+
 inline int64_t kv_page_bytes(const moe_kv_desc* d) {
   return (int64_t)d->page_size * (d->head_dim + d->head_dim / 16);
 }

@@ -500,15 +500,16 @@ int32_t moe_kv_read(const moe_kv_desc* desc, const moe_kv_batch* batch, const vo
   if (batch->n_tokens == 0 || batch->n_seqs == 0) return MOE_OK;
   if (!cache || (!k_out && !v_out)) return MOE_ERR_NULL;
   if ((uintptr_t)cache % 16 || ((uintptr_t)k_out | (uintptr_t)v_out) % 4) return MOE_ERR_ARG;
+  const int per_row = desc->n_kv_heads * (desc->head_dim / 8);
+  const int64_t grid = (int64_t)batch->n_tokens * ((per_row + kBlock - 1) / kBlock);
+  if (!kv_grid_fits(grid, kBlock)) return MOE_ERR_SHAPE;
   ReadArgs a{};
   a.kv = kv_args(desc, batch, n_pages);
   a.cache = (const uint8_t*)cache;
   a.k_out = k_out;
   a.v_out = v_out;
-  const int per_row = desc->n_kv_heads * (desc->head_dim / 8);
-  const int grid = batch->n_tokens * ((per_row + kBlock - 1) / kBlock);
   (void)hipGetLastError();
-  hipLaunchKernelGGL(k_kv_read, dim3(grid), dim3(kBlock), 0, (hipStream_t)hip_stream, a);
+  hipLaunchKernelGGL(k_kv_read, dim3((unsigned)grid), dim3(kBlock), 0, (hipStream_t)hip_stream, a);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }
 

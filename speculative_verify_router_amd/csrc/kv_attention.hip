@@ -213,7 +213,7 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
   if (((uintptr_t)q | (uintptr_t)out) % es || (uintptr_t)lse % 4 || (uintptr_t)cache % 16)
     return MOE_ERR_ARG;
   const AttnPlan p = attn_plan(desc, batch, dtype);
-  if (p.grid > INT32_MAX) return MOE_ERR_SHAPE;
+  if (!kv_grid_fits(p.grid, p.waves * kWave)) return MOE_ERR_SHAPE;
   if (p.bytes) {
     if (!workspace) return MOE_ERR_NULL;
     if (workspace_bytes < p.bytes) return MOE_ERR_WORKSPACE;

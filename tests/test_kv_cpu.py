@@ -299,3 +299,15 @@ def test_attention_of_nothing_needs_no_workspace(seqs, rows, max_rows):
     batch = svr.KvBatch(torch.zeros(seqs + 1, **i32), torch.zeros(seqs, **i32),
                         torch.zeros((seqs, 9), **i32), max_rows)
     assert svr.moe_kv_attention_workspace_bytes(kv_desc(), batch, rows) == 0
+
+
+def test_more_work_than_a_launch_can_take_is_refused():
+    """2^32 threads or more: a launch would be refused, after the checks."""
+    wide = dict(n_heads=1024, n_kv_heads=1024, head_dim=256)
+    many = kv_batch(n_seqs=65536, n_tokens=65536, max_rows=1)
+    assert 65536 * 1024 * 256 >= 2 ** 32
+    assert attention_status(desc=kv_desc(**wide), batch=many, qs=1024 * 256) == B.ERR_SHAPE
+    long = kv_batch(n_seqs=1, n_tokens=2 ** 20, max_rows=2 ** 20)
+    assert 2 ** 20 * 1024 // 32 * 256 >= 2 ** 32
+    assert attention_status(desc=kv_desc(n_heads=1024, n_kv_heads=64), batch=long, qs=1024 * 128) == B.ERR_SHAPE
+    assert read_status(desc=kv_desc(**wide), batch=long) == B.ERR_SHAPE
