@@ -69,14 +69,19 @@ struct AttnArgs {
   const uint8_t* cache;
   void* out;
   float* lse;
-  // [part row][head][split][D] sums not yet divided, and [..][split]: maximum
-  // (base 2), sum.  A part row is a row of the batch, or row m of sequence b
-  // as b * max_rows + m where those are fewer (a padded batch).
+  // Parts: D sums not yet divided, and their maximum (base 2) and sum.  Where
+  // the workgroup that makes the last one joins them, [part][key/value head]
+  // [row of the row tile]: only row tiles that are cut have parts, so there are
+  // at most two for each piece of work that runs at once, whatever the batch
+  // is.  For a second kernel, [part row][head][split]; a part row is a row of
+  // the batch, or row m of sequence b as b * max_rows + m where those are fewer
+  // (a padded batch).
   float* part_o;
   float2* part_ml;
-  unsigned* ctr;  // [sequence][row tile][key/value head] parts made, or NULL: a second kernel joins
+  unsigned* ctr;  // [row tile that is cut][key/value head] parts made, or NULL: a second kernel joins
   float c;         // scale * log2(e)
   int row_tiles, min_tiles, by_seq, search;
+  int first, extra;  // row tiles of all sequences; room for parts behind the first ones
   // Query heads a key/value head; row tiles of a sequence; splits at most;
   // Hk; work of a head that runs at once; row tiles side by side on an XCD;
   // max_rows.
@@ -170,16 +175,10 @@ __device__ __forceinline__ KvCut kv_cut(const AttnArgs& a, const KvRows& s) {
   return c;
 }
 __device__ __forceinline__ KvRows kv_lane_rows(const AttnArgs& a, int b) {
-  KvRows s{0, 0, 0, 0};
-  if (a.kv.n_seqs == 1) return kv_rows(a.kv, 0);  // in every lane
-  if (b < a.kv.n_seqs) s = kv_rows(a.kv, b);
+  KvRows s = kv_rows(a.kv, min(b, a.kv.n_seqs - 1));  // with no branch, so that several can be asked for at once
+  if (b >= a.kv.n_seqs && a.kv.n_seqs > 1) s = KvRows{0, 0, 0, 0};  // (one sequence: in every lane)
   return s;
 }
-// Whether workgroups look their work up in the sequences' counts, 64 at a
-// time: where a batch of several is split.
-__host__ __device__ __forceinline__ bool kv_listed(int n_seqs, int splits) { return n_seqs > 1 && splits > 1; }
-__device__ __forceinline__ bool kv_listed(const AttnArgs& a) { return kv_listed(a.kv.n_seqs, a.splits.d); }
-
 // Row tiles of all sequences in one row, with no counting: those of sequence b
 // begin at floor(offs[b] G / span) + b, which leaves room for all of them (and
 // for one more at most), so there are n_tokens G / span + n_seqs at most, and
@@ -201,8 +200,11 @@ __device__ __forceinline__ int kv_sequence_of_tile(const AttnArgs& a, int at) {
   }
   return lo;
 }
-// s: the lane's sequence, of the first 64.
-__device__ __forceinline__ int kv_per(const AttnArgs& a, const KvRows& s) {
+// Tiles of a split, and the most of a sequence.  s: the lane's sequence, of the first 64.
+struct KvPer {
+  int per, most;
+};
+__device__ __forceinline__ KvPer kv_per_most(const AttnArgs& a, const KvRows& s) {
   int64_t all = 0;
   int most = 0;
   if (a.kv.n_seqs == 1) {
@@ -212,8 +214,11 @@ __device__ __forceinline__ int kv_per(const AttnArgs& a, const KvRows& s) {
   } else {
     int64_t work = 0;
     const int lane = threadIdx.x & (kWave - 1);
+    KvRows now = s;
     for (int b = 0; b < a.kv.n_seqs; b += kWave) {
-      const KvCut c = kv_cut(a, b ? kv_lane_rows(a, b + lane) : s);
+      const KvRows next = kv_lane_rows(a, b + kWave + lane);
+      const KvCut c = kv_cut(a, now);
+      now = next;
       work += (int64_t)c.row_tiles * c.tiles;
       most = max(most, c.tiles);
     }
@@ -225,7 +230,27 @@ __device__ __forceinline__ int kv_per(const AttnArgs& a, const KvRows& s) {
   const int shift = max(0, 34 - (int)__builtin_clzll(all | 1));
   const int64_t fair = (int64_t)(a.share.of((int)(all >> shift) + a.share.d - 1) + (shift ? 1 : 0)) << shift;
   const int per = max(a.min_tiles, max((int)min(fair, (int64_t)kWholeRange), a.splits.of(most + a.splits.d - 1)));
-  return most <= 3 * a.min_tiles ? max(per, most) : per;  // four rounds of the waves take as long as joining
+  return KvPer{most <= 3 * a.min_tiles ? max(per, most) : per, most};  // four rounds of the waves take as long as joining
+}
+__device__ __forceinline__ int kv_per(const AttnArgs& a, const KvRows& s) { return kv_per_most(a, s).per; }
+
+
+// Parts of a sequence's row tiles behind their first ones.  All sequences have
+// fewer than a.extra: a part is at least (work of a head) / share tiles.
+__device__ __forceinline__ int kv_extra(const KvCut& c, int per) { return c.row_tiles * ((c.tiles - 1) / per); }
+// Those of the sequences before b.  s: the lane's sequence, of the first 64.
+__device__ __forceinline__ int kv_extra_before(const AttnArgs& a, int b, int per, KvRows s) {
+  int before = 0;
+  for (int b0 = 0;; b0 += kWave) {
+    if (b0) s = kv_lane_rows(a, b0 + (threadIdx.x & (kWave - 1)));
+    const int n = kv_extra(kv_cut(a, s), per), upto = wave_scan<false>(n);
+    if (b < b0 + kWave) return before + __builtin_amdgcn_readlane(upto, b - b0) - __builtin_amdgcn_readlane(n, b - b0);
+    before += __builtin_amdgcn_readlane(upto, kWave - 1);
+  }
+}
+__device__ __forceinline__ KvRows kv_rows_of_lane(const KvRows& s, int l) {
+  return KvRows{__builtin_amdgcn_readlane(s.off, l), __builtin_amdgcn_readlane(s.rows, l),
+                __builtin_amdgcn_readlane(s.len, l), __builtin_amdgcn_readlane(s.place0, l)};
 }
 
 // The tokens [beg, end) that rows of places [first, last] see, in tiles from
@@ -375,9 +400,11 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
   const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
 
-  // Work of a head is a list: sequences, their splits, the row tiles of a
-  // split.  Heads go round the XCDs, and a group of row tiles, which read the
-  // same tokens, lies eight workgroups apart, on one XCD, and shares its L2.
+  // Work of a head is a list: the row tiles of all sequences, with the first
+  // part of the tokens of each, then the other parts of those that are cut:
+  // sequences, their splits, the row tiles of a split.  Heads go round the
+  // XCDs, and a group of row tiles, which read the same tokens, lies eight
+  // workgroups apart, on one XCD, and shares its L2.
   const int G = a.G.d;
   int kvh, at;
   {
@@ -386,58 +413,76 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
     kvh = u - n * a.heads.d;
     at = n * a.group.d + v - y * a.group.d;
   }
-  int b, tile, split = 0, per = kWholeRange;
+  const bool cut = a.splits.d > 1;
+  int b = 0, tile, split = 0, per = kWholeRange;
+  int before = 0, apart = a.tiles.d;  // parts of the sequences before b; between those of a row tile
   KvRows sq;
-  if (a.search) {
-    b = kv_sequence_of_tile(a, at);
-    sq = kv_rows(a.kv, b);
-    tile = at - kv_first_tile(a, sq.off, b);
-    if (tile < 0) return;  // offsets that are not ascending
-  } else if (!kv_listed(a)) {  // as many splits, and row tiles, of each sequence
-    b = a.tiles.of(at);
-    tile = at - b * a.tiles.d;
-    if (a.kv.n_seqs == 1) {
-      split = b;
-      b = 0;
+  if (a.kv.n_seqs == 1) {  // as many splits of every row tile
+    split = a.tiles.of(at);
+    tile = at - split * a.tiles.d;
+    if (split >= a.splits.d) return;
+    sq = kv_rows(a.kv, 0);
+    if (cut) per = kv_per(a, sq);
+  } else if (at < a.first) {
+    KvRows s{0, 0, 0, 0};
+    if (cut) s = kv_lane_rows(a, lane);  // asked for with the sequence's own
+    if (a.search) {
+      b = kv_sequence_of_tile(a, at);
+      sq = kv_rows(a.kv, b);
+      tile = at - kv_first_tile(a, sq.off, b);
+      if (tile < 0) return;  // offsets that are not ascending
+    } else {
+      b = a.tiles.of(at);
+      tile = at - b * a.tiles.d;
+      sq = kv_rows(a.kv, b);
     }
-    if (b >= a.kv.n_seqs || split >= a.splits.d) return;
-    sq = kv_rows(a.kv, b);
-    if (a.splits.d > 1) per = kv_per(a, sq);
+    const KvCut c = kv_cut(a, sq);
+    if (cut && c.tiles > a.min_tiles) {  // others are whole, whatever `per` is
+      per = kv_per(a, s);
+      if (a.ctr && c.tiles > per) before = kv_extra_before(a, b, per, s);
+      apart = c.row_tiles;
+    }
   } else {
+    at -= a.first;
+    if (!cut || at >= a.extra) return;
     KvRows s = kv_lane_rows(a, lane);
-    if (a.splits.d > 1) per = kv_per(a, s);
-    for (b = 0;; b += kWave) {
+    const KvPer p = kv_per_most(a, s);
+    per = p.per;
+    if (p.most <= per) return;  // nothing is cut
+    for (;; b += kWave) {
       if (b >= a.kv.n_seqs) return;
       if (b) s = kv_lane_rows(a, b + lane);
       const KvCut c = kv_cut(a, s);
-      const int splits = max(1, (int)((unsigned)(c.tiles + per - 1) / (unsigned)per));
-      const int n = c.row_tiles * splits, upto = wave_scan<false>(n);
-      const uint64_t past = __ballot(upto > at);
+      const int n = kv_extra(c, per), upto = wave_scan<false>(n);
+      const uint64_t past = __ballot(before + upto > at);
       if (!past) {
-        at -= __builtin_amdgcn_readlane(upto, kWave - 1);
+        before += __builtin_amdgcn_readlane(upto, kWave - 1);
         continue;
       }
       const int l = __builtin_ctzll(past);
       b += l;
-      at -= __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l);
-      const int row_tiles = __builtin_amdgcn_readlane(c.row_tiles, l);
-      split = at / row_tiles;
-      tile = at - split * row_tiles;
-      sq.off = __builtin_amdgcn_readlane(s.off, l);
-      sq.rows = __builtin_amdgcn_readlane(s.rows, l);
-      sq.len = __builtin_amdgcn_readlane(s.len, l);
-      sq.place0 = __builtin_amdgcn_readlane(s.place0, l);
+      before += __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l);
+      apart = __builtin_amdgcn_readlane(c.row_tiles, l);
+      split = (at - before) / apart;
+      tile = at - before - split * apart;
+      ++split;
+      sq = kv_rows_of_lane(s, l);
       break;
     }
   }
 
   const int row_total = sq.rows * G, r0 = tile * 16 * RT;
-  if (r0 >= row_total) return;
+  if ((unsigned)r0 >= (unsigned)row_total) return;
   const int r_last = min(row_total, r0 + 16 * RT) - 1;
   const int first = sq.place0 + a.G.of(r0), last = sq.place0 + a.G.of(r_last);
   const KvRange rg = kv_range(a, sq.len, first, last, per);
   if (!rg.uses(split)) return;
-  const int t_end = min(rg.ntile, (split + 1) * rg.per), t_last = t_end - 1;
+  // The first part is what whole ones leave at the end: those behind it in the
+  // list are then all alike, and share the chip evenly whatever their order.
+  // (72 sequences of 2000 tokens 36 us, 44 with the rests among them.)
+  const int used = rg.whole() ? 1 : (int)((unsigned)(rg.ntile + rg.per - 1) / (unsigned)rg.per);
+  const int t_begin = (split ? split - 1 : used - 1) * rg.per;
+  const int t_end = min(rg.ntile, t_begin + rg.per), t_last = t_end - 1;
 
   // Sixteen tokens (a run) lie in one page.  A run outside [beg, end) becomes
   // one inside; what lies in a run outside of it is dropped.
@@ -462,7 +507,7 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
   // One tile of codes is kept in flight: keys of the next tile are asked for
   // as soon as this tile's are widened, values likewise, page numbers a tile
   // before that.
-  int t = split * rg.per + wv;
+  int t = t_begin + wv;
   int page[2], next_page[2];
   Codes<D> kc[2], vc[2];
   if (t < t_end) {
@@ -635,6 +680,16 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
     }
   }
 
+  // Where row r of the row tile has a part, and its output.
+  auto out_at = [&](int r) {
+    const int rm = a.G.of(r0 + r);
+    return (int64_t)(sq.off + rm) * a.kv.Hq + kvh * G + r0 + r - rm * G;
+  };
+  auto part_at = [&](int split, int r) {
+    const int part = (split ? (split - 1) * apart : a.extra) + before + tile;
+    return ((int64_t)part * a.kv.Hk + kvh) * (16 * RT) + r;
+  };
+
   // Join the waves: sums over the common maximum, a row tile at a time.
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
@@ -673,8 +728,7 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
           v[j] = w ? v[j] + x : x;
         }
       }
-      const int rm = a.G.of(r);
-      const int64_t at = (int64_t)(sq.off + rm) * a.kv.Hq + kvh * G + r - rm * G;
+      const int64_t at = out_at(r - r0);
       if (rg.whole()) {
         const float inv = L == 0.f ? 0.f : 1.f / L;
         T* out = (T*)a.out + at * D + jc;
@@ -684,8 +738,13 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
         if (jc == 0 && a.lse)
           a.lse[at] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.6931471805599453f;
       } else {
-        const int64_t row = a.by_seq ? (int64_t)b * a.kv.max_rows + rm : sq.off + rm;
-        const int64_t pt = (row * a.kv.Hq + kvh * G + r - rm * G) * a.splits.d + split;
+        int64_t pt;
+        if (a.ctr) {
+          pt = part_at(split, r - r0);
+        } else {
+          const int64_t to_seq = a.by_seq ? (int64_t)b * a.kv.max_rows - sq.off : 0;
+          pt = (at + to_seq * a.kv.Hq) * a.splits.d + split;
+        }
         float* part = a.part_o + pt * D + jc;
 #pragma unroll
         for (int j = 0; j < kReads; ++j)
@@ -709,55 +768,45 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
   wait_stores();
   __syncthreads();
   bool* s_last = reinterpret_cast<bool*>(s_ml);
-  const int used = (int)((unsigned)(rg.ntile + per - 1) / (unsigned)per);
-  unsigned* ctr = a.ctr + ((int64_t)b * a.tiles.d + tile) * a.kv.Hk + kvh;
+  unsigned* ctr = a.ctr + (before + tile) * a.kv.Hk + kvh;
   if (threadIdx.x == 0) *s_last = arrive(ctr) == (unsigned)(used - 1);
   __syncthreads();
   if (!*s_last) return;
   if (threadIdx.x == 0) store_shared(ctr, 0u);
-  // Where row r of the tile has its parts and its output.
-  auto places = [&](int r, int64_t& pt, int64_t& to) {
-    const int rm = a.G.of(r), h = kvh * G + r - rm * G;
-    to = (int64_t)(sq.off + rm) * a.kv.Hq + h;
-    pt = (a.by_seq ? ((int64_t)b * a.kv.max_rows + rm) * a.kv.Hq + h : to) * a.splits.d;
-  };
   float* s_w = join;  // [row][part]: w_s / sum
   for (int n = threadIdx.x; n < RT * 16 * kJoinHere; n += W * kWave) {
     static_assert(kJoinHere == 16, "a row's parts are a row of lanes");
     const int row = n / kJoinHere, part = n % kJoinHere;
     float2 ml = make_float2(-INFINITY, 0.f);
-    int64_t at = 0, lse_at = 0;
     const bool on = r0 + row < row_total;
-    if (on) {
-      places(r0 + row, at, lse_at);
-      if (part < used) ml = __builtin_bit_cast(float2, load_shared((const uint64_t*)a.part_ml + at + part));
-    }
+    if (on && part < used)
+      ml = __builtin_bit_cast(float2, load_shared((const uint64_t*)a.part_ml + part_at(part, row)));
     const float M = row16_max(ml.x), w = ml.x == M ? 1.f : __builtin_amdgcn_exp2f(ml.x - M);
     const float L = row16_sum(w * ml.y);
     s_w[n] = L == 0.f ? 0.f : w / L;
     if (on && part == 0 && a.lse)
-      a.lse[lse_at] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.6931471805599453f;
+      a.lse[out_at(row)] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.6931471805599453f;
   }
   __syncthreads();
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int row = 16 * rt + jr;
     if (r0 + row >= row_total) continue;
-    int64_t pt, to;
-    places(r0 + row, pt, to);
     f32x4v v[kReads];
 #pragma unroll
     for (int j = 0; j < kReads; ++j) v[j] = f32x4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int part = 0; part < used; ++part) {
       const float w = s_w[row * kJoinHere + part];
+      const float* from = a.part_o + part_at(part, row) * D + jc;
 #pragma unroll
       for (int j = 0; j < kReads; ++j)
-        if (has(j)) v[j] += w * load_part(a.part_o + (pt + part) * D + jc + kSpan * j);
+        if (has(j)) v[j] += w * load_part(from + kSpan * j);
     }
+    T* out = (T*)a.out + out_at(row) * D + jc;
 #pragma unroll
     for (int j = 0; j < kReads; ++j)
-      if (has(j)) store4((T*)a.out + to * D + jc + kSpan * j, v[j]);
+      if (has(j)) store4(out + kSpan * j, v[j]);
   }
 }
 

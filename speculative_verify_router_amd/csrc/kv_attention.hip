@@ -109,7 +109,7 @@ void launch_kv_join(const AttnArgs& a, int32_t dtype, unsigned n, hipStream_t st
 
 // How a batch is cut, as far as its sizes say (the lengths are on the device).
 struct AttnPlan {
-  int row_tiles, tiles, waves, splits, min_tiles, share, group, by_seq, search;
+  int row_tiles, tiles, waves, splits, min_tiles, share, group, by_seq, search, first, extra;
   bool join_here;
   int64_t part_rows;
   int64_t grid;
@@ -120,21 +120,36 @@ struct AttnPlan {
 // Returns whether row tiles are few, and tables long, enough for four splits
 // or more and as many as there is room for.
 bool attn_split(AttnPlan& p, const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype, int64_t all) {
-  p.min_tiles = p.waves;  // a tile a wave
+  // A part is a tile a wave at least, and as many more for every 64 sequences
+  // behind the first, which a workgroup passes over to find it.
+  p.min_tiles = p.waves * (1 + (b->n_seqs - 1) / kWave);
   // Work of a head that runs at once.
   const int resident = attn_waves(d->head_dim, p.row_tiles, attn_terms(dtype)) * kAttnWaves / p.waves;
   const int slots = 256 * resident / d->n_kv_heads;
-  // Every sequence's last split is half full on the average.
-  p.share = (int)(slots - all / 2 > slots / 2 ? slots - all / 2 : slots / 2);
+  // Every row tile has one part that is half full on the average.  Where two of
+  // each are more than run at once, even sequences are not cut: 97 of 2000
+  // tokens 35 us (46 in halves), and longer ones into parts of the mean.
+  int64_t share = slots - all / 2;
+  if (2 * all > slots && share > all) share = all;
+  p.share = (int)(share > slots / 2 ? share : slots / 2);
   p.share = p.share > 0 ? p.share : 1;
   int64_t seen = (int64_t)b->pages_per_seq * d->page_size;
   if (d->window && d->window + (int64_t)b->max_rows < seen) seen = d->window + (int64_t)b->max_rows;
-  const int64_t most = (seen / kAttnTile + 2 + p.min_tiles - 1) / p.min_tiles;
-  // One sequence gets all splits, several up to four times their even part.
-  int64_t s = 2 * all > slots ? 1 : b->n_seqs == 1 ? slots / all : (4 * slots + all - 1) / all;
-  s = s > kMaxSplits ? kMaxSplits : s;
-  p.splits = (int)(s < most ? s : most);
-  return slots / all >= 4 && s <= most;
+  const int64_t tiles = seen / kAttnTile + 2, most = (tiles + p.min_tiles - 1) / p.min_tiles;
+  if (b->n_seqs == 1) {
+    const int64_t s = 2 * all > slots ? 1 : slots / all;
+    p.splits = (int)(s < kMaxSplits ? s : kMaxSplits);
+  } else {
+    // Several sequences get up to four times their even part, and sixteen at
+    // least: how many are in use goes by the lengths, and a batch of even ones
+    // is not cut where there are as many as run at once.  One sequence of 60000
+    // tokens among 127 of up to 3000: 69 us, 523 if it is not cut.
+    const int64_t s = (4 * (int64_t)slots + all - 1) / all;
+    p.splits = tiles <= 3 * p.min_tiles ? 1 : s < kJoinHere ? kJoinHere : s < kMaxSplits ? (int)s : kMaxSplits;
+  }
+  const bool room = p.splits > 1 && p.splits <= most;
+  p.splits = p.splits < most ? p.splits : (int)most;
+  return slots / all >= 4 && room;
 }
 
 AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
@@ -147,8 +162,8 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   p.tiles = (int)((rows + span - 1) / span);
   int64_t all = (int64_t)b->n_seqs * p.tiles;
   const int64_t dense = (int64_t)b->n_tokens * G / span + b->n_seqs;  // see kv_first_tile
-  const bool uneven = all > dense;
-  all = uneven ? dense : all;
+  p.search = all > dense;
+  all = p.search ? dense : all;
   // Larger workgroups make fewer parts: 4 rows over 60000 tokens 32.0 us (34.4
   // with four waves), 15000 tokens 20.4 (21.5); but a part of 64 rows over
   // 16384, of which there are two, takes 106 us (96), 4 rows over 4000 tokens
@@ -159,18 +174,19 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
     attn_split(p, d, b, dtype, all);
   }
   p.group = p.tiles < 64 ? p.tiles : 64;
-  const bool listed = kv_listed(b->n_seqs, p.splits);
-  p.search = uneven && !listed && b->n_seqs > 1;
-  const int64_t list = listed ? p.share + all : all * p.splits;
-  p.grid = ((list + p.group - 1) / p.group * d->n_kv_heads + 7) / 8 * 8 * p.group;
+  p.first = (int)all;
+  p.extra = p.splits == 1 ? 0 : b->n_seqs == 1 ? (int)all * (p.splits - 1) : p.share;
+  p.grid = ((all + p.extra + p.group - 1) / p.group * d->n_kv_heads + 7) / 8 * 8 * p.group;
   const int64_t most_rows = (int64_t)b->n_seqs * b->max_rows;
   p.by_seq = most_rows < b->n_tokens;
   p.part_rows = p.by_seq ? most_rows : b->n_tokens;
   if (p.splits > 1) {
-    const size_t n = (size_t)p.part_rows * d->n_heads * p.splits;
+    p.join_here = p.splits <= kJoinHere;
+    const int first = b->n_seqs == 1 ? (int)all : p.extra;  // first parts lie as the ones behind them do
+    const size_t n = p.join_here ? (size_t)(p.extra + first) * d->n_kv_heads * span
+                                 : (size_t)p.part_rows * d->n_heads * p.splits;
     p.o_bytes = (n * d->head_dim * 4 + 255) & ~(size_t)255;
     p.bytes = kAttnCounters * sizeof(unsigned) + p.o_bytes + n * 8;
-    p.join_here = p.splits <= kJoinHere && (int64_t)b->n_seqs * p.tiles * d->n_kv_heads <= kAttnCounters;
   }
   return p;
 }
@@ -241,6 +257,8 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
   a.row_tiles = p.row_tiles;
   a.by_seq = p.by_seq;
   a.search = p.search;
+  a.first = p.first;
+  a.extra = p.extra;
   a.rows = make_divider(batch->max_rows);
   hipStream_t st = (hipStream_t)hip_stream;
   (void)hipGetLastError();

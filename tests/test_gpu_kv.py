@@ -564,19 +564,24 @@ def test_bf16_attention_adds_no_error_to_the_rounding_of_its_result(dim, heads, 
     assert share <= 1.05
 
 
-def check_attention_of(lay, plan, cache, dtype, rng, picks, ws=None):
+def check_attention_of(lay, plan, cache, dtype, rng, picks, ws=None, q=None):
     """check_attention of a large batch, with the oracle on the sequences `picks` only."""
-    q, q64 = rounded(rng.standard_normal((plan.T, lay.heads, lay.dim)), dtype)
+    q, q64 = rounded(rng.standard_normal((plan.T, lay.heads, lay.dim)), dtype) if q is None else q
     out = torch.full_like(q, 77.0)
     svr.moe_kv_attention(desc_of(lay), plan.batch(), q, dev(cache), out, ws=ws)
     got = out.double().cpu().numpy()
     assert (got[plan.offsets[-1]:] == 77).all() and not (got[:plan.offsets[-1]] == 77).any()
     for b in picks:
-        r = slice(plan.offsets[b], plan.offsets[b + 1])
-        ref, _, size, reach, seen = ko.attention(lay, cache, [0, r.stop - r.start], plan.lens[b:b + 1],
-                                                 plan.table[b:b + 1], q64[r])
-        err = np.abs(got[r] - ref)
-        assert np.all(err <= attention_tolerance(dtype, ref, size, reach, seen, lay.dim)), (b, np.nanmax(err))
+        first, end = int(plan.offsets[b]), int(plan.offsets[b + 1])
+        pieces = [(first, end)]
+        if end - first > 200:  # some rows of a prompt: as if they were the last ones
+            pieces = [(i, i + 40) for i in (first, (first + end) // 2, end - 40)]
+        for i, j in pieces:
+            ref, _, size, reach, seen = ko.attention(lay, cache, [0, j - i], plan.lens[b:b + 1] - (end - j),
+                                                     plan.table[b:b + 1], q64[i:j])
+            err = np.abs(got[i:j] - ref)
+            assert np.all(err <= attention_tolerance(dtype, ref, size, reach, seen, lay.dim)), (b, i, np.nanmax(err))
+    return got[:plan.offsets[-1]]
 
 
 @pytest.mark.parametrize("seqs,heads,kv_heads,rows", [(1100, 6, 3, 500), (1024, 8, 1, 700), (300, 10, 2, 900),
@@ -605,3 +610,48 @@ def test_attention_of_a_prompt_among_thousands_of_sequences():
     cache = rng.integers(0, 256, plan.empty_cache().shape).astype(np.uint8)
     cache[..., 16 * 64:] = 126  # scales
     check_attention_of(lay, plan, cache, "bf16", rng, [777, 0, 776, 778, seqs - 1] + list(rng.integers(0, seqs, 40)))
+
+
+@pytest.mark.parametrize("dtype,seqs,heads,kv_heads,dim,window,rows,length", [
+    ("bf16", 97, 8, 8, 64, 0, 1, 3000), ("f16", 300, 16, 4, 128, 0, 2, 4000), ("f32", 700, 8, 8, 64, 0, 1, 5000),
+    ("bf16", 100, 20, 4, 64, 0, 150, 3000), ("bf16", 130, 16, 8, 192, 2500, 3, 4000), ("f16", 64, 16, 16, 64, 0, 1, 2000),
+    ("bf16", 2, 16, 16, 64, 0, 1, 2000), ("f32", 66, 4, 4, 256, 0, 4, 2500)])
+def test_attention_of_a_long_sequence_among_many(dtype, seqs, heads, kv_heads, dim, window, rows, length):
+    """More sequences than run at once, of which a few are cut: each finds its parts among those of the others,
+    in a workspace that goes by neither their rows nor their number; again where none is long."""
+    log(f"long among many {dtype} D={dim} {seqs} of {heads}/{kv_heads} W={window}")
+    rng = np.random.default_rng(seqs + dim)
+    lay = ko.Layout(heads, kv_heads, dim, 16, window)
+    r = rng.integers(0, 3, seqs)
+    lens = r + rng.integers(0, 30, seqs)
+    long = sorted({0, seqs // 2, seqs - 1}) if seqs > 2 else [1]
+    for n, b in enumerate(long):
+        r[b], lens[b] = max(1, rows - n), length // (n + 1)
+    plan = Plan(lay, list(r), list(lens), rng, pad_rows=2)
+    cache = rng.integers(0, 256, plan.empty_cache().shape).astype(np.uint8)
+    cache[..., 16 * dim:] = rng.integers(124, 128, cache[..., 16 * dim:].shape)  # scales
+    n = svr.moe_kv_attention_workspace_bytes(desc_of(lay), plan.batch(), plan.T)
+    assert 0 < n < 2 ** 26
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:16384].zero_()
+    picks = sorted({*long, *rng.integers(0, seqs, 30).tolist()})
+    q = rounded(rng.standard_normal((plan.T, heads, dim)), dtype)
+    want = check_attention_of(lay, plan, cache, dtype, rng, picks, ws, q)
+    assert not ws[:16384].any()
+    full, plan.lens = plan.lens, np.minimum(plan.lens, 40).astype(np.int32)
+    check_attention_of(lay, plan, cache, dtype, rng, picks, ws)
+    plan.lens = full
+    assert np.array_equal(check_attention_of(lay, plan, cache, dtype, rng, [], ws, q), want)
+    assert not ws[:16384].any()
+
+
+@pytest.mark.parametrize("dtype,dim,window,lens", [
+    ("bf16", 256, 0, [2600]), ("f32", 256, 0, [2700, 400]), ("f16", 256, 0, [2600]), ("bf16", 192, 3000, [6000]),
+    ("f16", 128, 2500, [5000, 4000]), ("f32", 64, 4000, [9000])])
+def test_attention_of_parts_that_a_second_kernel_joins(dtype, dim, window, lens):
+    """More than sixteen parts a row, at every head size, and of rows whose window begins inside the tokens."""
+    log(f"second kernel {dtype} D={dim} W={window} {lens}")
+    rng = np.random.default_rng(dim + window)
+    lay = ko.Layout(4, 1, dim, 64, window)
+    plan = Plan(lay, [2] * len(lens), lens, rng, width=300)
+    check_attention(lay, plan, plan.filled_cache(rng), dtype, rng)

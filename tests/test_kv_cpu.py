@@ -311,3 +311,15 @@ def test_more_work_than_a_launch_can_take_is_refused():
     assert 2 ** 20 * 1024 // 32 * 256 >= 2 ** 32
     assert attention_status(desc=kv_desc(n_heads=1024, n_kv_heads=64), batch=long, qs=1024 * 128) == B.ERR_SHAPE
     assert read_status(desc=kv_desc(**wide), batch=long) == B.ERR_SHAPE
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(64, 4, 192), (32, 8, 128), (8, 8, 64), (16, 1, 256)])
+def test_sequences_of_a_long_table_can_be_cut_however_many_there_are(heads, kv_heads, dim):
+    """One long sequence among short ones must not be walked by a workgroup a head alone.  What parts need does not
+    go by the rows or sequences."""
+    d = kv_desc(n_heads=heads, n_kv_heads=kv_heads, head_dim=dim)
+    for seqs in (1, 2, 64, 65, 96, 97, 128, 200, 512, 1024, 1025, 4000):
+        out = ctypes.c_size_t()
+        b = kv_batch(n_seqs=seqs, n_tokens=seqs, max_rows=1, pages_per_seq=1000)
+        assert svr.lib().moe_kv_attention_workspace_bytes(d.c(), b, ctypes.byref(out)) == B.OK
+        assert 16384 < out.value < 2 ** 26, seqs
