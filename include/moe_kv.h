@@ -114,10 +114,9 @@ int32_t moe_kv_append(const moe_kv_desc* desc, const moe_kv_batch* batch, int32_
                       const float* inv_freq, const int32_t* positions, void* cache,
                       int32_t n_pages, void* q_out, void* hip_stream);
 
-/* Device workspace, in *bytes, of moe_kv_attention for this desc and the
- * sizes of this batch (the arrays may be NULL).  Other sizes need their own,
- * and smaller ones may need more (fewer rows are cut into more parts): for a
- * range of sizes, take the largest.  It begins with 16384 bytes of counters,
+/* Device workspace, in *bytes, of moe_kv_attention for this desc and every
+ * batch of at most these n_seqs, n_tokens, max_rows and pages_per_seq (the
+ * arrays may be NULL), 60 MB at most.  It begins with 16384 bytes of counters,
  * which must be zero before the first call that uses the workspace; every call
  * leaves them zero, so zero-fill a workspace once when it is allocated.  Calls
  * that share one must not overlap in time.  0 is possible, and then workspace

@@ -568,8 +568,8 @@ def moe_kv_attention_workspace_bytes(desc: KvDesc, batch: KvBatch, n_tokens: int
 
 
 def kv_workspace(desc: KvDesc, batch: KvBatch, n_tokens: int) -> torch.Tensor:
-    """A device workspace for moe_kv_attention on batches of this size (n_tokens rows), its
-    counters zeroed (calls keep them so)."""
+    """A device workspace for moe_kv_attention on batches of up to this size (sequences, rows of one,
+    table, n_tokens rows), its counters zeroed (calls keep them so)."""
     ws = torch.empty(moe_kv_attention_workspace_bytes(desc, batch, n_tokens), dtype=torch.uint8,
                      device=batch.page_table.device)
     ws[:KV_COUNTER_BYTES].zero_()

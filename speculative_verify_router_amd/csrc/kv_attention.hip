@@ -116,6 +116,13 @@ struct AttnPlan {
   size_t o_bytes, bytes;
 };
 
+// Tiles that a row can see by the batch's table and window.
+int64_t attn_seen_tiles(const moe_kv_desc* d, const moe_kv_batch* b) {
+  int64_t seen = (int64_t)b->pages_per_seq * d->page_size;
+  if (d->window && d->window + (int64_t)b->max_rows < seen) seen = d->window + (int64_t)b->max_rows;
+  return seen / kAttnTile + 2;
+}
+
 // The plan for workgroups of p.waves: the splits of `all` row tiles of a head.
 // Returns whether row tiles are few, and tables long, enough for four splits
 // or more and as many as there is room for.
@@ -133,9 +140,7 @@ bool attn_split(AttnPlan& p, const moe_kv_desc* d, const moe_kv_batch* b, int32_
   if (2 * all > slots && share > all) share = all;
   p.share = (int)(share > slots / 2 ? share : slots / 2);
   p.share = p.share > 0 ? p.share : 1;
-  int64_t seen = (int64_t)b->pages_per_seq * d->page_size;
-  if (d->window && d->window + (int64_t)b->max_rows < seen) seen = d->window + (int64_t)b->max_rows;
-  const int64_t tiles = seen / kAttnTile + 2, most = (tiles + p.min_tiles - 1) / p.min_tiles;
+  const int64_t tiles = attn_seen_tiles(d, b), most = (tiles + p.min_tiles - 1) / p.min_tiles;
   if (b->n_seqs == 1) {
     const int64_t s = 2 * all > slots ? 1 : slots / all;
     p.splits = (int)(s < kMaxSplits ? s : kMaxSplits);
@@ -191,6 +196,26 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   return p;
 }
 
+// What the plan of any batch of up to these sizes needs.  Row tiles times
+// splits are at most what runs at once for one sequence, 4 1/4 of that for
+// several (at most a quarter of it row tiles, each with a part too many); where
+// the last workgroup joins, twice p.share, which is at most what runs at once.
+size_t attn_most_bytes(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
+  if (b->n_seqs == 0 || b->n_tokens == 0 || b->max_rows == 0) return 0;
+  if (attn_seen_tiles(d, b) <= kAttnWaves) return 0;  // never cut
+  const int64_t rows = (int64_t)(b->max_rows < b->n_tokens ? b->max_rows : b->n_tokens) *
+                       (d->n_heads / d->n_kv_heads);
+  size_t most = 0;
+  for (int rt = 1; rt <= attn_row_tiles(rows, d->head_dim, dtype); ++rt) {
+    const int slots = 256 * attn_waves(d->head_dim, rt, attn_terms(dtype)) / d->n_kv_heads;
+    const int parts = b->n_seqs == 1 ? slots : slots < 1 ? 2 : 4 * slots + slots / 4;
+    const size_t n = (size_t)parts * d->n_kv_heads * 16 * rt;
+    const size_t bytes = kAttnCounters * sizeof(unsigned) + ((n * d->head_dim * 4 + 255) & ~(size_t)255) + n * 8;
+    most = bytes > most ? bytes : most;
+  }
+  return most;
+}
+
 }  // namespace
 }  // namespace svr
 
@@ -206,7 +231,7 @@ int32_t moe_kv_attention_workspace_bytes(const moe_kv_desc* desc, const moe_kv_b
   if (rc != MOE_OK) return rc;
   size_t most = 0;
   for (int32_t t : {MOE_F32, MOE_BF16, MOE_F16}) {
-    const size_t n = attn_plan(desc, batch, t).bytes;
+    const size_t n = attn_most_bytes(desc, batch, t);
     most = n > most ? n : most;
   }
   *bytes = most;

@@ -655,3 +655,21 @@ def test_attention_of_parts_that_a_second_kernel_joins(dtype, dim, window, lens)
     lay = ko.Layout(4, 1, dim, 64, window)
     plan = Plan(lay, [2] * len(lens), lens, rng, width=300)
     check_attention(lay, plan, plan.filled_cache(rng), dtype, rng)
+
+
+def test_attention_workspace_of_the_largest_batch_serves_the_others():
+    """A server's prompt is not cut, its single sequences are: one workspace, made for the former."""
+    rng = np.random.default_rng(62)
+    lay = ko.Layout(16, 2, 128, 16)
+    sizes = (([600, 1], [600, 300]), ([1], [2000]), ([4], [1500]), ([2] * 20, [90] * 20), ([1, 3], [2000, 40]),
+             ([64], [900]), ([1], [3]))
+    largest = svr.KvBatch(torch.zeros(21, dtype=torch.int32, device="cuda"),
+                          torch.zeros(20, dtype=torch.int32, device="cuda"),
+                          torch.zeros((20, 125), dtype=torch.int32, device="cuda"), 600)
+    for dtype in TYPES:
+        ws = svr.kv_workspace(desc_of(lay), largest, 601)
+        for rows, lens in sizes:
+            log(f"one workspace {dtype} {rows[:2]} {lens[:2]}")
+            plan = Plan(lay, rows, lens, rng)
+            check_attention_of(lay, plan, plan.filled_cache(rng), dtype, rng, sorted({0, len(rows) - 1}), ws)
+            assert not ws[:16384].any()

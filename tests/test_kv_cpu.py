@@ -323,3 +323,23 @@ def test_sequences_of_a_long_table_can_be_cut_however_many_there_are(heads, kv_h
         b = kv_batch(n_seqs=seqs, n_tokens=seqs, max_rows=1, pages_per_seq=1000)
         assert svr.lib().moe_kv_attention_workspace_bytes(d.c(), b, ctypes.byref(out)) == B.OK
         assert 16384 < out.value < 2 ** 26, seqs
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,window", [(64, 4, 192, 0), (32, 8, 128, 512), (8, 8, 64, 0), (1024, 1024, 256, 0)])
+def test_attention_workspace_serves_every_smaller_batch(heads, kv_heads, dim, window):
+    """Fewer rows are cut into more parts: a size that went by one batch alone would be too little for others."""
+    d = kv_desc(n_heads=heads, n_kv_heads=kv_heads, head_dim=dim, window=window)
+
+    def need(seqs, rows, max_rows, pages):
+        out = ctypes.c_size_t()
+        b = kv_batch(n_seqs=seqs, n_tokens=rows, max_rows=max_rows, pages_per_seq=pages)
+        assert svr.lib().moe_kv_attention_workspace_bytes(d.c(), b, ctypes.byref(out)) == B.OK
+        return out.value
+
+    most = need(256, 4096, 2048, 1000)
+    assert most < 60e6
+    for seqs in (1, 2, 3, 64, 100, 256):
+        for rows in (1, 4, 64, 512, 4096):
+            for max_rows in (1, 4, 33, 2048):
+                for pages in (1, 7, 1000):
+                    assert need(seqs, rows, max_rows, pages) <= most
