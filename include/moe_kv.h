@@ -16,7 +16,8 @@
  * rows each, rows of all sequences one after another in q, k, v and out;
  * seq_lens[b] counts the tokens of sequence b WITH its new rows.  Row i of
  * sequence b is the token at place p = seq_lens[b] - q_offsets[b+1] + i.
- * Rows at or behind q_offsets[n_seqs] (padding) are not read or written.
+ * Rows at or behind q_offsets[n_seqs] (padding) are not written; q, k, v and
+ * positions have them, with any values.
  * Token p of sequence b lives in page page_table[b][p / page_size], at
  * p % page_size.
  *

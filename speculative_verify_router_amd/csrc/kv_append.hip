@@ -269,7 +269,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(AppendArgs a) {
       }
     }
   };
-  // Asked for before anything else is known.
+  // Asked for before anything else is known (a row of no sequence too, to drop it).
   if (sk < k_end) load_keys(sk);
   load_queries(s);
 

@@ -673,3 +673,39 @@ def test_attention_workspace_of_the_largest_batch_serves_the_others():
             plan = Plan(lay, rows, lens, rng)
             check_attention_of(lay, plan, plan.filled_cache(rng), dtype, rng, sorted({0, len(rows) - 1}), ws)
             assert not ws[:16384].any()
+
+
+@pytest.mark.parametrize("seqs", [62, 63, 64, 65, 127, 400, 4097])
+def test_append_and_read_of_many_sequences(seqs):
+    """On both sides of the lookup of a row's sequence by one load of all offsets, with empty sequences at
+    either end; rows of no sequence hold NaN and stay out of the cache."""
+    log(f"append of {seqs} sequences")
+    rng = np.random.default_rng(seqs)
+    lay = ko.Layout(2, 1, 64, 16, 0, 32)
+    rows = rng.integers(0, 3, seqs)
+    rows[0] = rows[-1] = 0
+    rows[seqs // 2] = 5
+    plan = Plan(lay, list(rows), list(rows + rng.integers(0, 20, seqs)), rng, pad_rows=3)
+    n = int(plan.offsets[-1])
+    x = rng.standard_normal((plan.T, 4, 64))
+    x[n:] = np.nan
+    t, x64 = rounded(x, "bf16")
+    f = np.full(16, 0.25, np.float32)
+    cache = rng.integers(0, 256, plan.empty_cache().shape).astype(np.uint8)
+    got, q_out = run_append(lay, plan, cache, t[:, :2], t[:, 2:3], t[:, 3:], inv_freq=dev(f))
+    want = cache.copy()
+    ref = ko.append(lay, want, plan.offsets, plan.lens, plan.table, x64[:, :2], x64[:, 2:3], x64[:, 3:], inv_freq=f)
+    assert np.array_equal(got, want)
+    # A sine, a cosine, two products and a sum of 24 bits, of values up to |a| + |b|, then bf16's own rounding.
+    tol = 10 * 2.0 ** -24 * np.max(np.abs(ref[:n]), -1, keepdims=True) * 2 + 2.0 ** -8 * np.abs(ref[:n])
+    assert np.all(np.abs(q_out[:n] - ref[:n]) <= tol) and np.isnan(q_out[n:]).all()
+    k, v = (torch.full((plan.T, 1, 64), 7.0, device="cuda") for _ in "kv")
+    svr.moe_kv_read(desc_of(lay), plan.batch(), dev(want), k, v)
+    k, v = k.cpu().numpy(), v.cpu().numpy()
+    assert (k[n:] == 7).all() and (v[n:] == 7).all()
+    for b in range(seqs):
+        for i in range(plan.offsets[b], plan.offsets[b + 1]):
+            page, o = ko.slot(lay, plan.table[b], plan.n_pages, int(plan.lens[b]) - int(plan.offsets[b + 1]) + i)
+            kc, vc, ks, vs = ko.page_parts(lay, want[page, 0])
+            assert np.array_equal(k[i, 0], ko.vector_values(kc[o], ks[o])), (b, i)
+            assert np.array_equal(v[i, 0], ko.vector_values(vc[o], vs[o])), (b, i)
