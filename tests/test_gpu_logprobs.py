@@ -213,3 +213,23 @@ def test_workspace_made_on_the_stream_of_the_call():
     for o in got:
         for k, v in want.items():
             assert torch.equal(o[k], v), k
+
+
+def test_workspace_of_the_call_stays_on_its_stream():
+    """Everything but the workspaces is made, and waited for, before the calls: what this stream is given and
+    fills meanwhile can only be a workspace's memory, which it must not be."""
+    rng = np.random.default_rng(62)
+    x = draw(rng, 2, 131072, "f32")
+    want = run(x, [5, 6], 5)
+    t = dev(np.array([5, 6], np.int32))
+    n = svr.moe_logprobs_workspace_bytes(2, 131072, 5)
+    got = [{k: torch.zeros_like(v) for k, v in want.items()} for _ in range(20)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for o in got:
+        svr.moe_logprobs(x, t, stream=side, **o)
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xFF)
+    torch.cuda.synchronize()
+    for o in got:
+        for k, v in want.items():
+            assert torch.equal(o[k], v), k
