@@ -31,6 +31,8 @@
 // and 8 us; factors in registers and one step ahead, whose copies waited for
 // the stores: 50 and 26; eight channels of a key a lane: 127 registers instead
 // of 81, 4.9 us for 4 tokens; two workgroups a token: 38 us.
+#include <type_traits>
+
 #include "kv.h"
 
 namespace svr {
@@ -218,6 +220,12 @@ struct Raw {
                (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * i + 1]) << 16;
     }
   }
+  __device__ __forceinline__ void scale(float by) {
+    float x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = (*this)[i] * by;
+    set(x);
+  }
   // The neighbours swapped, where mask is set; 0 elsewhere.
   __device__ __forceinline__ void swap_of(const Raw& x, uint32_t mask) {
 #pragma unroll
@@ -348,7 +356,20 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(AppendArgs a) {
         float ss = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(x[n][e], x[n][e], ss);
-        r = norm_factor(group_sum<LG>(ss) * (1.f / D) + a.eps);
+        float mean = group_sum<LG>(ss) * (1.f / D) + a.eps;
+        // Squares that pass the range of 32 bits: once more, of scaled channels.
+        const bool huge = !(mean < 1e30f), tiny = mean < 1e-30f;
+        if constexpr (!std::is_same_v<T, _Float16>)
+          if (__ballot(huge || tiny)) {
+            const float by = huge ? 0x1p-96f : tiny ? 0x1p96f : 1.f;
+            x[n].scale(by);
+            y[n].scale(by);
+            ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[n][e], x[n][e], ss);
+            mean = group_sum<LG>(ss) * (1.f / D) + a.eps * by * by;
+          }
+        r = norm_factor(mean);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) t[e] = r * fmaf(x[n][e], qa[e], y[n][e] * qb[e]);

@@ -709,3 +709,30 @@ def test_append_and_read_of_many_sequences(seqs):
             kc, vc, ks, vs = ko.page_parts(lay, want[page, 0])
             assert np.array_equal(k[i, 0], ko.vector_values(kc[o], ks[o])), (b, i)
             assert np.array_equal(v[i, 0], ko.vector_values(vc[o], vs[o])), (b, i)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 192])
+def test_append_norm_of_heads_of_any_size(dtype, dim):
+    """Heads whose squares pass the range of 32 bits at either end, next to ordinary ones, without an epsilon."""
+    log(f"norm of any size {dtype} D={dim}")
+    rng = np.random.default_rng(dim)
+    lay = ko.Layout(10, 2, dim, 16, 0, 32, eps=0.0)
+    plan = Plan(lay, [5], [21], rng)
+    scales = np.array([1, 1e-4, 1e3] if dtype == "f16" else [1e-43, 1e-30, 1e-20, 1e-15, 1, 1e15, 1e19, 1e25, 3e37])
+    s = scales[(np.arange(5)[:, None] * 11 + np.arange(14)) % len(scales)]
+    t, x64 = rounded(rng.uniform(0.5, 1, (5, 14, dim)) * rng.choice([-1, 1], (5, 14, dim)) * s[:, :, None], dtype)
+    w = (1 + 0.1 * rng.standard_normal((2, dim))).astype(np.float32)
+    f = np.full(16, 0.25, np.float32)
+    cache = plan.empty_cache()
+    got, q_out = run_append(lay, plan, cache, t[:, :10], t[:, 10:12], t[:, 12:], q_norm=dev(w[0]), k_norm=dev(w[1]),
+                            inv_freq=dev(f))
+    with np.errstate(invalid="ignore"):
+        ref = ko.append(lay, cache, plan.offsets, plan.lens, plan.table, x64[:, :10], x64[:, 10:12], x64[:, 12:], *w, f)
+    assert np.array_equal(got, cache)
+    # As in check_append.
+    big = np.max(np.abs(ref), axis=-1, keepdims=True)
+    tol = (dim / 2 + 10) * 2.0 ** -24 * 2 * big + torch.finfo(TYPES[dtype]).eps / 2 * np.abs(ref) + 2.0 ** -25
+    nothing = np.isnan(ref)  # bf16 has no 1e-43: heads of zeros, whose norm is 0 / 0
+    assert nothing.any() == (dtype == "bf16") and np.array_equal(np.isnan(q_out), nothing)
+    assert np.all((np.abs(q_out - ref) <= tol) | nothing)
