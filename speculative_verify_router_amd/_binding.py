@@ -436,11 +436,15 @@ def _call_on(device: torch.device, stream, f, *args) -> int:
         return f(*args, handle)
 
 
-def _check_int32(obj, *names):
+def _check_bits(bits: int, **numbers):
     """ctypes would cut a larger number off in silence."""
-    for name in names:
-        if not -2 ** 31 <= getattr(obj, name) < 2 ** 31:
-            raise ValueError(f"{name}: {getattr(obj, name)} does not fit 32 bits")
+    for name, n in numbers.items():
+        if not -2 ** (bits - 1) <= n < 2 ** (bits - 1):
+            raise ValueError(f"{name}: {n} does not fit {bits} bits")
+
+
+def _check_int32(obj, *names):
+    _check_bits(32, **{name: getattr(obj, name) for name in names})
 
 
 def _default_workspace(stream, make, *args) -> torch.Tensor:
@@ -466,6 +470,8 @@ class KvDesc:
 
     def __post_init__(self):
         _check_int32(self, "n_heads", "n_kv_heads", "head_dim", "page_size", "window", "rotary_dims")
+        if self.scale != 0 and ctypes.c_float(self.scale).value == 0:
+            raise ValueError(f"scale: {self.scale} is zero in 32 bits, which stands for 1/sqrt(head_dim)")
         # The fields never change, so the C struct is made once.
         object.__setattr__(self, "_c", _KvDesc(
             self.n_heads, self.n_kv_heads, self.head_dim, self.page_size, self.window,
@@ -519,6 +525,7 @@ class KvBatch:
 
 def moe_kv_cache_bytes(desc: KvDesc, n_pages: int) -> int:
     out = ctypes.c_int64()
+    _check_bits(64, n_pages=n_pages)
     _check(lib().moe_kv_cache_bytes(desc.c(), n_pages, ctypes.byref(out)), "moe_kv_cache_bytes")
     return out.value
 
@@ -562,6 +569,7 @@ def moe_kv_append(desc: KvDesc, batch: KvBatch, q: Optional[torch.Tensor], k: to
 
 def moe_kv_attention_workspace_bytes(desc: KvDesc, batch: KvBatch, n_tokens: int) -> int:
     out = ctypes.c_size_t()
+    _check_bits(32, n_tokens=n_tokens)
     _check(lib().moe_kv_attention_workspace_bytes(desc.c(), batch.c(n_tokens), ctypes.byref(out)),
            "moe_kv_attention_workspace_bytes")
     return out.value
@@ -614,6 +622,8 @@ LOGPROBS_MAX_TOP = 64
 
 def moe_logprobs_workspace_bytes(max_rows: int, vocab: int, max_top: int = 0) -> int:
     out = ctypes.c_size_t()
+    _check_bits(32, max_rows=max_rows, max_top=max_top)
+    _check_bits(64, vocab=vocab)
     _check(lib().moe_logprobs_workspace_bytes(max_rows, vocab, max_top, ctypes.byref(out)),
            "moe_logprobs_workspace_bytes")
     return out.value

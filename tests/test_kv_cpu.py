@@ -343,3 +343,22 @@ def test_attention_workspace_serves_every_smaller_batch(heads, kv_heads, dim, wi
             for max_rows in (1, 4, 33, 2048):
                 for pages in (1, 7, 1000):
                     assert need(seqs, rows, max_rows, pages) <= most
+
+
+def test_the_binding_refuses_a_scale_that_is_none_in_32_bits():
+    """A scale of zero stands for 1/sqrt(head_dim)."""
+    for scale in (1e-50, 5e-324):
+        with pytest.raises(ValueError, match="scale"):
+            svr.KvDesc(4, 2, 64, scale=scale)
+    assert svr.KvDesc(4, 2, 64, scale=1e-38).c().scale > 0 and svr.KvDesc(4, 2, 64).c().scale == 0
+
+
+def test_the_binding_refuses_sizes_that_ctypes_would_cut_off():
+    z = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: svr.moe_logprobs_workspace_bytes(2 ** 32 + 4, 1000),
+                 lambda: svr.moe_logprobs_workspace_bytes(4, 2 ** 64 + 1000),
+                 lambda: svr.moe_logprobs_workspace_bytes(4, 1000, 2 ** 32),
+                 lambda: svr.moe_kv_cache_bytes(kv_desc(), 2 ** 64 + 1),
+                 lambda: svr.moe_kv_attention_workspace_bytes(kv_desc(), svr.KvBatch(z, z[:1], z[None], 1), 2 ** 32 + 1)):
+        with pytest.raises((ValueError, svr.MoeError)):
+            call()
