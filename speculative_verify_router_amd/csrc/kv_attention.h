@@ -22,20 +22,25 @@
 // shrink with the number of tokens, but so does the result, and its error
 // becomes as large as its own rounding (60000 tokens: 0.0023 of the result
 // instead of the 0.0016 that the rounding alone makes; two terms: 0.0016).  It
-// would save a third of the products: 458 and 581 us for the first call below.
+// would save a third of the products: 458 and 581 us for the first call below, on
+// one card.
 //
 // Bound: instructions.  A tile of two row tiles at D = 192 issues 96
 // widenings, 72 products and about 150 others, which overlap with the
-// products only in part; two waves a SIMD pass 32 tokens in 1.1 us each.
-// Measured with 64 query on 4 key/value heads of 192: 512 rows over 16384
-// tokens 581 us in bf16 (698 TFLOP/s, 64% of what a large bf16 product of the
-// library reaches here, with a half more products than that counts), 847 in
-// fp16 and 1027 in fp32 (396 TFLOP/s, three products each); 4 rows over 60000
-// tokens 32 us with the joining (49 MB); 1 row over 777 tokens 10 us.  29 sequences of up to 5000 tokens, fp16, 32 on 8
-// heads of 128: 25 us (82 MB, 3.3 TB/s).  Addresses by vector arithmetic in
-// every tile instead of once: 892 and 1056 in fp16 and fp32, 1 us for 4 rows.
+// products only in part.  Measured with 64 query on 4 key/value heads of 192,
+// 512 rows over 16384 tokens: 598 us in bf16 (680 TFLOP/s, 62% of what a large
+// bf16 product of the library reaches here, with a half more products than
+// that counts), 850 in fp16 and 1024 in fp32 (397 TFLOP/s, three products
+// each); from card to card up to a tenth more.  4 rows over 60000 tokens 32 us
+// with the joining (49 MB).  1 row: 4.5 us with one tile, 5.5 with one for
+// each wave, 1.2 for every further one of a wave, and 2.9 where parts are
+// joined: 9.5 over 777 tokens, 20.4 over 60000 (the second kernel, and a third
+// of the rate of the cache's bytes).  29 sequences of up to 5000 tokens, fp16,
+// 32 on 8 heads of 128: 24 us (82 MB, 3.4 TB/s).  Addresses by vector
+// arithmetic in every tile instead of once: 892 and 1056 us in fp16 and fp32,
+// 1 us for 4 rows.
 // Others that were measured, for the first bf16 call, the verify batch and the
-// single row, with one term a weight (458, 28.6 and 9.6 us as it is): 64 rows a wave (one wave a SIMD) 716 and 47 us; waves sharing
+// single row, with one term a weight (458, 28.6 and 9.6 us as it was): 64 rows a wave (one wave a SIMD) 716 and 47 us; waves sharing
 // widened tiles through shared memory, with 16x16 or 32x32 products, 475 to
 // 497, 29 to 33 and 5.6 to 7.3 us (with a second kernel after the last two);
 // eight waves in every workgroup 478, 33 and 11 us.

@@ -169,10 +169,10 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   const int64_t dense = (int64_t)b->n_tokens * G / span + b->n_seqs;  // see kv_first_tile
   p.search = all > dense;
   all = p.search ? dense : all;
-  // Larger workgroups make fewer parts: 4 rows over 60000 tokens 32.0 us (34.4
-  // with four waves), 15000 tokens 20.4 (21.5); but a part of 64 rows over
-  // 16384, of which there are two, takes 106 us (96), 4 rows over 4000 tokens
-  // 15.9 (15.0).
+  // Larger workgroups make fewer parts: 4 rows over 60000 tokens 34.7 us (37.2
+  // with four waves), 15000 tokens 21.8 (24.2); but a part of 64 rows over
+  // 16384, of which there are two, takes 114 us (101), 4 rows over 4000 tokens
+  // 26.0 (15.3).
   p.waves = kAttnPartWaves;
   if (p.row_tiles != 2 || !attn_split(p, d, b, dtype, all)) {
     p.waves = kAttnWaves;
