@@ -615,7 +615,7 @@ def test_attention_of_a_prompt_among_thousands_of_sequences():
 @pytest.mark.parametrize("dtype,seqs,heads,kv_heads,dim,window,rows,length", [
     ("bf16", 97, 8, 8, 64, 0, 1, 3000), ("f16", 300, 16, 4, 128, 0, 2, 4000), ("f32", 700, 8, 8, 64, 0, 1, 5000),
     ("bf16", 100, 20, 4, 64, 0, 150, 3000), ("bf16", 130, 16, 8, 192, 2500, 3, 4000), ("f16", 64, 16, 16, 64, 0, 1, 2000),
-    ("bf16", 2, 16, 16, 64, 0, 1, 2000), ("f32", 66, 4, 4, 256, 0, 4, 2500)])
+    ("bf16", 2, 16, 16, 64, 0, 1, 2000), ("f32", 66, 4, 4, 256, 0, 4, 2500), ("bf16", 4000, 2, 1, 64, 0, 1, 30000)])
 def test_attention_of_a_long_sequence_among_many(dtype, seqs, heads, kv_heads, dim, window, rows, length):
     """More sequences than run at once, of which a few are cut: each finds its parts among those of the others,
     in a workspace that goes by neither their rows nor their number; again where none is long."""
