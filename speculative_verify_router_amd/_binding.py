@@ -44,6 +44,12 @@ class _Weights(ctypes.Structure):
                 ("shared_up", ctypes.c_void_p), ("shared_down", ctypes.c_void_p)]
 
 
+class _Tree(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_rows", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32), ("max_children", ctypes.c_int32),
+                ("q_offsets", ctypes.c_void_p), ("parents", ctypes.c_void_p)]
+
+
 class _KvDesc(ctypes.Structure):
     _fields_ = [("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
@@ -105,7 +111,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         i32, i64, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
         D, W = ctypes.POINTER(_Desc), ctypes.POINTER(_Weights)
-        KD, KB = ctypes.POINTER(_KvDesc), ctypes.POINTER(_KvBatch)
+        KD, KB, TR = ctypes.POINTER(_KvDesc), ctypes.POINTER(_KvBatch), ctypes.POINTER(_Tree)
         sig = {
             "moe_version": (i32, []),
             "moe_strerror": (ctypes.c_char_p, [i32]),
@@ -129,6 +135,12 @@ def lib():
             "moe_kv_read": (i32, [KD, KB, vp, i32, vp, vp, vp]),
             "moe_logprobs_workspace_bytes": (i32, [i32, i64, i32, ctypes.POINTER(sz)]),
             "moe_logprobs": (i32, [vp, i32, i32, i64, i64, vp, vp, vp, i32, vp, vp, vp, sz, vp]),
+            "moe_tree_plan": (i32, [TR, vp, vp, i32, vp, vp]),
+            "moe_kv_tree_attention": (i32, [KD, KB, i32, vp, i32, vp, i64, vp, i32, vp, vp, vp, sz, vp]),
+            "moe_kv_commit": (i32, [KD, KB, vp, i64, vp, ctypes.POINTER(vp), i32, i32, vp, vp]),
+            "moe_sample_workspace_bytes": (i32, [TR, i64, ctypes.POINTER(sz)]),
+            "moe_verify_sample": (i32, [TR, vp, i32, i64, i64, vp, vp, i64, vp, vp, vp, vp, i32, vp, vp,
+                                        vp, vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -145,7 +157,9 @@ C_SYMBOLS = ("moe_version", "moe_strerror", "moe_tensor_bytes", "moe_workspace_b
              "moe_stage_name", "moe_dequant_rows", "moe_accept_workspace_bytes",
              "moe_verify_accept", "moe_kv_cache_bytes", "moe_kv_append",
              "moe_kv_attention_workspace_bytes", "moe_kv_attention", "moe_kv_read",
-             "moe_logprobs_workspace_bytes", "moe_logprobs")
+             "moe_logprobs_workspace_bytes", "moe_logprobs", "moe_tree_plan",
+             "moe_kv_tree_attention", "moe_kv_commit", "moe_sample_workspace_bytes",
+             "moe_verify_sample")
 
 
 def _ptr(t: Optional[torch.Tensor], dtype) -> Optional[int]:
@@ -370,6 +384,7 @@ BF16, F16 = 6, 7
 _ACT_DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 KV_ROTARY_INTERLEAVED = 1
 KV_COUNTER_BYTES = 16384
+KV_MAX_TOKENS = 1048576
 
 
 def _act_dtype(t: torch.Tensor) -> int:
@@ -511,6 +526,16 @@ class KvBatch:
         object.__setattr__(self, "_args", args)
         object.__setattr__(self, "_device", dev)
         object.__setattr__(self, "_c", None)
+        object.__setattr__(self, "_unread", None)
+
+    def c_rows_unread(self, device: torch.device) -> _KvBatch:
+        """The C struct for a call without rows, which n_tokens only bounds the offsets of."""
+        if device != self._device:
+            raise ValueError(f"batch: expected tensors on {device}, got {self._device}")
+        if self._unread is None:
+            object.__setattr__(self, "_unread", _KvBatch(self.page_table.shape[0], KV_MAX_TOKENS,
+                                                         self.max_rows, *self._args))
+        return self._unread
 
     def c(self, n_tokens: int, device: Optional[torch.device] = None) -> _KvBatch:
         """The C struct for rows on `device` (None: sizes only)."""
@@ -665,3 +690,186 @@ def moe_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor],
                   _on(dev, top_logprobs, f32, (N, k), "top_logprobs"),
                   _on(dev, ws, torch.uint8, None, "ws"), ws.numel())
     _check(st, "moe_logprobs")
+
+
+# include/moe_tree.h: trees of drafts, their attention and the commit of the accepted path.
+TREE_MAX_ROWS = 1024
+TREE_MAX_CACHES = 256
+
+
+@dataclasses.dataclass(frozen=True)
+class DraftTree:
+    """Trees of drafts of a batch of sequences (moe_tree): int32 device tensors
+    q_offsets [B+1] and parents [T] (None: chains, parents i - 1); max_rows: no
+    sequence has more rows; max_children: no row has more children.  The tensors
+    are captured by reference, as those of KvBatch."""
+    q_offsets: torch.Tensor
+    parents: Optional[torch.Tensor]
+    max_rows: int
+    max_children: int = 1
+
+    def __post_init__(self):
+        i32, dev = torch.int32, self.q_offsets.device
+        if self.q_offsets.dim() != 1 or self.q_offsets.shape[0] < 1:
+            raise ValueError("q_offsets: expected [sequences + 1]")
+        if self.parents is not None and self.parents.dim() != 1:
+            raise ValueError("parents: expected [rows]")
+        args = (_on(dev, self.q_offsets, i32, None, "q_offsets"),
+                _on(dev, self.parents, i32, None, "parents"))
+        _check_int32(self, "max_rows", "max_children")
+        object.__setattr__(self, "_args", args)
+        object.__setattr__(self, "_device", dev)
+        object.__setattr__(self, "_c", None)
+
+    @property
+    def mask_words(self) -> int:
+        """64-bit words of a row's mask."""
+        return max(1, -(-self.max_rows // 64))
+
+    def c(self, n_rows: int, device: Optional[torch.device] = None) -> _Tree:
+        """The C struct for rows on `device` (None: sizes only)."""
+        c = self._c
+        if device is not None and device != self._device:
+            raise ValueError(f"tree: expected tensors on {device}, got {self._device}")
+        if c is None or c.n_rows != n_rows:
+            if self.parents is not None and self.parents.shape[0] != n_rows and device is not None:
+                raise ValueError(f"parents: expected {n_rows} rows, got {self.parents.shape[0]}")
+            c = _Tree(self.q_offsets.shape[0] - 1, n_rows, self.max_rows, self.max_children, *self._args)
+            if device is not None:
+                object.__setattr__(self, "_c", c)
+        return c
+
+
+def moe_tree_plan(tree: DraftTree, seq_lens: Optional[torch.Tensor], mask: Optional[torch.Tensor],
+                  positions: Optional[torch.Tensor], stream=None):
+    """mask [T][words] int64 (words >= tree.mask_words) and positions [T] int32 outputs (either may
+    be None); seq_lens [B] int32, the tokens of each sequence with its rows (None without positions)."""
+    some = mask if mask is not None else positions
+    if some is None:
+        raise ValueError("moe_tree_plan: mask or positions is needed")
+    dev, T = some.device, some.shape[0]
+    t = tree.c(T, dev)
+    if mask is not None and mask.dim() != 2:
+        raise ValueError("mask: expected [rows][words]")
+    words = mask.shape[1] if mask is not None else 0
+    st = _call_on(dev, stream, lib().moe_tree_plan, t, _on(dev, seq_lens, torch.int32, (t.n_seqs,), "seq_lens"),
+                  _on(dev, mask, torch.int64, (T, words), "mask"), words,
+                  _on(dev, positions, torch.int32, (T,), "positions"))
+    _check(st, "moe_tree_plan")
+
+
+def moe_kv_tree_attention(desc: KvDesc, batch: KvBatch, mask: torch.Tensor, q: torch.Tensor,
+                          cache: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                          ws: Optional[torch.Tensor] = None, stream=None):
+    """As moe_kv_attention, for rows that see each other by mask [T][words] int64 (moe_tree_plan's,
+    or any other); a workspace of kv_workspace."""
+    dev = q.device
+    T, shape = q.shape[0], (q.shape[0], desc.n_heads, desc.head_dim)
+    if ws is None:
+        ws = _default_workspace(stream, kv_workspace, desc, batch, T)
+    qp, qs = _rows(dev, q, q.dtype, shape, "q")
+    if mask.dim() != 2:
+        raise ValueError("mask: expected [rows][words]")
+    words = mask.shape[1]
+    st = _call_on(dev, stream, lib().moe_kv_tree_attention, desc.c(), batch.c(T, dev), _act_dtype(q),
+                  _on(dev, mask, torch.int64, (T, words), "mask"), words, qp, qs,
+                  _cache(desc, cache, dev), cache.shape[0], _on(dev, out, q.dtype, shape, "out"),
+                  _on(dev, lse, torch.float32, shape[:2], "lse"),
+                  _on(dev, ws, torch.uint8, None, "ws"), ws.numel())
+    _check(st, "moe_kv_tree_attention")
+
+
+def moe_kv_commit(desc: KvDesc, batch: KvBatch, path: torch.Tensor, n_accepted: torch.Tensor,
+                  caches: Sequence[torch.Tensor], kept_lens: Optional[torch.Tensor] = None, stream=None):
+    """path [B][entries] and n_accepted [B] int32, as moe_verify_sample gives them; caches: those of
+    all layers, of one shape; kept_lens [B] int32 output.  The batch's rows are the tree's."""
+    dev, i32 = path.device, torch.int32
+    caches = list(caches)
+    if not caches:
+        raise ValueError("moe_kv_commit: a cache is needed")
+    b = batch.c_rows_unread(dev)
+    if path.dim() != 2:
+        raise ValueError("path: expected [sequences][entries]")
+    at = [_cache(desc, c, dev) for c in caches]
+    if len(set(at)) != len(at):
+        raise ValueError("moe_kv_commit: a cache twice")
+    if any(c.shape != caches[0].shape for c in caches):
+        raise ValueError("moe_kv_commit: expected caches of one shape")
+    if kept_lens is not None and b.n_seqs and kept_lens.data_ptr() == batch.seq_lens.data_ptr():
+        raise ValueError("moe_kv_commit: kept_lens is seq_lens, which other workgroups still read")
+    st = _call_on(dev, stream, lib().moe_kv_commit, desc.c(), b,
+                  _on(dev, path, i32, (b.n_seqs, path.shape[1]), "path"), path.shape[1],
+                  _on(dev, n_accepted, i32, (b.n_seqs,), "n_accepted"),
+                  (ctypes.c_void_p * len(at))(*at), len(at), caches[0].shape[0],
+                  _on(dev, kept_lens, i32, (b.n_seqs,), "kept_lens"))
+    _check(st, "moe_kv_commit")
+
+
+# include/moe_sample.h: sampled verification of drafts.
+SAMPLE_COUNTER_BYTES = 131072
+
+
+def moe_sample_workspace_bytes(tree: DraftTree, n_rows: int, vocab: int) -> int:
+    out = ctypes.c_size_t()
+    _check_bits(32, n_rows=n_rows)
+    _check_bits(64, vocab=vocab)
+    _check(lib().moe_sample_workspace_bytes(tree.c(n_rows), vocab, ctypes.byref(out)),
+           "moe_sample_workspace_bytes")
+    return out.value
+
+
+def sample_workspace(tree: DraftTree, n_rows: int, vocab: int) -> torch.Tensor:
+    """A device workspace for moe_verify_sample on trees of up to n_rows rows and these sequences, its
+    counters zeroed (calls keep them so)."""
+    ws = torch.empty(moe_sample_workspace_bytes(tree, n_rows, vocab), dtype=torch.uint8,
+                     device=tree.q_offsets.device)
+    ws[:SAMPLE_COUNTER_BYTES].zero_()
+    return ws
+
+
+def _logit_rows(t: torch.Tensor, what: str) -> int:
+    """The row stride of [rows][vocabulary] with whole rows, possibly apart."""
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected [rows][vocabulary], got shape {tuple(t.shape)}")
+    N, V = t.shape
+    if N and V and t.stride(1) != 1 and V != 1:
+        raise ValueError(f"{what}: expected whole rows, got strides {t.stride()}")
+    return t.stride(0) if N > 1 else V
+
+
+def moe_verify_sample(tree: DraftTree, logits: torch.Tensor, tokens: torch.Tensor,
+                      accept_u: torch.Tensor, sample_u: torch.Tensor, accepted: torch.Tensor,
+                      n_accepted: torch.Tensor, path: Optional[torch.Tensor] = None,
+                      draft_probs: Optional[torch.Tensor] = None,
+                      temperature: Optional[torch.Tensor] = None,
+                      verify_h: Optional[torch.Tensor] = None,
+                      pending_h: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                      stream=None):
+    """logits [T][V] float32, bfloat16 or float16 and draft_probs [T][V] float32 (rows possibly
+    apart); tokens [T] int32, accept_u [T], sample_u [B], temperature [B] float32; accepted and path
+    [B][tree.max_rows], n_accepted [B] int32 outputs; verify_h [T][h] and pending_h [B][h] float32,
+    both or neither."""
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
+    stride = _logit_rows(logits, "logits")
+    T, V = logits.shape
+    t = tree.c(T, dev)
+    B = t.n_seqs
+    qp, qs = None, 0
+    if draft_probs is not None:
+        qs = _logit_rows(draft_probs, "draft_probs")
+        if draft_probs.device != dev or draft_probs.dtype != f32 or draft_probs.shape != logits.shape:
+            raise ValueError(f"draft_probs: expected float32 {tuple(logits.shape)} on {dev}, got "
+                             f"{draft_probs.dtype} {tuple(draft_probs.shape)} on {draft_probs.device}")
+        qp = draft_probs.data_ptr()
+    h = 0 if verify_h is None else verify_h.shape[-1]
+    if ws is None:
+        ws = _default_workspace(stream, sample_workspace, tree, T, V)
+    st = _call_on(dev, stream, lib().moe_verify_sample, t, logits.data_ptr(), _act_dtype(logits), V, stride,
+                  _on(dev, tokens, i32, (T,), "tokens"), qp, qs,
+                  _on(dev, temperature, f32, (B,), "temperature"), _on(dev, accept_u, f32, (T,), "accept_u"),
+                  _on(dev, sample_u, f32, (B,), "sample_u"), _on(dev, verify_h, f32, (T, h), "verify_h"), h,
+                  _on(dev, accepted, i32, (B, tree.max_rows), "accepted"),
+                  _on(dev, path, i32, (B, tree.max_rows), "path"),
+                  _on(dev, n_accepted, i32, (B,), "n_accepted"), _on(dev, pending_h, f32, (B, h), "pending_h"),
+                  _on(dev, ws, torch.uint8, None, "ws"), ws.numel())
+    _check(st, "moe_verify_sample")

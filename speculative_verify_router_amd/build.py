@@ -26,12 +26,13 @@ SOURCES = [os.path.join(CSRC, f) for f in (
     "launch_ffn_q4_k.hip", "launch_ffn_q2_k.hip", "launch_ffn_q3_k.hip", "launch_ffn_q6_k.hip",
     "accept.hip", "kv_append.hip", "kv_attention.hip", "launch_attention_d64.hip",
     "launch_attention_d128.hip", "launch_attention_d192.hip", "launch_attention_d256.hip",
-    "logprobs.hip")]
+    "logprobs.hip", "tree.hip", "sample.hip")]
 HEADERS = [os.path.join(CSRC, f) for f in ("common.h", "quant.h", "route.h", "ffn.h", "phases.h", "misc.h",
                                            "gemm.h", "launch.h", "launch_ffn.h", "kv.h",
-                                           "kv_attention.h", "launch_attention.h")] + [
+                                           "kv_attention.h", "launch_attention.h", "row_tile.h",
+                                           "tree.h")] + [
     os.path.join(ROOT, "include", h) for h in ("moe_layer.h", "moe_accept.h", "moe_kv.h",
-                                               "moe_logprobs.h")]
+                                               "moe_logprobs.h", "moe_tree.h", "moe_sample.h")]
 
 ARCH = "gfx950"
 

@@ -86,6 +86,10 @@ struct AttnArgs {
   unsigned* ctr;  // [row tile that is cut][key/value head] parts made, or NULL: a second kernel joins
   float c;         // scale * log2(e)
   int row_tiles, min_tiles, by_seq, search;
+  int reach;  // tokens that a window's row tile lies over at most, with its first and last tile's
+  // Rows of a tree (moe_tree.h): the new rows that each row sees, in 32-bit words; NULL: those before it.
+  const uint32_t* mask;
+  int mask_words;
   int first, extra;  // row tiles of all sequences; room for parts behind the first ones
   // Query heads a key/value head; row tiles of a sequence; splits at most;
   // Hk; work of a head that runs at once; row tiles side by side on an XCD;
@@ -174,8 +178,7 @@ __device__ __forceinline__ KvCut kv_cut(const AttnArgs& a, const KvRows& s) {
   const int span = 16 * a.row_tiles;
   c.row_tiles = (s.rows * a.G.d + span - 1) / span;
   int seen = min(s.len, a.kv.pages_per_seq << a.kv.page_shift);
-  // Rows of a tile: whole tokens, and one cut at either end.
-  if (a.kv.window) seen = (int)min((int64_t)seen, (int64_t)a.kv.window + a.G.of(span) + 2 + kAttnTile);
+  if (a.kv.window) seen = min(seen, a.reach);
   c.tiles = (seen + kAttnTile - 1) / kAttnTile;
   return c;
 }
@@ -274,6 +277,43 @@ __device__ __forceinline__ KvRange kv_range(const AttnArgs& a, int len, int firs
   r.per = per;
   return r;
 }
+// With rows of a tree, whichever the row tile: from the tokens that a row with
+// no mark sees to the last new row.
+__device__ __forceinline__ KvRange kv_tree_range(const AttnArgs& a, const KvRows& sq, int per) {
+  return kv_range(a, sq.len, sq.place0 - 1, sq.place0 + sq.rows - 1, per);
+}
+
+// The new rows that a row of a tree sees.
+struct TreeMask {
+  const uint32_t* words;  // of the row
+  int n;                  // words
+  __device__ __forceinline__ uint32_t word(int w) const { return w < 0 ? ~0u : w < n ? words[w] : 0u; }
+  // Bit i: new row from + i is seen; a row below 0 is a token before the new rows, from >= -32.
+  __device__ __forceinline__ uint32_t bits(int from) const {
+    return __builtin_amdgcn_alignbit(word((from >> 5) + 1), word(from >> 5), from & 31);
+  }
+  // The first place that the row sees of those before and among the new rows
+  // (from place0 on, `rows` of them), where it sees the last `window`.
+  __device__ __forceinline__ int first_seen(int place0, int rows, int window) const {
+    auto valid = [&](int w) { return 32 * w + 32 <= rows ? words[w] : words[w] & ((1u << (rows & 31)) - 1); };
+    const int used = min(n, (rows + 31) / 32);
+    int marks = 0;
+    for (int w = 0; w < used; ++w) marks += __popc(valid(w));
+    int skip = marks - window;  // marked rows that are too far back
+    if (skip < 0) return place0 + skip;
+    for (int w = 0; w < used; ++w) {
+      uint32_t m = valid(w);
+      const int here = __popc(m);
+      if (skip < here) {
+        while (skip-- > 0) m &= m - 1;
+        return place0 + 32 * w + __builtin_ctz(m);
+      }
+      skip -= here;
+    }
+    return place0 + rows;  // (not reached: marks > skip)
+  }
+};
+
 template <int D>
 __device__ __forceinline__ constexpr int step_channel(int step, int g) {
   constexpr int kFull = 4 * (D / 128);
@@ -388,7 +428,10 @@ constexpr int attn_waves(int D, int RT, int NT) {
 // Terms of a softmax weight, for NT of a query value: never one, see above.
 constexpr int attn_weight_terms(int NT) { return NT < 2 ? 2 : NT; }
 
-template <int D, int RT, int NT, int W, typename T>
+// kTree: rows of a tree see the new rows that a.mask marks.  Tiles of tokens
+// before the new rows are the same; the last ones, a 32nd of the tree's rows,
+// take the rows' bits from memory, asked for before the next tile's codes.
+template <int D, int RT, int NT, int W, typename T, bool kTree>
 __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attention(AttnArgs a) {
   constexpr int KS = D / 32, CB = D / 16, NP = attn_weight_terms(NT);
   constexpr int kRowBytes = 2 * D + 16;            // a staged token: the pad spreads the banks
@@ -480,7 +523,7 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
   if ((unsigned)r0 >= (unsigned)row_total) return;
   const int r_last = min(row_total, r0 + 16 * RT) - 1;
   const int first = sq.place0 + a.G.of(r0), last = sq.place0 + a.G.of(r_last);
-  const KvRange rg = kv_range(a, sq.len, first, last, per);
+  const KvRange rg = kTree ? kv_tree_range(a, sq, per) : kv_range(a, sq.len, first, last, per);
   if (!rg.uses(split)) return;
   // The first part is what whole ones leave at the end: those behind it in the
   // list are then all alike, and share the chip evenly whatever their order.
@@ -530,14 +573,21 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
   // The rows' queries, and the tokens that each sees: [lo, hi].
   bf16x8 qf[RT][KS][NT];
   int lo[RT], hi[RT];
+  TreeMask marks[RT];  // (unused without a tree)
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int r = r0 + 16 * rt + l16;
     const bool on = r < row_total;
     const int m = a.G.of(min(r, row_total - 1)), h = kvh * G + min(r, row_total - 1) - m * G;
     const int place = sq.place0 + m;
-    hi[rt] = on ? min(place, rg.end - 1) : -1;
-    lo[rt] = a.kv.window ? place - a.kv.window + 1 : 0;
+    if constexpr (kTree) {
+      marks[rt] = TreeMask{a.mask + (int64_t)(sq.off + m) * a.mask_words, a.mask_words};
+      hi[rt] = on ? rg.end - 1 : -1;
+      lo[rt] = a.kv.window ? marks[rt].first_seen(sq.place0, sq.rows, a.kv.window) : 0;
+    } else {
+      hi[rt] = on ? min(place, rg.end - 1) : -1;
+      lo[rt] = a.kv.window ? place - a.kv.window + 1 : 0;
+    }
     const T* qp = (const T*)a.q + (int64_t)(sq.off + m) * a.qs + (int64_t)h * D;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
@@ -557,7 +607,8 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
     }
   }
   // Tokens between these need no mask.
-  const int all_hi = min(first, rg.end - 1), all_lo = a.kv.window ? last - a.kv.window + 1 : 0;
+  const int all_hi = min(kTree ? sq.place0 - 1 : first, rg.end - 1);
+  const int all_lo = a.kv.window ? (kTree ? sq.place0 + sq.rows - 1 : last) - a.kv.window + 1 : 0;
 
   float mx[RT], sum[RT];
   f32x4v o[RT][CB];
@@ -584,6 +635,12 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
         const int tk = tok0 + 16 * u + l16;
         if (tk < rg.beg || tk >= rg.end) vc[u].clear();
       }
+    }
+    uint32_t see[RT];  // of a tree: bit i for token tok0 + i
+    if constexpr (kTree) {
+      const bool among = tok0 + kAttnTile > sq.place0;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) see[rt] = among ? marks[rt].bits(tok0 - sq.place0) : ~0u;
     }
     f32x4v s[RT][2];
 #pragma unroll
@@ -625,7 +682,9 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int tk = tok0 + 16 * u + 4 * g + i;
-            if (gone[u] || tk > hi[rt] || tk < lo[rt]) s[rt][u][i] = -INFINITY;
+            bool hidden = gone[u] || tk > hi[rt] || tk < lo[rt];
+            if constexpr (kTree) hidden |= !(see[rt] >> (16 * u + 4 * g + i) & 1);
+            if (hidden) s[rt][u][i] = -INFINITY;
           }
     }
     // Softmax.  The maximum in use follows only where a score passes it by

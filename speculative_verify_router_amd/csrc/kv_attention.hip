@@ -1,6 +1,8 @@
-// Host side of attention over the paged 4-bit cache (include/moe_kv.h): the
+// Host side of attention over the paged 4-bit cache (include/moe_kv.h, and
+// with rows of a tree include/moe_tree.h): the
 // split of the work, and the kernel that joins the splits of a row.
 #include "kv_attention.h"
+#include "tree.h"
 
 namespace svr {
 
@@ -50,7 +52,8 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(AttnArgs a) {
   const int span = 16 * a.row_tiles, G = a.G.d;
   const int r0 = (m * G + (int)blockIdx.x - kvh * G) & ~(span - 1);
   const int r_last = min(sq.rows * G, r0 + span) - 1;
-  const KvRange rg = kv_range(a, sq.len, sq.place0 + a.G.of(r0), sq.place0 + a.G.of(r_last), per);
+  const KvRange rg = a.mask ? kv_tree_range(a, sq, per)
+                            : kv_range(a, sq.len, sq.place0 + a.G.of(r0), sq.place0 + a.G.of(r_last), per);
   if (rg.whole()) return;  // written already
   float M = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -216,35 +219,10 @@ size_t attn_most_bytes(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtyp
   return most;
 }
 
-}  // namespace
-}  // namespace svr
-
-using namespace svr;
-
-extern "C" {
-
-int32_t moe_kv_attention_workspace_bytes(const moe_kv_desc* desc, const moe_kv_batch* batch,
-                                         size_t* bytes) {
-  if (!bytes) return MOE_ERR_NULL;
-  int32_t rc = kv_check_desc(desc);
-  if (rc == MOE_OK) rc = kv_check_batch(desc, batch, false);
-  if (rc != MOE_OK) return rc;
-  size_t most = 0;
-  for (int32_t t : {MOE_F32, MOE_BF16, MOE_F16}) {
-    const size_t n = attn_most_bytes(desc, batch, t);
-    most = n > most ? n : most;
-  }
-  *bytes = most;
-  return MOE_OK;
-}
-
-int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int32_t dtype,
-                         const void* q, int64_t q_stride, const void* cache, int32_t n_pages,
-                         void* out, float* lse, void* workspace, size_t workspace_bytes,
-                         void* hip_stream) {
-  int32_t rc = kv_check_desc(desc);
-  if (rc == MOE_OK) rc = kv_check_batch(desc, batch, true);
-  if (rc != MOE_OK) return rc;
+// Attention of a batch's rows; mask: those of a tree (NULL: each sees the ones before it).
+int32_t attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int32_t dtype, const uint64_t* mask,
+                  int32_t mask_words, const void* q, int64_t q_stride, const void* cache, int32_t n_pages,
+                  void* out, float* lse, void* workspace, size_t workspace_bytes, void* hip_stream) {
   const int es = kv_elem_size(dtype);
   if (!es) return MOE_ERR_DTYPE;
   if (n_pages < 1) return MOE_ERR_SHAPE;
@@ -280,6 +258,10 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
   a.group = make_divider(p.group);
   a.min_tiles = p.min_tiles;
   a.row_tiles = p.row_tiles;
+  // Rows of a tile: whole tokens, and one cut at either end; those of a tree: all of them.
+  a.reach = a.kv.window + (mask ? batch->max_rows : 16 * p.row_tiles / a.G.d) + 2 + kAttnTile;
+  a.mask = reinterpret_cast<const uint32_t*>(mask);
+  a.mask_words = 2 * mask_words;
   a.by_seq = p.by_seq;
   a.search = p.search;
   a.first = p.first;
@@ -287,6 +269,7 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
   a.rows = make_divider(batch->max_rows);
   hipStream_t st = (hipStream_t)hip_stream;
   (void)hipGetLastError();
+  int32_t rc;
   switch (desc->head_dim) {
     case 64: rc = launch_kv_attention<64>(a, dtype, p.row_tiles, p.waves, (int)p.grid, st); break;
     case 128: rc = launch_kv_attention<128>(a, dtype, p.row_tiles, p.waves, (int)p.grid, st); break;
@@ -302,6 +285,55 @@ int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int
     default: launch_kv_join<256>(a, dtype, n, st); break;
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+}  // namespace
+}  // namespace svr
+
+using namespace svr;
+
+extern "C" {
+
+int32_t moe_kv_attention_workspace_bytes(const moe_kv_desc* desc, const moe_kv_batch* batch,
+                                         size_t* bytes) {
+  if (!bytes) return MOE_ERR_NULL;
+  int32_t rc = kv_check_desc(desc);
+  if (rc == MOE_OK) rc = kv_check_batch(desc, batch, false);
+  if (rc != MOE_OK) return rc;
+  size_t most = 0;
+  for (int32_t t : {MOE_F32, MOE_BF16, MOE_F16}) {
+    const size_t n = attn_most_bytes(desc, batch, t);
+    most = n > most ? n : most;
+  }
+  *bytes = most;
+  return MOE_OK;
+}
+
+int32_t moe_kv_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int32_t dtype,
+                         const void* q, int64_t q_stride, const void* cache, int32_t n_pages,
+                         void* out, float* lse, void* workspace, size_t workspace_bytes,
+                         void* hip_stream) {
+  int32_t rc = kv_check_desc(desc);
+  if (rc == MOE_OK) rc = kv_check_batch(desc, batch, true);
+  if (rc != MOE_OK) return rc;
+  return attention(desc, batch, dtype, nullptr, 0, q, q_stride, cache, n_pages, out, lse, workspace,
+                   workspace_bytes, hip_stream);
+}
+
+int32_t moe_kv_tree_attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int32_t dtype,
+                              const uint64_t* mask, int32_t mask_words, const void* q,
+                              int64_t q_stride, const void* cache, int32_t n_pages, void* out,
+                              float* lse, void* workspace, size_t workspace_bytes,
+                              void* hip_stream) {
+  int32_t rc = kv_check_desc(desc);
+  if (rc == MOE_OK) rc = kv_check_batch(desc, batch, true);
+  if (rc != MOE_OK) return rc;
+  if (mask_words < 1 || mask_words > MOE_TREE_MAX_ROWS / 64 || batch->max_rows > 64 * mask_words)
+    return MOE_ERR_SHAPE;
+  if (batch->n_tokens > 0 && batch->n_seqs > 0 && batch->max_rows > 0 && !mask) return MOE_ERR_NULL;
+  if ((uintptr_t)mask % 8) return MOE_ERR_ARG;
+  return attention(desc, batch, dtype, mask, mask_words, q, q_stride, cache, n_pages, out, lse,
+                   workspace, workspace_bytes, hip_stream);
 }
 
 }  // extern "C"

@@ -11,8 +11,12 @@ int32_t launch_kv_attention(const AttnArgs& a, int32_t dtype, int row_tiles, int
   const dim3 n(grid), t(waves * kWave);
 #define SVR_ATTN(RT, NT, W, T)                                                          \
   if constexpr (RT <= attn_most_row_tiles(D, NT)) {                                     \
-    if (row_tiles == RT && waves == W)                                                  \
-      hipLaunchKernelGGL((k_kv_attention<D, RT, NT, W, T>), n, t, 0, st, a);            \
+    if (row_tiles == RT && waves == W) {                                                \
+      if (a.mask)                                                                       \
+        hipLaunchKernelGGL((k_kv_attention<D, RT, NT, W, T, true>), n, t, 0, st, a);    \
+      else                                                                              \
+        hipLaunchKernelGGL((k_kv_attention<D, RT, NT, W, T, false>), n, t, 0, st, a);   \
+    }                                                                                   \
   }
   if (dtype == MOE_BF16) {
     SVR_ATTN(1, 1, kAttnWaves, bf16)

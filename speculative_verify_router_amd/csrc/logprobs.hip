@@ -29,12 +29,11 @@
 
 #include "common.h"
 #include "moe_logprobs.h"
+#include "row_tile.h"
 
 namespace svr {
 namespace {
 
-constexpr int kLpCols = 16;                // columns of a lane in a tile
-constexpr int kLpTile = kLpCols * kWave;   // columns of a wave's tile
 // Rows of several workgroups are rows of a small batch: kLpSpread workgroups
 // a call are wanted, so a row is cut only where there are at most half as many.
 constexpr int kLpSpread = 1024;
@@ -197,54 +196,9 @@ struct TopKeys {
   }
 };
 
-// 16 columns of a lane: pieces of 16 bytes, lane after lane.  Kept as the
-// words they come in: as elements, the compiler takes 16-bit ones apart where
-// they are loaded, and waits for them there.
-template <typename T>
-struct LpTile {
-  static constexpr int kElems = 16 / sizeof(T);  // of a piece
-  static constexpr int kPieces = kLpCols / kElems;
-  uint32_t w[4 * kPieces];
-
-  // Of the tile at column base, past the caches; columns from V on are -inf.
-  // (The memory path takes 16 bytes at any address.)
-  __device__ __forceinline__ void load(const T* row, int base, int V, int lane) {
-    const T* at = row + base + lane * kElems;
-    if (base + kLpTile <= V) {
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p) {
-        typedef uint32_t Four __attribute__((ext_vector_type(4), aligned(2)));
-        const Four q = __builtin_nontemporal_load(reinterpret_cast<const Four*>(at + p * (kElems * kWave)));
-        __builtin_memcpy(w + 4 * p, &q, 16);
-      }
-    } else {
-      T x[kLpCols];
-#pragma unroll
-      for (int e = 0; e < kLpCols; ++e) {
-        const int c = (e / kElems) * (kElems * kWave) + e % kElems;
-        x[e] = base + lane * kElems + c < V ? at[c] : (T)-INFINITY;
-      }
-      __builtin_memcpy(w, x, sizeof(x));
-    }
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < 4 * kPieces; ++i) w[i] = 0;
-  }
-  // Whole words up to here, and waited for here.
-  __device__ __forceinline__ void arrive() {
-#pragma unroll
-    for (int i = 0; i < 4 * kPieces; ++i) asm("" : "+v"(w[i]));
-  }
-  __device__ __forceinline__ float operator[](int e) const {
-    if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, w[e]);
-    else return (float)__builtin_bit_cast(T, (uint16_t)(e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu));
-  }
-};
-
 template <typename T>
 __global__ __launch_bounds__(kBlock) void k_logprobs(LpArgs a) {
-  constexpr int E = LpTile<T>::kElems;
+  constexpr int E = RowTile<T>::kElems;
   __shared__ uint64_t s_buf[kWavesPerBlock][2 * kWave];
   __shared__ Sums s_sums[kWavesPerBlock];
   __shared__ int s_last;
@@ -263,20 +217,20 @@ __global__ __launch_bounds__(kBlock) void k_logprobs(LpArgs a) {
   Sums s{-INFINITY, 0.f, 0.f};
   TopKeys top{s_buf[wv], a.k, a.k ? 0ull : ~0ull};
   // (Columns stay below 2^30 + a tile of each wave.)
-  const int c_begin = blk * a.tiles_per_block * kLpTile;
-  const int c_end = min(c_begin + a.tiles_per_block * kLpTile, a.V);
-  LpTile<T> raw;
-  int base = c_begin + wv * kLpTile;
+  const int c_begin = blk * a.tiles_per_block * kRowTile;
+  const int c_end = min(c_begin + a.tiles_per_block * kRowTile, a.V);
+  RowTile<T> raw;
+  int base = c_begin + wv * kRowTile;
   if (base < c_end) raw.load(x, base, a.V, lane);
-  for (; base < c_end; base += kWavesPerBlock * kLpTile) {
-    float v[kLpCols], mx = -INFINITY;
+  for (; base < c_end; base += kWavesPerBlock * kRowTile) {
+    float v[kTileCols], mx = -INFINITY;
     raw.arrive();
 #pragma unroll
-    for (int e = 0; e < kLpCols; ++e) {
+    for (int e = 0; e < kTileCols; ++e) {
       v[e] = raw[e];
       mx = fmaxf(mx, v[e]);
     }
-    const int next = base + kWavesPerBlock * kLpTile;
+    const int next = base + kWavesPerBlock * kRowTile;
     if (next < c_end) raw.load(x, next, a.V, lane);
     else raw.clear();  // nothing kept, which would be copied in every tile
     if (mx > s.m) s = lp_join(s, Sums{mx, 0.f, 0.f});
@@ -284,7 +238,7 @@ __global__ __launch_bounds__(kBlock) void k_logprobs(LpArgs a) {
     // Four chains each, then one addition to the sums of all tiles.
     float z[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < kLpCols; ++e) {
+    for (int e = 0; e < kTileCols; ++e) {
       const float d = v[e] - m;
       const float w = __builtin_amdgcn_exp2f(d * kLog2e);
       z[e & 3] += w;
@@ -298,13 +252,13 @@ __global__ __launch_bounds__(kBlock) void k_logprobs(LpArgs a) {
       if (top.thr == 0 || __popcll(in) >= a.k) top.raise(column(0) < a.V ? order_key(mx) : 0u);
       const float above = key_value((uint32_t)(top.thr >> 32));
       if (top.held == a.k && above > -INFINITY && __popcll(in) <= 8) {
-        top.one_by_one<kLpCols>([&](int e) { return v[e] >= above; },
+        top.one_by_one<kTileCols>([&](int e) { return v[e] >= above; },
                                 [&](int e) { return lp_key(v[e], (uint32_t)column(e)); });
       } else {  // -inf and NaN too, which no comparison of values tells apart
-        uint64_t key[kLpCols];
+        uint64_t key[kTileCols];
 #pragma unroll
-        for (int e = 0; e < kLpCols; ++e) key[e] = column(e) < a.V ? lp_key(v[e], (uint32_t)column(e)) : 0;
-        top.together<kLpCols>([&](int e) { return key[e] > top.thr; }, [&](int e) { return key[e]; });
+        for (int e = 0; e < kTileCols; ++e) key[e] = column(e) < a.V ? lp_key(v[e], (uint32_t)column(e)) : 0;
+        top.together<kTileCols>([&](int e) { return key[e] > top.thr; }, [&](int e) { return key[e]; });
       }
     }
   }
@@ -403,7 +357,7 @@ struct LpPlan {
 // with less than a tile a wave.
 LpPlan lp_plan(int64_t rows, int64_t vocab, int k) {
   LpPlan p{};
-  const int64_t tiles = (vocab + kLpTile - 1) / kLpTile;
+  const int64_t tiles = (vocab + kRowTile - 1) / kRowTile;
   const int64_t most = (tiles + kWavesPerBlock - 1) / kWavesPerBlock;
   int64_t want = kLpSpread / (rows > 0 ? rows : 1);
   want = want < 1 ? 1 : want > most ? most : want;
