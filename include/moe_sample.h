@@ -7,10 +7,10 @@
  *
  * The target's distribution after row n of a sequence with temperature T:
  *   p(x) = e^(l_x / T) / sum_y e^(l_y / T).
- * NaN and -inf have probability zero, +inf counts as the largest float.  A
- * temperature that is not above zero (0, negative, NaN) is greedy: p is one for
- * the largest logit (the lowest column of equal ones) and zero elsewhere, and
- * no random number matters.
+ * NaN, -inf and the lowest float have probability zero, +inf counts as the
+ * largest float.  A temperature above 2^64 counts as that; one below 2^-126 (0,
+ * negative) or NaN is greedy: p is one for the largest logit (the lowest column
+ * of equal ones) and zero elsewhere, and no random number matters.
  *
  * From the root on, a row's children (moe_tree.h) are tried in ascending
  * order.  Child k has the token x_k and the random number u_k in [0, 1).
@@ -27,10 +27,11 @@
  * (or that has none) gives one more token: the first column whose cumulative
  * weight is above sample_u[b] times the sum of what is left of p, or of w.
  * Where nothing is left it is the target's most likely token; -1 where the row
- * has no distribution (all logits NaN or -inf), after which nothing is accepted.
+ * has no distribution (no logit that counts), after which nothing is accepted.
  *
- * Weights, sums and comparisons are 64-bit, in an order that depends on the
- * sizes alone: borders of the cumulative sum lie closer than 32 bits resolve.
+ * Weights (to 1e-13 of them), sums and comparisons are 64-bit, in an order that
+ * depends on the sizes alone: borders of the cumulative sum lie closer than 32
+ * bits resolve.
  * Status codes, ownership and ordering are those of moe_layer.h.
  */
 #ifndef SVR_MOE_SAMPLE_H

@@ -17,16 +17,16 @@ LARGEST = float(np.finfo(np.float32).max)
 def distribution(x, temperature):
     """The target's probabilities of one row of logits, or None where it has none."""
     x = np.asarray(x, np.float64).copy()
-    x[np.isnan(x)] = -np.inf
+    x[np.isnan(x) | (x <= -LARGEST)] = -np.inf
     x[np.isposinf(x)] = LARGEST
     if np.isneginf(x).all():
         return None
     p = np.zeros_like(x)
-    if not temperature > 0:
+    if not temperature >= 2.0 ** -126:
         p[np.argmax(x)] = 1.0
         return p
     some = x > -np.inf
-    e = np.exp((x[some] - x.max()) / temperature)
+    e = np.exp((x[some] - x.max()) / min(temperature, 2.0 ** 64))
     p[some] = e / e.sum()
     return p
 
@@ -46,7 +46,7 @@ def sequence(logits, parents, tokens, draft_probs, temperature, accept_u, sample
     while True:
         r = off + path[-1]
         p = distribution(logits[r], temperature)
-        greedy = not temperature > 0
+        greedy = not temperature >= 2.0 ** -126
         best = None if p is None else int(np.argmax(p))  # (equal ones: the lower column)
         went = None
         for c in to.children(parents, off, rows, path[-1], most):

@@ -9,9 +9,8 @@
 // in it.
 //   Weights are 64-bit: a column weighs 1e-6 of a row, so a cumulative sum of
 // 32 bits would give another token one time in a hundred.  2^t for t <= 0 is
-// a power of two times its Taylor sum on [-1/2, 1/2] (to (t ln 2)^11 / 11!: the
-// rest is below 7e-15); 64-bit products and sums run at the rate of 32-bit ones
-// here.
+// a power of two times a polynomial of degree nine on [-1/2, 1/2], the one
+// whose largest relative error is least (8e-14) of those that are 1 at 0.
 //   Given drafts: a row's children are left out of its tiles' sums and weighed
 // one by one.  At the row where the path ends all of them are rejected, so the
 // tiles' sums are those of what is left, with nothing subtracted; one launch.
@@ -29,7 +28,9 @@ namespace svr {
 namespace {
 
 constexpr size_t kSampleCounterBytes = 2 * MOE_SAMPLE_MAX_ROWS * sizeof(unsigned);
-constexpr int kSampleSpread = 2048;  // workgroups of a call that are wanted
+// Workgroups of a call that are wanted: for all rows, and for the rounds of
+// drawn drafts, most of whose rows are done.
+constexpr int kSampleSpread = 2048, kRoundSpread = 2048;
 
 struct SampleArgs {
   TreeArgs tree;
@@ -50,8 +51,8 @@ struct SampleArgs {
   int last;        // the launch that ends the call
 };
 
-// What a row's last workgroup finds, five words: the sum z relative to its
-// maximum, c and S of the drafts rejected so far, the maximum and a token
+// What a row's last workgroup finds, five words: one over its sum relative to
+// its maximum (given drafts: the sum without them), c and S of the drafts rejected so far, the maximum and a token
 // (greedy: the largest; given drafts with nothing else left: the best of them),
 // the accepted child and how many were tried.
 constexpr int kInfo = 5;
@@ -82,34 +83,51 @@ __device__ __forceinline__ RowInfo load_info(const uint64_t* p) {
   return r;
 }
 
-// A logit as the definition takes it: NaN as -inf, +inf as the largest float.
+// A logit as the definition takes it: NaN and -inf as the lowest float, which
+// has no weight, +inf as the largest.  (A signalling NaN is made a quiet one
+// first: the median of three would give that one back.  Of a bf16 one the
+// compiler would take that as done.)
+constexpr float kLargest = 3.4028234663852886e38f;
 __device__ __forceinline__ float finite(float v) {
-  return v > -INFINITY ? fminf(v, 3.4028234663852886e38f) : -INFINITY;
+  asm("" : "+v"(v));
+  return __builtin_amdgcn_fmed3f(__builtin_canonicalizef(v), -kLargest, kLargest);
 }
+__device__ __forceinline__ bool counts(float v) { return v > -kLargest; }
 
-// 2^t for t <= 0; 0 for -inf and NaN.
-__device__ __forceinline__ double exp2_below(double t) {
-  t = fmax(t, -1100.0);
-  const double k = __builtin_rint(t), r = t - k;
-  // (ln 2)^n / n!
-  double p = 4.44553827187081e-10;
-  p = fma(p, r, 7.054911620801121e-09);
-  p = fma(p, r, 1.0178086009239696e-07);
-  p = fma(p, r, 1.3215486790144305e-06);
-  p = fma(p, r, 1.5252733804059838e-05);
-  p = fma(p, r, 0.00015403530393381606);
-  p = fma(p, r, 0.0013333558146428441);
-  p = fma(p, r, 0.009618129107628477);
-  p = fma(p, r, 0.055504108664821576);
-  p = fma(p, r, 0.2402265069591007);
-  p = fma(p, r, 0.6931471805599453);
-  p = fma(p, r, 1.0);
-  return __builtin_ldexp(p, (int)k);
+// To a whole number as the instruction does it: it stops at the type's ends,
+// where a conversion in C++ means nothing.
+__device__ __forceinline__ int whole(double k) {
+  int i;
+  asm("v_cvt_i32_f64 %0, %1" : "=v"(i) : "v"(k));
+  return i;
 }
-// The weight of a logit v <= m.
+// 2^t for finite t <= 0, to 8e-14 of it.
+__device__ __forceinline__ double exp2_below(double t) {
+#pragma clang fp contract(off)
+  const double k = __builtin_rint(t), r = t - k;
+  double p = 9.168151968465799e-08;
+  p = fma(p, r, 1.3255182694780334e-06);
+  p = fma(p, r, 1.525849287352463e-05);
+  p = fma(p, r, 0.00015403456037099);
+  p = fma(p, r, 0.0013333547331838614);
+  p = fma(p, r, 0.00961812915917161);
+  p = fma(p, r, 0.05550410873970943);
+  p = fma(p, r, 0.2402265069581371);
+  p = fma(p, r, 0.6931471805585506);
+  p = fma(p, r, 1.0);
+  return __builtin_amdgcn_ldexp(p, whole(k));
+}
+// The weight of a finite logit v <= m.  (The product is rounded before its
+// whole part is taken off: of a huge one, an exact product would leave a huge rest.)
 __device__ __forceinline__ double weight(float v, float m, double scale) {
+#pragma clang fp contract(off)
   return exp2_below(((double)v - (double)m) * scale);
 }
+
+// The same outside of the loops over columns.  What a launch does last, its last
+// workgroups do alone, with instructions that come from memory as they go: as
+// one function these are fewer.
+__device__ __attribute__((noinline)) double weight_once(float v, float m, double scale) { return weight(v, m, scale); }
 
 // Over the wave: sums of lanes 0 .. own (the same in every run), in the last
 // lane that of all.
@@ -128,41 +146,22 @@ __device__ __forceinline__ double wave_scan_d(double v) {
   v += dpp_d<kDppBcast31, 0xC>(v);
   return v;
 }
-__device__ __forceinline__ double last_lane(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, two((uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, kWave - 1),
-                                        (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), kWave - 1)));
-}
 __device__ __forceinline__ float wave_max(float v) { return key_value(wave_max_u32(order_key(v))); }
 
-// Shared memory of the last workgroup of a row, and of a sequence.
+// Shared memory of a row's workgroup.
 struct Shared {
-  int kid[MOE_TREE_MAX_ROWS];   // places of a row's children
-  int tok[MOE_TREE_MAX_ROWS];   // their tokens; the path
-  union {
-    float val[MOE_TREE_MAX_ROWS];  // their logits, -inf for those that cannot be accepted
-    int chosen[MOE_TREE_MAX_ROWS];
-    double w[kRowTile];            // weights of a tile
-  };
+  int kid[MOE_TREE_MAX_ROWS];  // places of the row's children
+  int tok[MOE_TREE_MAX_ROWS];  // their tokens
+  int chosen[MOE_TREE_MAX_ROWS];
+  int path[MOE_TREE_MAX_ROWS];  // the accepted rows; the rows of a round
   double sum[kWavesPerBlock];
-  float mx[kWavesPerBlock];
   int at[kWavesPerBlock];
-  int kids, last, n, tile;
+  int kids, last, n, tile;  // n: entries of path, less one
   double rest;
   RowInfo info;
 };
 
 // Over the workgroup, in every thread; barriers on both sides.
-__device__ __forceinline__ float block_max(Shared& s, float v) {
-  v = wave_max(v);
-  if ((threadIdx.x & (kWave - 1)) == 0) s.mx[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = s.mx[0];
-#pragma unroll
-  for (int w = 1; w < kWavesPerBlock; ++w) v = fmaxf(v, s.mx[w]);
-  __syncthreads();
-  return v;
-}
 __device__ __forceinline__ int block_min(Shared& s, uint32_t v) {
   v = wave_min_u32(v);
   if ((threadIdx.x & (kWave - 1)) == 0) s.at[threadIdx.x >> 6] = (int)v;
@@ -201,53 +200,94 @@ struct Row {
   double scale;  // log2(e) / T
   bool greedy;
 };
+__device__ __forceinline__ void set_temperature(Row& r, float t) {
+  r.greedy = !(t >= 1.17549435e-38f);  // (smaller ones may read as zero, here or there)
+  r.scale = r.greedy ? 1.0 : 1.4426950408889634 / fmin((double)t, 1.8446744073709552e19);
+}
 __device__ __forceinline__ Row find_row(const SampleArgs& a, int row) {
-  KvArgs k{};
-  k.offs = a.tree.offs;
-  k.n_seqs = a.tree.n_seqs;
   Row r{};
   r.row = row;
-  r.b = kv_sequence_of(k, row);
-  if (r.b < 0) return r;
-  r.seq = tree_rows(a.tree, r.b);
+  float t = 1.f;
+  if (a.tree.n_seqs < kWave) {  // every offset and temperature at once: one wait instead of three
+    const int lane = threadIdx.x & (kWave - 1);
+    const int off = a.tree.offs[min(lane, a.tree.n_seqs)];
+    const float temp = a.temp ? a.temp[min(lane, a.tree.n_seqs - 1)] : 1.f;
+    r.b = __popcll(__ballot(lane <= a.tree.n_seqs && off <= row)) - 1;
+    if (r.b >= a.tree.n_seqs) r.b = -1;
+    if (r.b < 0) return r;
+    r.seq = tree_rows(a.tree, __builtin_amdgcn_readlane(off, r.b), __builtin_amdgcn_readlane(off, r.b + 1));
+    t = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, temp), r.b));
+  } else {
+    KvArgs k{};
+    k.offs = a.tree.offs;
+    k.n_seqs = a.tree.n_seqs;
+    r.b = kv_sequence_of(k, row);
+    if (r.b < 0) return r;
+    r.seq = tree_rows(a.tree, r.b);
+    if (a.temp) t = a.temp[r.b];
+  }
   r.i = row - r.seq.off;
-  if (r.i >= r.seq.rows) {
+  if ((unsigned)r.i >= (unsigned)r.seq.rows) {
     r.b = -1;
     return r;
   }
-  const float t = a.temp ? a.temp[r.b] : 1.f;
-  r.greedy = !(t > 0.f);
-  r.scale = r.greedy ? 1.0 : 1.4426950408889634 / (double)t;
+  set_temperature(r, t);
   return r;
 }
 
-// The children of row i, in order: their places and tokens.  By one wave.
-__device__ __forceinline__ void list_children(const SampleArgs& a, const TreeRows& seq, int i, Shared& s) {
+// The children of row i, in order: their places and tokens.  By one wave.  The
+// next 64 rows' tokens and parents may have been asked for before it was known
+// where their sequence ends.
+struct Next {
+  int token, parent;
+};
+__device__ __forceinline__ Next load_next(const SampleArgs& a, int row) {
+  const int j = min(row + 1 + (int)(threadIdx.x & (kWave - 1)), a.tree.n_rows - 1);
+  return Next{a.tokens[j], a.tree.parents ? a.tree.parents[j] : 0};
+}
+__device__ __forceinline__ void list_children(const SampleArgs& a, const TreeRows& seq, int i, Shared& s, Next next) {
   const int lane = threadIdx.x & (kWave - 1);
   int n = 0;
-  if (!a.tree.parents) {
-    n = i + 1 < seq.rows;
-    if (n && lane == 0) {
-      s.kid[0] = i + 1;
-      s.tok[0] = a.tokens[seq.off + i + 1];
+  for (int j0 = i + 1;;) {
+    const int j = j0 + lane;
+    const bool is = j < seq.rows && (a.tree.parents ? next.parent == i : j == i + 1);
+    const uint64_t m = __ballot(is);
+    const int at = n + __popcll(m & ((1ull << lane) - 1));
+    if (is && at < a.tree.max_children) {
+      s.kid[at] = j;
+      s.tok[at] = next.token;
     }
-  } else {
-    for (int j0 = (i + 1) & ~(kWave - 1); j0 < seq.rows && n < a.tree.max_children; j0 += kWave) {
-      const int j = j0 + lane;
-      const bool in = j > i && j < seq.rows;
-      const int token = in ? a.tokens[seq.off + j] : 0;
-      const bool is = in && a.tree.parents[seq.off + j] == i;
-      const uint64_t m = __ballot(is);
-      const int at = n + __popcll(m & ((1ull << lane) - 1));
-      if (is && at < a.tree.max_children) {
-        s.kid[at] = j;
-        s.tok[at] = token;
-      }
-      n += __popcll(m);
-    }
-    n = min(n, a.tree.max_children);
+    n = min(n + (int)__popcll(m), a.tree.max_children);
+    j0 += kWave;
+    if (!a.tree.parents || j0 >= seq.rows || n == a.tree.max_children) break;
+    next = load_next(a, seq.off + j0 - 1);
   }
   if (lane == 0) s.kids = n;
+}
+
+// What a child is tried with.  Asked for while the row's logits are on their
+// way, by thread k for child k: the row's last workgroup needs it at once.
+struct Kid {
+  float val, u, q;
+};
+template <typename T>
+__device__ __forceinline__ Kid load_kid(const SampleArgs& a, const Row& r, const Shared& s, int k) {
+  Kid c{-kLargest, 1.f, 0.f};
+  if (k >= s.kids) return c;
+  const int t = s.tok[k];
+  if (t >= 0 && t < a.V) {
+    c.val = (float)((const T*)a.x)[(int64_t)r.row * a.stride + t];
+    c.u = a.accept_u[r.seq.off + s.kid[k]];
+    if (a.q) c.q = a.q[(int64_t)r.row * a.q_stride + t];
+  }
+  return c;
+}
+
+// A counter's place: 512 in a row lie in a line of 128 bytes each.  Those of one
+// line are counted one after another, however different (61 rows of 32
+// workgroups each: 26 us with the counters side by side, 18 so).
+__device__ __forceinline__ unsigned* counter(unsigned* ctr, int i) {
+  return ctr + ((i & 511) << 5 | i >> 9);
 }
 
 // Counts the caller in; whether it is the last of n.  The workgroup's shared
@@ -283,77 +323,117 @@ __device__ __forceinline__ int first_largest(const SampleArgs& a, int row, float
   return block_min(s, col);
 }
 
-// The row's sums from its tiles'.  kWithKids: and from its children, in s.val.
-template <bool kWithKids>
-__device__ __forceinline__ RowInfo join_row(const SampleArgs& a, const Row& r, Shared& s) {
-  const float* tm = a.tm + (int64_t)r.row * a.tiles;
-  const double* tz = a.tz + (int64_t)r.row * a.tiles;
-  RowInfo f{0.0, 0.0, 1.0, -INFINITY, kNone, kNone, 0};
-  float mx = -INFINITY;
-  for (int t = threadIdx.x; t < a.tiles; t += kBlock) mx = fmaxf(mx, load_shared(tm + t));
-  if (kWithKids)
-    for (int k = threadIdx.x; k < s.kids; k += kBlock) mx = fmaxf(mx, s.val[k]);
-  f.mx = block_max(s, mx);
-  if (f.mx == -INFINITY || r.greedy) return f;
-  double z = 0.0;
-  for (int t = threadIdx.x; t < a.tiles; t += kBlock) {
-    const float m = load_shared(tm + t);
-    if (m > -INFINITY) z += load_shared(tz + t) * weight(m, f.mx, r.scale);
-  }
-  f.z = block_scan(s, z).all;
-  return f;
+// Over the workgroup, in every thread; barriers on both sides.
+__device__ __forceinline__ float block_max(Shared& s, float v) {
+  v = wave_max(v);
+  if ((threadIdx.x & (kWave - 1)) == 0) s.at[threadIdx.x >> 6] = __builtin_bit_cast(int, v);
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWavesPerBlock; ++w) v = fmaxf(v, __builtin_bit_cast(float, s.at[w]));
+  __syncthreads();
+  return v;
 }
 
-// Drawn drafts from where they were left: f.s is the sum of what c leaves.  By
-// one thread.  Stops at the first that is accepted, or rejected (then open).
+// The row's maximum, over its tiles' and `also`, and its sum relative to that.
+struct Joined {
+  float m;
+  double z;
+};
+__device__ __forceinline__ Joined join_row(const SampleArgs& a, const Row& r, float also, Shared& s) {
+  const float* tm = a.tm + (int64_t)r.row * a.tiles;
+  const double* tz = a.tz + (int64_t)r.row * a.tiles;
+  const int first = min((int)threadIdx.x, a.tiles - 1);
+  float m = load_shared(tm + first);
+  double z = load_shared(tz + first);
+  if ((int)threadIdx.x >= a.tiles) z = 0.0;
+  float most = fmaxf(m, also);
+#pragma unroll 1
+  for (int t = threadIdx.x + kBlock; t < a.tiles; t += kBlock) most = fmaxf(most, load_shared(tm + t));
+  Joined j{block_max(s, most), 0.0};
+  if (!counts(j.m) || r.greedy) return j;
+  double sum = 0.0;
+#pragma unroll 1
+  for (int t = threadIdx.x;;) {
+    sum += z * weight_once(m, j.m, r.scale);
+    t += kBlock;
+    if (t >= a.tiles) break;
+    m = load_shared(tm + t);
+    z = load_shared(tz + t);
+  }
+  j.z = block_scan(s, sum).all;
+  return j;
+}
+
+__device__ __forceinline__ float of_lane(float v, int l) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+
+// Drawn drafts from where they were left: f.s is the sum of what c leaves.
+// Stops at the first that is accepted, or rejected (then open).  By one wave;
+// kid: of child `lane`.
 template <typename T>
-__device__ __forceinline__ void try_drawn(const SampleArgs& a, const Row& r, const Shared& s, RowInfo& f) {
-  const T* x = (const T*)a.x + (int64_t)r.row * a.stride;
-  const float* q = a.q + (int64_t)r.row * a.q_stride;
+__device__ __forceinline__ void try_drawn(const SampleArgs& a, const Row& r, const Shared& s, Kid kid, RowInfo& f) {
   f.chosen = kNone;
+#pragma unroll 1
   while (f.tried < s.kids) {
     const int k = f.tried++, t = s.tok[k];
     if (t < 0 || t >= a.V) continue;
-    if (r.greedy) {
-      if (t == f.best) f.chosen = s.kid[k];
-    } else if (f.z > 0.0) {
-      const double qt = fmax((double)q[t], 0.0), u = (double)a.accept_u[r.seq.off + s.kid[k]];
-      const double w = fmax(weight(finite((float)x[t]), f.mx, r.scale) / f.z - f.c * qt, 0.0);
-      if (u * qt * f.s < w) {
-        f.chosen = s.kid[k];
-      } else {
-        f.c += f.s;
-        f.chosen = kOpen;
-      }
+    if (k >= kWave) kid = load_kid<T>(a, r, s, (k & ~(kWave - 1)) + (int)threadIdx.x);
+    const int l = __builtin_amdgcn_readfirstlane(k & (kWave - 1));
+    const double q = fmax((double)of_lane(kid.q, l), 0.0);
+    const double w = fmax(weight_once(finite(of_lane(kid.val, l)), f.mx, r.scale) * f.z - f.c * q, 0.0);
+    if ((double)of_lane(kid.u, l) * q * f.s < w) {
+      f.chosen = s.kid[k];
+    } else {
+      f.c += f.s;
+      f.chosen = kOpen;
     }
-    if (f.chosen != kNone) return;
+    return;
   }
 }
 
-// Given drafts: the first whose u times what is left is below its weight.
-// By one wave.  f.z: the sum without them.
-__device__ __forceinline__ void try_given(const SampleArgs& a, const Row& r, Shared& s, RowInfo& f) {
+// Given drafts: the first whose u times what is left is below its weight.  By
+// the workgroup; kid: of child `threadIdx.x`.  One that an earlier child has
+// already, or that is no token, cannot be accepted.
+template <typename T>
+__device__ __forceinline__ void try_given(const SampleArgs& a, const Row& r, Shared& s, Kid kid, RowInfo& f) {
   const int lane = threadIdx.x & (kWave - 1);
-  double tail = f.z;
-  for (int k0 = (s.kids - 1) & ~(kWave - 1); k0 >= 0; k0 -= kWave) {
-    // Lanes from the last child to the first: sums of those that come later.
-    const int k = k0 + kWave - 1 - lane;
-    const bool in = k < s.kids;
-    const float v = in ? s.val[k] : -INFINITY;
-    const double w = v > -INFINITY ? weight(v, f.mx, r.scale) : 0.0;
-    const double u = in ? (double)a.accept_u[r.seq.off + s.kid[k]] : 1.0;
-    const double upto = wave_scan_d(w);
-    const uint64_t ok = __ballot(w > 0.0 && u * (tail + upto) < w);
-    if (ok) f.chosen = s.kid[k0 + __builtin_clzll(ok)];
-    tail += last_lane(upto);
+  auto of_child = [&](int k) {
+    Kid c = s.kids > kWave ? load_kid<T>(a, r, s, k) : kid;
+    bool ok = k < s.kids;
+#pragma unroll 1
+    for (int j = 0; j < k && ok; ++j) ok = s.tok[j] != s.tok[k];
+    c.val = ok ? finite(c.val) : -kLargest;
+    return c;
+  };
+  Kid c{-kLargest, 1.f, 0.f};
+  float most = -kLargest;
+  if (threadIdx.x < kWave) {
+    c = of_child(lane);
+    most = c.val;
+#pragma unroll 1
+    for (int k = lane + kWave; k < s.kids; k += kWave) most = fmaxf(most, of_child(k).val);
   }
-  if (f.z == 0.0) {  // the best of them, the lowest token of equal ones
-    float m = -INFINITY;
-    for (int k = 0; k < s.kids; ++k)
-      if (s.val[k] > m || (s.val[k] == m && m > -INFINITY && s.tok[k] < f.best)) {
-        m = s.val[k];
-        f.best = s.tok[k];
-      }
+  const Joined j = join_row(a, r, most, s);
+  f.mx = j.m;
+  f.z = j.z;
+  if (!counts(f.mx) || threadIdx.x >= kWave) return;
+  // From the last child to the first: the sum of those that come later.
+  double left = f.z;
+#pragma unroll 1
+  for (int k = s.kids - 1, k0 = kWave * (s.kids > kWave ? s.kids : 0); k >= 0; --k) {
+    if (k < k0) {  // (more than a wave's)
+      k0 = k & ~(kWave - 1);
+      c = of_child(k0 + lane);
+    }
+    const int l = __builtin_amdgcn_readfirstlane(k & (kWave - 1));
+    const float v = of_lane(c.val, l);
+    if (!counts(v)) continue;
+    const double w = weight_once(v, f.mx, r.scale);
+    left += w;
+    if (w > 0.0 && (double)of_lane(c.u, l) * left < w) f.chosen = s.kid[k];
+    // Nothing else left: the best of them, the lowest token of equal ones.
+    if (f.z == 0.0 && v == f.mx && (f.best < 0 || s.tok[k] < f.best)) f.best = s.tok[k];
   }
 }
 
@@ -362,107 +442,109 @@ __device__ __forceinline__ void try_given(const SampleArgs& a, const Row& r, Sha
 template <typename T>
 __device__ void finish(const SampleArgs& a, const Row& r, Shared& s) {
   const TreeRows& seq = r.seq;
-  for (int j = threadIdx.x; j < seq.rows; j += kBlock)
-    s.chosen[j] = (int)(uint32_t)load_shared(a.info + (int64_t)(seq.off + j) * kInfo + 4);
+  const float sample_u = a.sample_u[r.b];
+  // Each thread's first row is kept: the path's last row is likely among them.
+  RowInfo mine{};
+#pragma unroll 1
+  for (int j = threadIdx.x; j < seq.rows; j += kBlock) {
+    const RowInfo f = load_info(a.info + (int64_t)(seq.off + j) * kInfo);
+    s.chosen[j] = f.chosen;
+    if (j < kBlock) mine = f;
+  }
   __syncthreads();
   if (threadIdx.x == 0) {
     int n = 0, at = 0;
-    s.tok[0] = 0;
+    s.path[0] = 0;
     for (;;) {
       const int to = s.chosen[at];
       if (to <= at || to >= seq.rows) break;
       at = to;
-      s.tok[++n] = at;
+      s.path[++n] = at;
     }
     s.n = n;
-    s.info = load_info(a.info + (int64_t)(seq.off + at) * kInfo);
   }
   __syncthreads();
-  const int n = s.n, i = s.tok[n], row = seq.off + i;
-  const RowInfo f = s.info;
+  const int n = s.n, i = s.path[n], row = seq.off + i;
+  if ((int)threadIdx.x == (i < kBlock ? i : 0))
+    s.info = i < kBlock ? mine : load_info(a.info + (int64_t)row * kInfo);
+  // Threads take runs of the row's tiles, in order.
+  const float* tm = a.tm + (int64_t)row * a.tiles;
+  const double* tz = a.tz + (int64_t)row * a.tiles;
+  const int run = (a.tiles + kBlock - 1) / kBlock, t0 = min((int)threadIdx.x * run, a.tiles);
+  const int t1 = min(t0 + run, a.tiles);
+  const float m0 = load_shared(tm + min(t0, a.tiles - 1));
+  const double z0 = load_shared(tz + min(t0, a.tiles - 1));
+  if (!a.q && threadIdx.x < kWave) list_children(a, seq, i, s, load_next(a, row));
+
   int32_t* accepted = a.accepted + (int64_t)r.b * a.tree.max_rows;
+#pragma unroll 1
   for (int j = threadIdx.x; j < a.tree.max_rows; j += kBlock) {
-    if (j != n) accepted[j] = j < n ? a.tokens[seq.off + s.tok[j + 1]] : -1;
-    if (a.path) a.path[(int64_t)r.b * a.tree.max_rows + j] = j <= n ? s.tok[j] : -1;
+    if (j != n) accepted[j] = j < n ? a.tokens[seq.off + s.path[j + 1]] : -1;
+    if (a.path) a.path[(int64_t)r.b * a.tree.max_rows + j] = j <= n ? s.path[j] : -1;
   }
   if (threadIdx.x == 0) a.n_acc[r.b] = n;
   if (a.vh)
     for (int j = threadIdx.x; j < a.hdim; j += kBlock)
       a.pending[(int64_t)r.b * a.hdim + j] = a.vh[(int64_t)row * a.hdim + j];
-  __syncthreads();  // s.tok and s.chosen are done with
-
+  __syncthreads();
+  const RowInfo f = s.info;
   int token = f.best;
-  if (!r.greedy && f.mx > -INFINITY) {
-    // The tile: threads take runs of tiles, in order.
-    const float* tm = a.tm + (int64_t)row * a.tiles;
-    const double* tz = a.tz + (int64_t)row * a.tiles;
+  if (!r.greedy && counts(f.mx)) {
     const bool less = a.q && f.c > 0.0;  // sums of (p - c q)+
-    auto tile_sum = [&](int t) {
-      const double z = load_shared(tz + t);
-      if (less) return z;
-      const float m = load_shared(tm + t);
-      return m > -INFINITY ? z * weight(m, f.mx, r.scale) : 0.0;
-    };
-    const int run = (a.tiles + kBlock - 1) / kBlock, t0 = min((int)threadIdx.x * run, a.tiles);
-    const int t1 = min(t0 + run, a.tiles);
-    double mine = 0.0;
-    for (int t = t0; t < t1; ++t) mine += tile_sum(t);
-    const Scan sc = block_scan(s, mine);
-    const double want = (double)a.sample_u[r.b] * sc.all;
+    auto scaled = [&](double z, float m) { return less ? z : z * weight_once(m, f.mx, r.scale); };
+    const double head = t0 < t1 ? scaled(z0, m0) : 0.0;
+    double own = head;
+#pragma unroll 1
+    for (int t = t0 + 1; t < t1; ++t) own += scaled(load_shared(tz + t), load_shared(tm + t));
+    const Scan sc = block_scan(s, own);
+    const double want = (double)sample_u * sc.all;
     if (sc.all > 0.0) {
       // The first run that passes it; the last that holds anything where
       // rounding leaves none.
-      const bool holds = mine > 0.0;
-      int by = block_min(s, holds && sc.before + mine > want ? threadIdx.x : ~0u);
+      const bool holds = own > 0.0;
+      int by = block_min(s, holds && sc.before + own > want ? threadIdx.x : ~0u);
       if (by < 0) by = ~block_min(s, holds ? ~threadIdx.x : ~0u);
       if ((int)threadIdx.x == by) {
-        double before = sc.before;
-        int tile = t0, last = t0;
-        double rest = 0.0;
-        bool found = false;
-        for (int t = t0; t < t1 && !found; ++t) {
-          const double z = tile_sum(t);
-          if (z > 0.0) {
-            last = t;
-            rest = want - before;
-            if (before + z > want) {
-              tile = t;
-              found = true;
-            }
-          }
+        double before = sc.before, z = head;
+        s.tile = t0;
+        s.rest = want - before;
+#pragma unroll 1
+        for (int t = t0; !(before + z > want);) {
           before += z;
+          if (++t == t1) break;
+          z = scaled(load_shared(tz + t), load_shared(tm + t));
+          if (z > 0.0) {
+            s.tile = t;
+            s.rest = want - before;
+          }
         }
-        s.tile = found ? tile : last;
-        s.rest = rest;
-      }
-      if (threadIdx.x < kWave) {
-        if (!a.q) list_children(a, seq, i, s);
-        else if (threadIdx.x == 0) s.kids = 0;
       }
       __syncthreads();
-      const int base = s.tile * kRowTile;
+      // The column: four a thread, in order.
+      constexpr int kOwn = kRowTile / kBlock;
+      const int base = s.tile * kRowTile, c0 = base + (int)threadIdx.x * kOwn;
       const T* x = (const T*)a.x + (int64_t)row * a.stride;
       const float* q = a.q + (int64_t)row * a.q_stride;
-      for (int c = threadIdx.x; c < kRowTile; c += kBlock) {
-        double w = 0.0;
-        if (base + c < a.V) {
-          const float v = finite((float)x[base + c]);
-          if (v > -INFINITY) w = weight(v, f.mx, r.scale);
-          if (less) w = fmax(w / f.z - f.c * fmax((double)q[base + c], 0.0), 0.0);
-        }
-        s.w[c] = w;
-      }
-      __syncthreads();
-      for (int k = threadIdx.x; k < s.kids; k += kBlock) {
-        const int c = s.tok[k] - base;
-        if (s.tok[k] >= 0 && (unsigned)c < (unsigned)kRowTile) s.w[c] = 0.0;
-      }
-      __syncthreads();
-      constexpr int kOwn = kRowTile / kBlock;
-      double w[kOwn], own = 0.0;
+      double w[kOwn];
+      float v[kOwn], d[kOwn];
 #pragma unroll
       for (int e = 0; e < kOwn; ++e) {
-        w[e] = s.w[threadIdx.x * kOwn + e];
+        const int c = min(c0 + e, a.V - 1);
+        v[e] = (float)x[c];
+        d[e] = less ? q[c] : 0.f;
+      }
+      bool left_out[kOwn] = {};
+      if (!a.q)
+#pragma unroll 1
+        for (int k = 0; k < s.kids; ++k)
+#pragma unroll
+          for (int e = 0; e < kOwn; ++e) left_out[e] |= s.tok[k] == c0 + e;
+      own = 0.0;
+#pragma unroll
+      for (int e = 0; e < kOwn; ++e) {
+        v[e] = finite(v[e]);
+        w[e] = c0 + e < a.V && counts(v[e]) && !left_out[e] ? weight_once(v[e], f.mx, r.scale) : 0.0;
+        if (less) w[e] = fmax(w[e] * f.z - f.c * fmax((double)d[e], 0.0), 0.0);
         own += w[e];
       }
       double cum = block_scan(s, own).before;
@@ -492,19 +574,22 @@ __global__ __launch_bounds__(kBlock) void k_sample_rows(SampleArgs a) {
   __shared__ Shared s;
   const int lane = threadIdx.x & (kWave - 1), wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int blk = blockIdx.x % a.blocks;
-  const Row r = find_row(a, blockIdx.x / a.blocks);
-  if (r.b < 0) return;
+  const int row = blockIdx.x / a.blocks;
   constexpr int E = RowTile<T>::kElems;
-  const T* x = (const T*)a.x + (int64_t)r.row * a.stride;
+  const T* x = (const T*)a.x + (int64_t)row * a.stride;
   const int t_end = min((blk + 1) * a.tiles_per_block, a.tiles);
   int t = blk * a.tiles_per_block + wv;
   RowTile<T> raw;
-  if (t < t_end) raw.load(x, t * kRowTile, a.V, lane);
+  if (t < t_end) raw.load(x, t * kRowTile, a.V, lane);  // whatever row it is: all of them have logits
+  Next next{};
+  if (wv == 0) next = load_next(a, row);
+  const Row r = find_row(a, row);
+  if (r.b < 0) return;
   const bool leave_out = !kDrawn && !r.greedy;
-  if (leave_out) {
-    if (wv == 0) list_children(a, r.seq, r.i, s);
-    __syncthreads();
-  }
+  if (wv == 0) list_children(a, r.seq, r.i, s, next);
+  __syncthreads();
+  Kid kid{};
+  if (wv == 0) kid = load_kid<T>(a, r, s, lane);
   for (; t < t_end; t += kWavesPerBlock) {
     float v[kTileCols];
     raw.arrive();
@@ -522,7 +607,7 @@ __global__ __launch_bounds__(kBlock) void k_sample_rows(SampleArgs a) {
           if (at / E % kWave == lane)
 #pragma unroll
             for (int e = 0; e < kTileCols; ++e)
-              if (e == mine) v[e] = -INFINITY;
+              if (e == mine) v[e] = -kLargest;
         }
       }
     float m = v[0];
@@ -530,7 +615,7 @@ __global__ __launch_bounds__(kBlock) void k_sample_rows(SampleArgs a) {
     for (int e = 1; e < kTileCols; ++e) m = fmaxf(m, v[e]);
     m = wave_max(m);
     double z = 0.0;
-    if (m > -INFINITY && !r.greedy) {
+    if (counts(m) && !r.greedy) {
       double part[2] = {0.0, 0.0};
 #pragma unroll
       for (int e = 0; e < kTileCols; ++e) part[e & 1] += weight(v[e], m, r.scale);
@@ -541,43 +626,29 @@ __global__ __launch_bounds__(kBlock) void k_sample_rows(SampleArgs a) {
       store_shared(a.tz + (int64_t)r.row * a.tiles + t, z);
     }
   }
-  if (!last_of(a.row_ctr + r.row, a.blocks, s)) return;
+  if (!last_of(counter(a.row_ctr, r.row), a.blocks, s)) return;
 
-  if (!leave_out) {
-    if (wv == 0) list_children(a, r.seq, r.i, s);
-    __syncthreads();
-  } else {
-    // Their logits; one that an earlier child has already, or that is no
-    // token, cannot be accepted.
-    for (int k = threadIdx.x; k < s.kids; k += kBlock) {
-      const int c = s.tok[k];
-      bool ok = c >= 0 && c < a.V;
-      for (int j = 0; j < k && ok; ++j) ok = s.tok[j] != c;
-      s.val[k] = ok ? finite((float)x[c]) : -INFINITY;
-    }
-    __syncthreads();
-  }
-  RowInfo f;
+  RowInfo f{0.0, 0.0, 1.0, -kLargest, kNone, kNone, 0};
   if (leave_out) {
-    f = join_row<true>(a, r, s);
-    if (f.mx > -INFINITY && wv == 0) try_given(a, r, s, f);
+    try_given<T>(a, r, s, kid, f);
   } else {
-    f = join_row<false>(a, r, s);
-    if (f.mx > -INFINITY) {
-      if (r.greedy) f.best = first_largest<T>(a, r.row, f.mx, s);
-      if (threadIdx.x == 0) {
-        if (kDrawn) {
-          try_drawn<T>(a, r, s, f);
-        } else {
-          for (int k = 0; k < s.kids && f.chosen == kNone; ++k)
-            if (s.tok[k] == f.best) f.chosen = s.kid[k];
-        }
+    const Joined j = join_row(a, r, -kLargest, s);
+    if (counts(j.m)) {
+      if (r.greedy) {
+        f.best = first_largest<T>(a, r.row, j.m, s);
+#pragma unroll 1
+        for (int k = s.kids - 1; k >= 0; --k)
+          if (s.tok[k] == f.best) f.chosen = s.kid[k];
+      } else {
+        f.mx = j.m;
+        f.z = 1.0 / j.z;
+        if (wv == 0) try_drawn<T>(a, r, s, kid, f);
       }
     }
   }
   if (threadIdx.x == 0) store_info(a.info + (int64_t)r.row * kInfo, f);
   if (kDrawn) return;
-  if (last_of(a.seq_ctr + r.b, r.seq.rows, s)) finish<T>(a, r, s);
+  if (last_of(counter(a.seq_ctr, r.b), r.seq.rows, s)) finish<T>(a, r, s);
 }
 
 // 16 draft probabilities of a lane, of the columns that its logits have.
@@ -608,6 +679,7 @@ struct ProbTile {
 // launch change that meanwhile, only from can to cannot: workgroups of a row
 // may differ then, and what the row's sums are does not matter any more.
 __device__ __forceinline__ bool reachable(const SampleArgs& a, const Row& r, Shared& s) {
+#pragma unroll 1
   for (int j = 1 + (int)threadIdx.x; j <= r.i; j += kBlock) {
     const int p = tree_parent(a.tree, r.seq.off, j);
     bool on = false;
@@ -618,13 +690,9 @@ __device__ __forceinline__ bool reachable(const SampleArgs& a, const Row& r, Sha
     s.chosen[j] = on ? p : kNone;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int at = r.i;
-    while (at > 0) at = s.chosen[at];
-    s.n = at == 0;
-  }
-  __syncthreads();
-  return s.n;
+  int at = r.i;
+  while (at > 0) at = s.chosen[at];
+  return at == 0;
 }
 
 // Sums of (p - c q)+ of the rows that are open, and their next children.
@@ -633,64 +701,78 @@ __global__ __launch_bounds__(kBlock) void k_sample_round(SampleArgs a) {
   __shared__ Shared s;
   const int lane = threadIdx.x & (kWave - 1), wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int blk = blockIdx.x % a.blocks;
-  const Row r = find_row(a, blockIdx.x / a.blocks);
+  const int row = blockIdx.x / a.blocks;
+  uint64_t* info = a.info + (int64_t)row * kInfo;
+  RowInfo f = load_info(info);  // of the launch before (of a row of no sequence: whatever lies there)
+  const Row r = find_row(a, row);
   if (r.b < 0) return;
-  uint64_t* info = a.info + (int64_t)r.row * kInfo;
-  RowInfo f = load_info(info);  // of the launch before
   if (f.chosen == kOpen) {
-    const bool on = reachable(a, r, s);
+    const T* x = (const T*)a.x + (int64_t)r.row * a.stride;
+    const float* q = a.q + (int64_t)r.row * a.q_stride;
+    const int t_end = min((blk + 1) * a.tiles_per_block, a.tiles);
+    int t = blk * a.tiles_per_block + wv;
+    RowTile<T> raw;
+    ProbTile<RowTile<T>::kElems> draft;
+    if (t < t_end) {
+      raw.load(x, t * kRowTile, a.V, lane);
+      draft.load(q, t * kRowTile, a.V, lane);
+    }
+    if (wv == 0) list_children(a, r.seq, r.i, s, load_next(a, row));
+    const bool on = reachable(a, r, s);  // (and a barrier)
     if (on) {
-      const T* x = (const T*)a.x + (int64_t)r.row * a.stride;
-      const float* q = a.q + (int64_t)r.row * a.q_stride;
-      const double inv = 1.0 / f.z;
-      const int t_end = min((blk + 1) * a.tiles_per_block, a.tiles);
-      for (int t = blk * a.tiles_per_block + wv; t < t_end; t += kWavesPerBlock) {
-        RowTile<T> raw;
-        ProbTile<RowTile<T>::kElems> draft;
-        raw.load(x, t * kRowTile, a.V, lane);
-        draft.load(q, t * kRowTile, a.V, lane);
+      Kid kid{};
+      if (wv == 0) kid = load_kid<T>(a, r, s, lane);
+      const double share = f.c / f.z;
+      while (t < t_end) {
         double part[2] = {0.0, 0.0};
 #pragma unroll
         for (int e = 0; e < kTileCols; ++e) {
-          const double p = weight(finite(raw[e]), f.mx, r.scale) * inv;
-          part[e & 1] += fmax(p - f.c * fmax((double)draft.w[e], 0.0), 0.0);
+          const double w = weight(finite(raw[e]), f.mx, r.scale);
+          part[e & 1] += fmax(fma(-share, (double)fmaxf(draft.w[e], 0.f), w), 0.0);
         }
-        const double z = wave_scan_d(part[0] + part[1]);
+        const double z = wave_scan_d(part[0] + part[1]) * f.z;
         if (lane == kWave - 1) store_shared(a.tz + (int64_t)r.row * a.tiles + t, z);
+        t += kWavesPerBlock;
+        if (t < t_end) {
+          raw.load(x, t * kRowTile, a.V, lane);
+          draft.load(q, t * kRowTile, a.V, lane);
+        }
       }
-    }
-    if (!last_of(a.row_ctr + r.row, a.blocks, s)) return;
-    if (on) {
+      if (!last_of(counter(a.row_ctr, r.row), a.blocks, s)) return;
       double sum = 0.0;
-      for (int t = threadIdx.x; t < a.tiles; t += kBlock) sum += load_shared(a.tz + (int64_t)r.row * a.tiles + t);
+#pragma unroll 1
+      for (int k = threadIdx.x; k < a.tiles; k += kBlock) sum += load_shared(a.tz + (int64_t)r.row * a.tiles + k);
       f.s = block_scan(s, sum).all;
-      if (wv == 0) list_children(a, r.seq, r.i, s);
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        try_drawn<T>(a, r, s, f);
-        store_info(info, f);
+      if (wv == 0) {
+        try_drawn<T>(a, r, s, kid, f);
+        if (lane == 0) store_info(info, f);
       }
+    } else if (!last_of(counter(a.row_ctr, r.row), a.blocks, s)) {
+      return;
     }
   } else if (blk != 0) {
     return;
   }
-  if (a.last && last_of(a.seq_ctr + r.b, r.seq.rows, s)) finish<T>(a, r, s);
+  if (a.last && last_of(counter(a.seq_ctr, r.b), r.seq.rows, s)) finish<T>(a, r, s);
 }
 
 struct SamplePlan {
-  int tiles, blocks, tiles_per_block;
+  int tiles;
   size_t info_bytes, z_bytes, bytes;
 };
+
+// Workgroups of a row, and the tiles of each: whole rounds of the four waves.
+void sample_cut(int64_t rows, int tiles, int64_t spread, int* blocks, int* tiles_per_block) {
+  const int64_t most = (tiles + kWavesPerBlock - 1) / kWavesPerBlock;
+  int64_t want = spread / (rows > 0 ? rows : 1);
+  want = want < 1 ? 1 : want > most ? most : want;
+  *tiles_per_block = (int)((most + want - 1) / want * kWavesPerBlock);
+  *blocks = (tiles + *tiles_per_block - 1) / *tiles_per_block;
+}
 
 SamplePlan sample_plan(int64_t rows, int64_t vocab) {
   SamplePlan p{};
   p.tiles = (int)((vocab + kRowTile - 1) / kRowTile);
-  const int64_t most = (p.tiles + kWavesPerBlock - 1) / kWavesPerBlock;
-  int64_t want = kSampleSpread / (rows > 0 ? rows : 1);
-  want = want < 1 ? 1 : want > most ? most : want;
-  // Whole rounds of the four waves.
-  p.tiles_per_block = (int)((most + want - 1) / want * kWavesPerBlock);
-  p.blocks = (p.tiles + p.tiles_per_block - 1) / p.tiles_per_block;
   p.info_bytes = ((size_t)rows * kInfo * 8 + 255) & ~(size_t)255;
   p.z_bytes = (size_t)rows * p.tiles * 8;
   p.bytes = kSampleCounterBytes + p.info_bytes + p.z_bytes + (size_t)rows * p.tiles * 4;
@@ -707,16 +789,20 @@ int32_t sample_check(const moe_tree* tree, int64_t vocab, bool arrays) {
 }
 
 template <typename T>
-void launch_sample(SampleArgs& a, unsigned grid, hipStream_t st) {
-  const dim3 g(grid), t(kBlock);
+void launch_sample(SampleArgs& a, hipStream_t st) {
+  const dim3 t(kBlock);
+  sample_cut(a.tree.n_rows, a.tiles, kSampleSpread, &a.blocks, &a.tiles_per_block);
+  const dim3 g((unsigned)a.tree.n_rows * (unsigned)a.blocks);
   if (!a.q) {
     hipLaunchKernelGGL((k_sample_rows<T, false>), g, t, 0, st, a);
     return;
   }
   hipLaunchKernelGGL((k_sample_rows<T, true>), g, t, 0, st, a);
+  sample_cut(a.tree.n_rows, a.tiles, kRoundSpread, &a.blocks, &a.tiles_per_block);
+  const dim3 rounds((unsigned)a.tree.n_rows * (unsigned)a.blocks);
   for (int k = 1; k <= a.tree.max_children; ++k) {
     a.last = k == a.tree.max_children;
-    hipLaunchKernelGGL(k_sample_round<T>, g, t, 0, st, a);
+    hipLaunchKernelGGL(k_sample_round<T>, rounds, t, 0, st, a);
   }
 }
 
@@ -765,8 +851,6 @@ int32_t moe_verify_sample(const moe_tree* tree, const void* logits, int32_t dtyp
   a.stride = row_stride;
   a.V = (int)vocab;
   a.tiles = p.tiles;
-  a.blocks = p.blocks;
-  a.tiles_per_block = p.tiles_per_block;
   a.tokens = tokens;
   a.q = draft_probs;
   a.q_stride = draft_stride;
@@ -784,13 +868,12 @@ int32_t moe_verify_sample(const moe_tree* tree, const void* logits, int32_t dtyp
   a.info = (uint64_t*)((uint8_t*)workspace + kSampleCounterBytes);
   a.tz = (double*)((uint8_t*)a.info + p.info_bytes);
   a.tm = (float*)((uint8_t*)a.tz + p.z_bytes);
-  const unsigned grid = (unsigned)tree->n_rows * (unsigned)p.blocks;
   hipStream_t st = (hipStream_t)hip_stream;
   (void)hipGetLastError();
   switch (dtype) {
-    case MOE_F32: launch_sample<float>(a, grid, st); break;
-    case MOE_BF16: launch_sample<bf16>(a, grid, st); break;
-    default: launch_sample<_Float16>(a, grid, st); break;
+    case MOE_F32: launch_sample<float>(a, st); break;
+    case MOE_BF16: launch_sample<bf16>(a, st); break;
+    default: launch_sample<_Float16>(a, st); break;
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH;
 }

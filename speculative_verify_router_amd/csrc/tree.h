@@ -37,13 +37,15 @@ inline TreeArgs tree_args(const moe_tree* t) {
 struct TreeRows {
   int off, rows, all;
 };
-__device__ __forceinline__ TreeRows tree_rows(const TreeArgs& a, int b) {
+__device__ __forceinline__ TreeRows tree_rows(const TreeArgs& a, int off, int end) {
   TreeRows s;
-  s.off = a.offs[b];
-  const int end = a.offs[b + 1];
+  s.off = off;
   s.all = s.off >= 0 && end > s.off && end <= a.n_rows ? end - s.off : 0;
   s.rows = min(s.all, a.max_rows);
   return s;
+}
+__device__ __forceinline__ TreeRows tree_rows(const TreeArgs& a, int b) {
+  return tree_rows(a, a.offs[b], a.offs[b + 1]);
 }
 
 // The row that row i > 0 of a sequence follows, or -1.

@@ -2,10 +2,11 @@
 (oracle/sample_oracle.py), every call through the C ABI.
 
 Outputs are whole numbers and have to be equal.  They depend on comparisons of 64-bit numbers, which the
-library and the oracle round differently: a weight is off by at most (ln 2 / 2)^12 / 12! = 7e-15 and some
-2^-53 for each of at most 30 operations, a sum by 2^-53 for each term in a row of additions, at most 2^-53
-of 1500 (the oracle's; a tile's and its join's are fewer).  So no comparison whose sides lie 1e-12 apart (of
-a probability of one) can fall differently; the oracle says how far apart the closest were, and every test
+library and the oracle round differently: a weight is off by at most 8e-14 (its polynomial) and some 2^-53
+for each of at most 30 operations, so a probability by twice that, 1.7e-13; a sum by 2^-53 for each of its
+additions in a row, here at most 1500 times 2^-53 = 1.7e-13 (NumPy's pairwise and cumulative sums of rows
+that weigh one; a tile's and its join's are fewer).  So no comparison whose sides lie 1e-12 apart (of a
+probability of one) can fall differently; the oracle says how far apart the closest were, and every test
 asserts that first."""
 
 import numpy as np
@@ -170,6 +171,24 @@ def test_logits_that_are_not_finite(drawn, greedy):
     x[18, 7] = 3.4e38
     x[21, :1024] = -np.inf               # a tile of nothing
     c.logits, c.x = dev(x.astype(np.float32)), x.astype(np.float32).astype(np.float64)
+    check(c)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("drawn", [False, True])
+def test_masks_of_the_lowest_value_and_signalling_nan(dtype, drawn):
+    rng = np.random.default_rng(70)
+    c = Case([4] * 6, 1100, 1, rng, dtype, drawn)
+    low = torch.finfo(TYPES[dtype]).min
+    x = np.where(rng.random(c.x.shape) < 0.5, low, c.x)
+    x[20:22] = low                      # a whole row: one weight for 16-bit types, none for float
+    c.set_logits(x, dtype)
+    bits = {"f32": (torch.int32, 0x7F800001), "bf16": (torch.int16, 0x7F81), "f16": (torch.int16, 0x7C01)}[dtype]
+    c.logits.view(bits[0])[:, 5::7] = bits[1]   # NaN of the kind that an operation would trap on
+    c.x = c.logits.double().cpu().numpy()
+    assert np.isnan(c.x[:, 5::7]).all()
+    check(c)
+    c.temperature[:] = [np.inf, 1e30, 1e-30, 0.0, np.inf, 3e38]
     check(c)
 
 
