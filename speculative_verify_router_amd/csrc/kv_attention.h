@@ -331,6 +331,18 @@ __device__ __forceinline__ void split_terms(float x, bf16 (&t)[NT]) {
   }
 }
 
+// Two at a time: as many conversions as pairs.
+template <int NT>
+__device__ __forceinline__ void split_terms(float x, float y, bf16x2 (&t)[NT]) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    t[n] = __builtin_convertvector((f32x2{x, y}), bf16x2);
+    x -= (float)t[n].x;
+    y -= (float)t[n].y;
+  }
+}
+
 // Where a lane finds its part of a token l of sixteen (a run): 32 channels in
 // 16 bytes of codes for each full 128 channels, 16 in 8 bytes for a last 64,
 // and the aligned dword that holds their scale, with its place there.  Runs
@@ -380,6 +392,25 @@ struct Codes {
         w[4 * p + 1] = v.y;
       }
       e[p] = *reinterpret_cast<const uint32_t*>(scales + at.scale[p]);
+    }
+  }
+  // The same with the run's offsets in its page as scalars of a buffer load.
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t page, uint32_t codes, uint32_t scales,
+                                       const LanePart<D>& at) {
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      if (LanePart<D>::full(p)) {
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(page, at.code + 64 * p, codes, 0);
+        w[4 * p] = v.x;
+        w[4 * p + 1] = v.y;
+        w[4 * p + 2] = v.z;
+        w[4 * p + 3] = v.w;
+      } else {
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(page, at.half + 64 * p, codes, 0);
+        w[4 * p] = v.x;
+        w[4 * p + 1] = v.y;
+      }
+      e[p] = __builtin_amdgcn_raw_buffer_load_b32(page, at.scale[p], scales, 0);
     }
   }
   // The scale of word k, in the exponent of a float.
@@ -434,6 +465,12 @@ constexpr int attn_weight_terms(int NT) { return NT < 2 ? 2 : NT; }
 template <int D, int RT, int NT, int W, typename T, bool kTree>
 __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attention(AttnArgs a) {
   constexpr int KS = D / 32, CB = D / 16, NP = attn_weight_terms(NT);
+  // The two waves of a SIMD: one that is at its products goes first, so that
+  // the other's softmax fills what they leave (61 rows over 60000 tokens, bf16,
+  // 311 us without, 298 with the sums' products first, 288 with the scores'
+  // too).  Of two terms a query value the scores' are too many for that, of
+  // three the sums' too.
+  constexpr bool kScoresFirst = RT == 2 && NT == 1, kSumsFirst = RT == 2 && NT < 3;
   constexpr int kRowBytes = 2 * D + 16;            // a staged token: the pad spreads the banks
   constexpr int kStage = kAttnTile * kRowBytes;    // a wave's staged tokens
   constexpr int kJoinRow = D + 4;                  // floats of a joined row
@@ -545,11 +582,30 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
   };
   auto page_of = [&](int t, int u) { return table[run(t, u) >> a.kv.page_shift]; };
   const LanePart<D> part(l16, g);
-  auto load_keys_or_values = [&](int t, int u, int page, int side, Codes<D>& x) {
+  // Where a run lies: its page, and the offsets of its first token there.
+  const uint32_t page_bytes = (uint32_t)a.kv.page_bytes, page_step = page_bytes * (uint32_t)a.kv.Hk;  // below 2^29
+  const uint8_t* head = a.cache + (int64_t)kvh * page_bytes;
+  struct RunAt {
+    const uint8_t* page;
+    uint32_t code, scale;
+  };
+  auto run_at = [&](int t, int u, int page) {
     page = (unsigned)page < (unsigned)a.kv.n_pages ? page : 0;
-    const uint8_t* c = a.cache + ((int64_t)page * a.kv.Hk + kvh) * a.kv.page_bytes;
-    const int i = run(t, u) & (P - 1);
-    x.load(c + (side * P + i) * (D / 2), c + P * D + (side * P + i) * (D / 32), part);
+    const uint32_t i = run(t, u) & (P - 1);
+    return RunAt{head + (uint64_t)(uint32_t)page * page_step, i * (D / 2),
+                 P * D + i * (D / 32)};
+  };
+  auto load_at = [&](const RunAt& r, uint32_t code, uint32_t scale, Codes<D>& x) {
+    // Two row tiles: bound by instructions, of which a buffer load takes fewer.
+    // One: by latency, of which it has more (29 sequences of up to four rows,
+    // fp16, 27 us instead of 25; two row tiles 263 and 256 us for 61 rows over
+    // 60000 tokens).
+    if constexpr (RT == 2) x.load(make_rsrc(r.page, page_bytes), code, scale, part);
+    else x.load(r.page + code, r.page + scale, part);
+  };
+  auto load_keys = [&](const RunAt& r, Codes<D>& x) { load_at(r, r.code, r.scale, x); };
+  auto load_values = [&](const RunAt& r, Codes<D>& x) {
+    load_at(r, r.code + P * (D / 2), r.scale + P * (D / 32), x);
   };
 
   // One tile of codes is kept in flight: keys of the next tile are asked for
@@ -564,10 +620,11 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
       page[u] = page_of(t, u);
       next_page[u] = page_of(t + W, u);
     }
+    const RunAt at[2] = {run_at(t, 0, page[0]), run_at(t, 1, page[1])};
 #pragma unroll
-    for (int u = 0; u < 2; ++u) load_keys_or_values(t, u, page[u], 0, kc[u]);
+    for (int u = 0; u < 2; ++u) load_keys(at[u], kc[u]);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) load_keys_or_values(t, u, page[u], 1, vc[u]);
+    for (int u = 0; u < 2; ++u) load_values(at[u], vc[u]);
   }
 
   // The rows' queries, and the tokens that each sees: [lo, hi].
@@ -642,6 +699,7 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) see[rt] = among ? marks[rt].bits(tok0 - sq.place0) : ~0u;
     }
+    if constexpr (kScoresFirst) __builtin_amdgcn_s_setprio(1);
     f32x4v s[RT][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -657,8 +715,10 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
             s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[rt][k][n], s[rt][u], 0, 0, 0);
       }
     }
+    if constexpr (kScoresFirst) __builtin_amdgcn_s_setprio(0);
+    const RunAt next[2] = {run_at(t + W, 0, next_page[0]), run_at(t + W, 1, next_page[1])};
 #pragma unroll
-    for (int u = 0; u < 2; ++u) load_keys_or_values(t + W, u, next_page[u], 0, kc[u]);
+    for (int u = 0; u < 2; ++u) load_keys(next[u], kc[u]);
 
     // Values to shared memory, widened; the next ones are asked for.
 #pragma unroll
@@ -669,7 +729,7 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
             widen(vc[u].w[k], vc[u].scale(k, part));
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      load_keys_or_values(t + W, u, next_page[u], 1, vc[u]);
+      load_values(next[u], vc[u]);
       page[u] = next_page[u];
       next_page[u] = page_of(t + 2 * W, u);
     }
@@ -719,17 +779,25 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
     for (int rt = 0; rt < RT; ++rt) {
       const float m0 = mx[rt] == -INFINITY ? 0.f : mx[rt];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        bf16 x[NP];
-        const float p = __builtin_amdgcn_exp2f(fmaf(s[rt][i / 4][i % 4], a.c, -m0));
-        sum[rt] += p;
-        split_terms<NP>(p, x);
+      for (int i = 0; i < 8; i += 2) {
+        bf16x2 x[NP];
+        float p[2];
 #pragma unroll
-        for (int n = 0; n < NP; ++n) pf[rt][n][i] = x[n];
+        for (int j = 0; j < 2; ++j) {
+          p[j] = __builtin_amdgcn_exp2f(fmaf(s[rt][i / 4][i % 4 + j], a.c, -m0));
+          sum[rt] += p[j];
+        }
+        split_terms<NP>(p[0], p[1], x);
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+          pf[rt][n][i] = x[n].x;
+          pf[rt][n][i + 1] = x[n].y;
+        }
       }
     }
 
     // O^T += V^T P^T.
+    if constexpr (kSumsFirst) __builtin_amdgcn_s_setprio(1);
     const uint8_t* from = stage + (4 * g + l16 / 4) * kRowBytes + 8 * (l16 % 4);
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
@@ -742,6 +810,7 @@ __global__ __launch_bounds__(W* kWave, attn_waves(D, RT, NT)) void k_kv_attentio
         for (int rt = 0; rt < RT; ++rt)
           o[rt][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][n], o[rt][cb], 0, 0, 0);
     }
+    if constexpr (kSumsFirst) __builtin_amdgcn_s_setprio(0);
   }
 
   // Where row r of the row tile has a part, and its output.
