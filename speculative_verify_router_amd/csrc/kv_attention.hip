@@ -115,6 +115,7 @@ struct AttnPlan {
   int row_tiles, tiles, waves, splits, min_tiles, share, group, by_seq, search, first, extra;
   bool join_here;
   int64_t part_rows;
+  int64_t cost;  // of one tree's parts
   int64_t grid;
   size_t o_bytes, bytes;
 };
@@ -126,6 +127,32 @@ int64_t attn_seen_tiles(const moe_kv_desc* d, const moe_kv_batch* b) {
   return seen / kAttnTile + 2;
 }
 
+// Splits of one tree's row tiles, which see the same tokens, so that parts are
+// alike, and what they cost, in tiles: those of a part, and what it costs to
+// begin and to join.  Row tiles of a head and a split are one group, groups go
+// round the XCDs (see the kernel).  An XCD with one group more than it has room
+// for takes a second round, whose row tiles no longer read the same tokens at the
+// same time: 24 rows over 40000 tokens, 4 heads, eight waves 101 us with four
+// splits, 146 with five to ten.
+struct TreeSplits {
+  int splits;
+  int64_t cost;
+};
+TreeSplits tree_splits(int64_t row_tiles, int heads, int resident, int64_t tiles, int min_tiles, int64_t most_parts) {
+  const int64_t group = row_tiles < 64 ? row_tiles : 64, room = 256 / 8 * resident;  // workgroups of an XCD at once
+  TreeSplits best{1, 0};
+  for (int s = 1; s <= kMaxSplits && (s - 1) * min_tiles < tiles && row_tiles * s <= most_parts; ++s) {
+    const int64_t groups = (row_tiles * s + group - 1) / group * heads;
+    const int64_t rounds = ((groups + 7) / 8 * group + room - 1) / room;
+    int64_t cost = (tiles + s - 1) / s;
+    cost = cost > min_tiles ? cost : min_tiles;
+    if (rounds > 1) cost = rounds * (cost * 8 / 5 + 12);
+    cost += 12 + (s > 1 ? 8 : 0) + (s > kJoinHere ? 8 : 0);
+    if (s == 1 || cost < best.cost) best = TreeSplits{s, cost};
+  }
+  return best;
+}
+
 // The plan for workgroups of p.waves: the splits of `all` row tiles of a head.
 // Returns whether row tiles are few, and tables long, enough for four splits
 // or more and as many as there is room for.
@@ -133,6 +160,10 @@ bool attn_split(AttnPlan& p, const moe_kv_desc* d, const moe_kv_batch* b, int32_
   // A part is a tile a wave at least, and as many more for every 64 sequences
   // behind the first, which a workgroup passes over to find it.
   p.min_tiles = p.waves * (1 + (b->n_seqs - 1) / kWave);
+  // Trees of few rows: two, since joining takes as long as a step (13 rows over
+  // 777 tokens 11.2 us, 12.4 with one, 13.6 with three; fp32, a window of 512
+  // 18.8 and 23.6).
+  if (tree && p.row_tiles == 1) p.min_tiles *= 2;
   // Work of a head that runs at once.
   const int resident = attn_waves(d->head_dim, p.row_tiles, attn_terms(dtype)) * kAttnWaves / p.waves;
   const int slots = 256 * resident / d->n_kv_heads;
@@ -142,12 +173,14 @@ bool attn_split(AttnPlan& p, const moe_kv_desc* d, const moe_kv_batch* b, int32_
   int64_t share = slots - all / 2;
   if (2 * all > slots && share > all) share = all;
   p.share = (int)(share > slots / 2 ? share : slots / 2);
-  // Rows of one tree see the same tokens, so all parts can be alike: 61 rows over
-  // 60000 tokens 256 us, 275 with a last part of two thirds.
-  if (tree && b->n_seqs == 1) p.share = slots;
+  if (tree && b->n_seqs == 1) p.share = slots;  // parts alike (61 rows over 60000 tokens 256 us, 275 without)
   p.share = p.share > 0 ? p.share : 1;
   const int64_t tiles = attn_seen_tiles(d, b), most = (tiles + p.min_tiles - 1) / p.min_tiles;
-  if (b->n_seqs == 1) {
+  if (tree && b->n_seqs == 1) {
+    const TreeSplits t = tree_splits(all, d->n_kv_heads, resident, tiles, p.min_tiles, 4 * (int64_t)slots);
+    p.splits = t.splits;
+    p.cost = t.cost;
+  } else if (b->n_seqs == 1) {
     const int64_t s = 2 * all > slots ? 1 : slots / all;
     p.splits = (int)(s < kMaxSplits ? s : kMaxSplits);
   } else {
@@ -169,6 +202,12 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype, b
   const int G = d->n_heads / d->n_kv_heads;
   const int64_t rows = (int64_t)(b->max_rows < b->n_tokens ? b->max_rows : b->n_tokens) * G;
   p.row_tiles = attn_row_tiles(rows, d->head_dim, dtype);
+  // Trees of which a wave has two or three steps of 16 rows in all, as far as the
+  // table says: their time is one step after another, which is shorter for one
+  // row tile (7 rows over 777 tokens 10.5 us, 15.2 with two; 13 over 10000 28 and
+  // 42; but 7 over 40000 49 and 45, 32 over 10000 42 and 36).
+  if (tree && (int64_t)b->n_seqs * ((rows + 15) / 16) * d->n_kv_heads * attn_seen_tiles(d, b) <= 8192)
+    p.row_tiles = 1;
   const int span = 16 * p.row_tiles;
   p.tiles = (int)((rows + span - 1) / span);
   int64_t all = (int64_t)b->n_seqs * p.tiles;
@@ -180,10 +219,12 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype, b
   // 16384, of which there are two, takes 114 us (101), 4 rows over 4000 tokens
   // 26.0 (15.3).
   p.waves = kAttnPartWaves;
-  if (p.row_tiles != 2 || !attn_split(p, d, b, dtype, all, tree)) {
-    p.waves = kAttnWaves;
-    attn_split(p, d, b, dtype, all, tree);
-  }
+  const bool large = p.row_tiles == 2 && attn_split(p, d, b, dtype, all, tree);
+  const AttnPlan parts = p;
+  p.waves = kAttnWaves;
+  if (!large || (tree && b->n_seqs == 1)) attn_split(p, d, b, dtype, all, tree);
+  // (One tree: those that cost less, of which the larger take a tile in half the time.)
+  if (large && (!tree || b->n_seqs > 1 || parts.cost <= 2 * p.cost)) p = parts;
   p.group = p.tiles < 64 ? p.tiles : 64;
   p.first = (int)all;
   p.extra = p.splits == 1 ? 0 : b->n_seqs == 1 ? (int)all * (p.splits - 1) : p.share;
@@ -203,9 +244,10 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype, b
 }
 
 // What the plan of any batch of up to these sizes needs.  Row tiles times
-// splits are at most what runs at once for one sequence, 4 1/4 of that for
-// several (at most a quarter of it row tiles, each with a part too many); where
-// the last workgroup joins, twice p.share, which is at most what runs at once.
+// splits are at most what runs at once for one sequence, four times that for one
+// tree, 4 1/4 for several (at most a quarter of it row tiles, each with a part
+// too many); where the last workgroup joins, twice p.share, which is at most what
+// runs at once.
 size_t attn_most_bytes(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   if (b->n_seqs == 0 || b->n_tokens == 0 || b->max_rows == 0) return 0;
   if (attn_seen_tiles(d, b) <= kAttnWaves) return 0;  // never cut
@@ -214,7 +256,7 @@ size_t attn_most_bytes(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtyp
   size_t most = 0;
   for (int rt = 1; rt <= attn_row_tiles(rows, d->head_dim, dtype); ++rt) {
     const int slots = 256 * attn_waves(d->head_dim, rt, attn_terms(dtype)) / d->n_kv_heads;
-    const int parts = b->n_seqs == 1 ? slots : slots < 1 ? 2 : 4 * slots + slots / 4;
+    const int parts = slots < 1 ? 2 : 4 * slots + slots / 4;
     const size_t n = (size_t)parts * d->n_kv_heads * 16 * rt;
     const size_t bytes = kAttnCounters * sizeof(unsigned) + ((n * d->head_dim * 4 + 255) & ~(size_t)255) + n * 8;
     most = bytes > most ? bytes : most;
