@@ -50,7 +50,7 @@ extern "C" {
 #define MOE_SAMPLE_MAX_VOCAB 1073741824 /* 2^30 columns */
 
 /* Device workspace, in *bytes, of moe_verify_sample for trees of up to these
- * n_seqs and n_rows (the arrays may be NULL) and vocab columns.  It begins
+ * n_seqs and n_rows (the arrays may be NULL) and up to vocab columns.  It begins
  * with 131072 bytes of counters, which must be zero before the first call that
  * uses the workspace; every call leaves them zero, so zero-fill a workspace
  * once when it is allocated.  Calls that share one must not overlap in time.

@@ -94,15 +94,15 @@ int32_t moe_kv_tree_attention(const moe_kv_desc* desc, const moe_kv_batch* batch
  *              where it is larger, as 0 where it is negative.
  *   caches     n_caches (1 to MOE_TREE_MAX_CACHES) device pointers, in HOST
  *              memory, read before the call returns: caches of one layout, with
- *              n_pages pages each.  No two may be the same.
+ *              n_pages pages each.  No two may be the same or overlap.
  *   kept_lens  [n_seqs] int32 out, may be NULL, not seq_lens itself:
  *              base + n_accepted[b] + 1, seq_lens[b] for a sequence without rows.
  * The trees' rows are those of the batch below max_rows.
  * MOE_ERR_NULL: a NULL struct, batch array, path, n_accepted, caches or cache.
  * MOE_ERR_SHAPE: desc, batch, n_pages, path_stride or n_caches out of range, or
  * n_seqs * n_kv_heads * n_caches 2^24 or more.  MOE_ERR_ARG: a pointer not
- * aligned to its elements, a cache not 16-byte aligned, kept_lens equal to
- * seq_lens.  n_seqs == 0: MOE_OK. */
+ * aligned to its elements, a cache not 16-byte aligned or there twice, kept_lens
+ * equal to seq_lens.  n_seqs == 0: MOE_OK. */
 int32_t moe_kv_commit(const moe_kv_desc* desc, const moe_kv_batch* batch, const int32_t* path,
                       int64_t path_stride, const int32_t* n_accepted, void* const* caches,
                       int32_t n_caches, int32_t n_pages, int32_t* kept_lens, void* hip_stream);

@@ -109,7 +109,7 @@ def check_tree(lay, plan, cache, dtype, rng, scale=None, q=None, ws=None):
     # The score's roundings, the weights' sum (a rounding for each token), the logarithm and its sum.
     u, r = 2.0 ** -24, rl[on]
     t = (lay.dim + 4) * u * reach[on] + (64 + seen[on, None]) * u + 8 * u * np.abs(np.where(empty, 0, r))
-    assert np.all(np.abs(g[on] - r)[~empty] <= t[~empty])
+    assert np.all(np.abs(g[on][~empty] - r[~empty]) <= t[~empty])
     return got, ref
 
 

@@ -250,8 +250,8 @@ def commit_status(**kw):
 def test_commit_refusals():
     for kw, status in [
         (dict(path=None), B.ERR_NULL), (dict(n=None), B.ERR_NULL), (dict(caches=None, n_caches=1), B.ERR_NULL),
-        (dict(caches=(A, None)), B.ERR_NULL), (dict(caches=(A, A + 8)), B.ERR_ARG), (dict(caches=()), B.ERR_SHAPE),
-        (dict(caches=[A] * 257), B.ERR_SHAPE), (dict(stride=0), B.ERR_SHAPE), (dict(pages=0), B.ERR_SHAPE),
+        (dict(caches=(A, None)), B.ERR_NULL), (dict(caches=(A, A + 8)), B.ERR_ARG), (dict(caches=(A, A + 64, A)), B.ERR_ARG), (dict(caches=()), B.ERR_SHAPE),
+        (dict(caches=[A + 64 * i for i in range(257)]), B.ERR_SHAPE), (dict(stride=0), B.ERR_SHAPE), (dict(pages=0), B.ERR_SHAPE),
         (dict(path=A + 2), B.ERR_ARG), (dict(n=A + 1), B.ERR_ARG), (dict(kept=A + 2), B.ERR_ARG), (dict(kept=A), B.ERR_ARG),
         (dict(batch=None), B.ERR_NULL), (dict(batch=kv_batch(page_table=None)), B.ERR_NULL),
         (dict(batch=kv_batch(pages_per_seq=0)), B.ERR_SHAPE), (dict(desc=kv_desc(page_size=17)), B.ERR_SHAPE),
