@@ -88,21 +88,21 @@ int32_t moe_kv_tree_attention(const moe_kv_desc* desc, const moe_kv_batch* batch
  * it lies.  path[b][0] is the root, 0; a path ascends, so path[b][i] >= i; an
  * entry below i or not among the sequence's rows is not moved, nor is a token
  * from or to a place that has no page.  What lies behind base + n_accepted[b] is
- * as good as free.
+ * as good as free.  Pages that tokens move from or to belong to one sequence.
  *   path       [n_seqs][path_stride], path_stride >= 1 entries a sequence.
  *   n_accepted [n_seqs]; taken as path_stride - 1 or the sequence's rows - 1
  *              where it is larger, as 0 where it is negative.
  *   caches     n_caches (1 to MOE_TREE_MAX_CACHES) device pointers, in HOST
  *              memory, read before the call returns: caches of one layout, with
  *              n_pages pages each.  No two may be the same or overlap.
- *   kept_lens  [n_seqs] int32 out, may be NULL, not seq_lens itself:
+ *   kept_lens  [n_seqs] int32 out, may be NULL, neither seq_lens nor n_accepted:
  *              base + n_accepted[b] + 1, seq_lens[b] for a sequence without rows.
  * The trees' rows are those of the batch below max_rows.
  * MOE_ERR_NULL: a NULL struct, batch array, path, n_accepted, caches or cache.
  * MOE_ERR_SHAPE: desc, batch, n_pages, path_stride or n_caches out of range, or
  * n_seqs * n_kv_heads * n_caches 2^24 or more.  MOE_ERR_ARG: a pointer not
- * aligned to its elements, a cache not 16-byte aligned or there twice, kept_lens
- * equal to seq_lens.  n_seqs == 0: MOE_OK. */
+ * aligned to its elements, a cache not 16-byte aligned, caches that overlap, kept_lens
+ * equal to seq_lens or n_accepted.  n_seqs == 0: MOE_OK. */
 int32_t moe_kv_commit(const moe_kv_desc* desc, const moe_kv_batch* batch, const int32_t* path,
                       int64_t path_stride, const int32_t* n_accepted, void* const* caches,
                       int32_t n_caches, int32_t n_pages, int32_t* kept_lens, void* hip_stream);

@@ -795,8 +795,9 @@ def moe_kv_commit(desc: KvDesc, batch: KvBatch, path: torch.Tensor, n_accepted: 
         raise ValueError("moe_kv_commit: a cache twice")
     if any(c.shape != caches[0].shape for c in caches):
         raise ValueError("moe_kv_commit: expected caches of one shape")
-    if kept_lens is not None and b.n_seqs and kept_lens.data_ptr() == batch.seq_lens.data_ptr():
-        raise ValueError("moe_kv_commit: kept_lens is seq_lens, which other workgroups still read")
+    if kept_lens is not None and b.n_seqs and kept_lens.data_ptr() in (batch.seq_lens.data_ptr(),
+                                                                       n_accepted.data_ptr()):
+        raise ValueError("moe_kv_commit: kept_lens is seq_lens or n_accepted, which other workgroups still read")
     st = _call_on(dev, stream, lib().moe_kv_commit, desc.c(), b,
                   _on(dev, path, i32, (b.n_seqs, path.shape[1]), "path"), path.shape[1],
                   _on(dev, n_accepted, i32, (b.n_seqs,), "n_accepted"),

@@ -162,15 +162,19 @@ int32_t moe_kv_commit(const moe_kv_desc* desc, const moe_kv_batch* batch, const 
   if (batch->n_seqs == 0) return MOE_OK;
   if (!path || !n_accepted || !caches) return MOE_ERR_NULL;
   CommitArgs a{};
+  const uint64_t bytes = (uint64_t)n_pages * desc->n_kv_heads * (uint64_t)kv_page_bytes(desc);
   for (int32_t c = 0; c < n_caches; ++c) {
     if (!caches[c]) return MOE_ERR_NULL;
     if ((uintptr_t)caches[c] % 16) return MOE_ERR_ARG;
-    for (int32_t e = 0; e < c; ++e)
-      if (caches[e] == caches[c]) return MOE_ERR_ARG;  // its tokens would move twice, or from half written ones
+    for (int32_t e = 0; e < c; ++e) {  // tokens of both would move twice, or from half written ones
+      const uint64_t p = (uint64_t)(uintptr_t)caches[e], q = (uint64_t)(uintptr_t)caches[c];
+      if ((p < q ? q - p : p - q) < bytes) return MOE_ERR_ARG;
+    }
     a.cache[c] = (uint8_t*)caches[c];
   }
   if (((uintptr_t)path | (uintptr_t)n_accepted | (uintptr_t)kept_lens) % 4) return MOE_ERR_ARG;
-  if (kept_lens == batch->seq_lens) return MOE_ERR_ARG;  // which other workgroups still read
+  // What other workgroups still read.
+  if (kept_lens && (kept_lens == batch->seq_lens || kept_lens == n_accepted)) return MOE_ERR_ARG;
   a.kv = kv_args(desc, batch, n_pages);
   a.path = path;
   a.path_stride = path_stride;

@@ -357,6 +357,25 @@ def test_commit_of_many_sequences_and_layers():
                  layers=6, wide=11)
 
 
+def test_commit_of_layers_side_by_side():
+    """All layers' caches in one tensor, in any order, with no room between; overlapping ones are refused."""
+    rng = np.random.default_rng(35)
+    lay = ko.Layout(2, 2, 64, 16)
+    plan = Plan(lay, [9], [40], rng)
+    batch = plan.batch()
+    path, n = dev(np.array([[0, 3, 8]], np.int32)), dev(np.array([2], np.int32))
+    start = dev(rng.integers(0, 256, (3, plan.n_pages, 2, lay.page_bytes)).astype(np.uint8))
+    one, all_ = start.clone(), start.clone()
+    for c in one:
+        svr.moe_kv_commit(desc_of(lay), batch, path, n, [c])
+    svr.moe_kv_commit(desc_of(lay), batch, path, n, [all_[2], all_[0], all_[1]])
+    torch.cuda.synchronize()
+    assert torch.equal(one, all_) and not torch.equal(one, start)
+    pages = all_.view(-1, 2, lay.page_bytes)
+    with pytest.raises(svr.MoeError):
+        svr.moe_kv_commit(desc_of(lay), batch, path, n, [pages[:plan.n_pages], pages[1:plan.n_pages + 1]])
+
+
 def test_plan_and_commit_on_another_stream_and_in_a_graph():
     rng = np.random.default_rng(34)
     lay = ko.Layout(2, 1, 64, 16)

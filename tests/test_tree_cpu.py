@@ -253,6 +253,8 @@ def test_commit_refusals():
         (dict(caches=(A, None)), B.ERR_NULL), (dict(caches=(A, A + 8)), B.ERR_ARG), (dict(caches=(A, A + 64, A)), B.ERR_ARG), (dict(caches=()), B.ERR_SHAPE),
         (dict(caches=[A + 64 * i for i in range(257)]), B.ERR_SHAPE), (dict(stride=0), B.ERR_SHAPE), (dict(pages=0), B.ERR_SHAPE),
         (dict(path=A + 2), B.ERR_ARG), (dict(n=A + 1), B.ERR_ARG), (dict(kept=A + 2), B.ERR_ARG), (dict(kept=A), B.ERR_ARG),
+        (dict(n=A + 64), B.ERR_ARG),  # kept_lens
+        (dict(caches=(A + 1024, A, A + 9 * 2 * kv_desc().page_bytes - 16)), B.ERR_ARG),  # pages of the first two
         (dict(batch=None), B.ERR_NULL), (dict(batch=kv_batch(page_table=None)), B.ERR_NULL),
         (dict(batch=kv_batch(pages_per_seq=0)), B.ERR_SHAPE), (dict(desc=kv_desc(page_size=17)), B.ERR_SHAPE),
         (dict(desc=kv_desc(n_heads=1024, n_kv_heads=1024), batch=kv_batch(n_seqs=16384)), B.ERR_SHAPE),
@@ -371,6 +373,8 @@ def test_the_binding_refuses_what_it_cannot_pass_on():
         svr.moe_kv_commit(d, batch, torch.zeros((2, 3), **i32), z[:1], [cache])
     with pytest.raises(ValueError, match="kept_lens is seq_lens"):
         svr.moe_kv_commit(d, batch, path, z[:1], [cache], batch.seq_lens)
+    with pytest.raises(ValueError, match="or n_accepted"):
+        svr.moe_kv_commit(d, batch, path, z[1:2], [cache], z[1:2])
     with pytest.raises(ValueError, match="device tensor"):
         svr.moe_kv_commit(d, batch, path, z[:1], [cache])
 
