@@ -410,3 +410,56 @@ def test_tokens_are_distributed_as_the_targets(kids, drawn):
     # Five standard deviations of each count.
     assert got.sum() == n and np.all(np.abs(got - n * p) <= 5 * np.sqrt(n * p * (1 - p)))
     assert 0 < int((count > 0).sum()) < n
+
+
+@pytest.mark.parametrize("drawn", [False, True])
+def test_rows_that_lie_beyond_32_bits(drawn):
+    """Rows of logits and of probabilities so far apart that the last ones are more than 2^31 elements, and
+    2^32 bytes, from the first."""
+    c = Case([3], 1500, 1, np.random.default_rng(72), "bf16", drawn)
+    want = c.want()
+
+    def apart(t, stride):
+        rows = torch.empty(2 * stride + 1500, dtype=t.dtype, device="cuda").as_strided((3, 1500), (stride, 1))
+        rows.copy_(t)
+        return rows
+
+    c.logits = apart(c.logits, 2 ** 30 + 3)
+    check(c, want, **(dict(draft_probs=apart(dev(c.q), 2 ** 30 + 1)) if drawn else {}))
+
+
+def test_padded_batches_and_their_graph():
+    """Rows behind the last sequence; a captured call replayed for other numbers of rows and sequences without any."""
+    cases = [Case(rows, 2000, 2, np.random.default_rng(74 + i), "f32", drawn, pad=20 - sum(rows), max_rows=9,
+                  chain=False)
+             for i, rows in enumerate(([4, 9, 2], [1, 0, 0], [0, 8, 9], [5, 5, 5])) for drawn in (False, True)]
+    for drawn in (False, True):
+        first = next(c for c in cases if (c.q is not None) == drawn)
+        args, named = first.device()
+        args = (args[0], args[1].clone(), *args[2:])  # (the logits are the case's own)
+        tree, q = args[0], named["draft_probs"]
+        out = first.outputs()
+        ws = svr.sample_workspace(tree, 20, 2000)
+        call = lambda: svr.moe_verify_sample(*args, *out, **named, ws=ws)  # noqa: E731
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        for c in [c for c in cases if (c.q is not None) == drawn] * 2:
+            got = check(c, ws=ws)
+            new, more = c.device()
+            tree.q_offsets.copy_(new[0].q_offsets)
+            tree.parents.copy_(new[0].parents)
+            for a, b in zip(args[1:], new[1:]):
+                a.copy_(b)
+            named["temperature"].copy_(more["temperature"])
+            if drawn:
+                q.copy_(more["draft_probs"])
+            for t in out:
+                t.fill_(-7)
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert [t.tolist() for t in out] == [got["accepted"], got["n_accepted"], got["path"]]
+            assert not ws[:131072].any()

@@ -422,3 +422,71 @@ def test_plan_and_commit_on_another_stream_and_in_a_graph():
     assert torch.equal(second[2], first[2] + 1)
     g.replay()
     assert all(torch.equal(a, b) for a, b in zip(second, outputs()))
+
+
+def test_trees_in_a_cache_beyond_four_gibibytes():
+    """The last pages of a cache of 4.5 GB, one and two row tiles a wave: attention and commit."""
+    rng = np.random.default_rng(36)
+    lay = ko.Layout(8, 8, 128, 1024)
+    n = 4000
+    assert (n - 2) * 8 * lay.page_bytes > 2 ** 32
+    big = svr.kv_cache(desc_of(lay), n)
+    for rows, width in ((5, 2), (40, 16)):
+        plan = TreePlan(lay, [rows], [1500], rng, width=width, spare=0)
+        small = plan.filled_cache(rng)
+        table = np.full((1, width), -1, np.int32)
+        for j in range(2):
+            table[0, j] = n - 1 - j
+            big[n - 1 - j] = dev(small[plan.table[0, j]])
+        batch = svr.KvBatch(dev(plan.offsets), dev(plan.lens), dev(table), rows)
+        q = rounded(rng.standard_normal((rows, 8, 128)), "bf16")
+        out, _ = check_tree(lay, plan, small, "bf16", rng, q=q)
+        got = torch.empty_like(q[0])
+        svr.moe_kv_tree_attention(desc_of(lay), batch, as_words(plan.mask), q[0], big, got)
+        path, kept = np.array([[0, 2, 4]], np.int32), torch.empty(1, dtype=torch.int32, device="cuda")
+        svr.moe_kv_commit(desc_of(lay), batch, dev(path), dev(np.array([2], np.int32)), [big], kept)
+        to.commit(lay, small, plan.offsets, plan.lens, plan.table, rows, path, [2])
+        assert np.array_equal(got.double().cpu().numpy(), out)
+        for j in range(2):
+            assert np.array_equal(big[n - 1 - j].cpu().numpy(), small[plan.table[0, j]])
+        assert int(kept[0]) == 1500 - rows + 3
+
+
+def test_tree_attention_of_rows_apart_on_two_streams_and_in_a_graph():
+    """Views of a fused projection; calls at once on workspaces of their own; replays follow masks and lengths."""
+    rng = np.random.default_rng(37)
+    lay = ko.Layout(16, 2, 128, 16)
+    plan = TreePlan(lay, [21, 4], [900, 260], rng)
+    T, d, batch = plan.T, desc_of(lay), plan.batch()
+    cache = plan.filled_cache(rng)
+    t, q64 = rounded(rng.standard_normal((T, 16, 128)), "bf16")
+    fused = torch.full((T, 20, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    fused[:, 3:19] = t
+    q = fused[:, 3:19]
+    want, _ = check_tree(lay, plan, cache, "bf16", rng, q=(q, q64))
+    gpu, mask, lens = dev(cache), as_words(plan.mask), batch.seq_lens
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    ws = [svr.kv_workspace(d, batch, T) for _ in streams]
+    outs = [torch.empty((T, 16, 128), dtype=torch.bfloat16, device="cuda") for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for o, w, st in zip(outs, ws, streams):
+            svr.moe_kv_tree_attention(d, batch, mask, q, gpu, o, ws=w, stream=st)
+    torch.cuda.synchronize()
+    assert all(np.array_equal(o.double().cpu().numpy(), want) for o in outs)
+
+    g, out = torch.cuda.CUDAGraph(), outs[0]
+    with torch.cuda.graph(g, stream=streams[0]):
+        svr.moe_kv_tree_attention(d, batch, mask, q, gpu, out, ws=ws[0])
+    own = to.plan(plan.offsets, None, plan.lens, plan.max_rows, plan.mask.shape[1])[0]  # chains
+    for new_mask, new_lens in ((plan.mask, plan.lens), (own, plan.lens), (own, plan.lens - [17, 250]),
+                               (plan.mask, plan.lens)):
+        mask.copy_(as_words(new_mask))
+        lens.copy_(dev(np.asarray(new_lens, np.int32)))
+        svr.moe_kv_tree_attention(d, batch, mask, q, gpu, outs[1], ws=ws[1])
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, outs[1]) and not out.isnan().any()
+    assert np.array_equal(out.double().cpu().numpy(), want)
