@@ -174,6 +174,16 @@ bool attn_split(AttnPlan& p, const moe_kv_desc* d, const moe_kv_batch* b, int32_
   if (2 * all > slots && share > all) share = all;
   p.share = (int)(share > slots / 2 ? share : slots / 2);
   if (tree && b->n_seqs == 1) p.share = slots;  // parts alike (61 rows over 60000 tokens 256 us, 275 without)
+  // Trees have work for longer parts than single rows do, and more of them on the
+  // average than run at once: parts of the mean however many row tiles there are
+  // (up to twice what runs at once, by the workspace), eight steps a wave at
+  // least (29 trees of up to 26 rows over 5000 tokens, fp16, 75 us, 82 without; 40
+  // of up to 7 over 20000 198 and 241; with one step at least 60 of up to 10 over
+  // 3000 54 us, 48 with eight).  Even trees are not cut, as before.
+  if (tree && b->n_seqs > 1 && 2 * all > slots) {
+    p.share = (int)(all < 2 * slots ? all : 2 * slots);
+    p.min_tiles = p.min_tiles > 8 * p.waves ? p.min_tiles : 8 * p.waves;
+  }
   p.share = p.share > 0 ? p.share : 1;
   const int64_t tiles = attn_seen_tiles(d, b), most = (tiles + p.min_tiles - 1) / p.min_tiles;
   if (tree && b->n_seqs == 1) {
@@ -247,7 +257,7 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype, b
 // splits are at most what runs at once for one sequence, four times that for one
 // tree, 4 1/4 for several (at most a quarter of it row tiles, each with a part
 // too many); where the last workgroup joins, twice p.share, which is at most what
-// runs at once.
+// runs at once, of trees twice that.
 size_t attn_most_bytes(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   if (b->n_seqs == 0 || b->n_tokens == 0 || b->max_rows == 0) return 0;
   if (attn_seen_tiles(d, b) <= kAttnWaves) return 0;  // never cut

@@ -221,6 +221,25 @@ def test_tree_attention_over_uneven_sequences(seqs, heads, kv_heads, window):
     check_tree(lay, plan, plan.filled_cache(rng), "bf16", rng)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("seqs,heads,kv_heads,longest,window", [
+    (30, 16, 4, 4000, 0), (30, 16, 4, 4000, 3500), (70, 8, 4, 4000, 0), (6, 16, 16, 4000, 0),
+])
+def test_trees_of_which_more_than_run_at_once(dtype, seqs, heads, kv_heads, longest, window):
+    """Parts of the mean of uneven sequences, and even ones that are not cut."""
+    log(f"more than at once {dtype} {seqs} {heads}/{kv_heads} W={window}")
+    rng = np.random.default_rng(seqs + window)
+    lay = ko.Layout(heads, kv_heads, 64, 16, window)
+    rows = rng.integers(1, 27, seqs)
+    lens = rows + rng.integers(0, 900, seqs)
+    rows[seqs // 2], lens[seqs // 2], lens[0], lens[-1] = 26, longest, 2500, 27
+    plan = TreePlan(lay, list(rows), list(lens), rng)
+    check_tree(lay, plan, plan.filled_cache(rng), dtype, rng)
+    if seqs == 6:
+        plan = TreePlan(lay, [26] * seqs, [700] * seqs, rng, width=300)
+        check_tree(lay, plan, plan.filled_cache(rng), dtype, rng)
+
+
 def test_tree_attention_hides_pages_that_are_not_there():
     rng = np.random.default_rng(23)
     lay = ko.Layout(4, 2, 128, 16)
