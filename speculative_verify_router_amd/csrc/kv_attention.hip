@@ -127,6 +127,14 @@ int64_t attn_seen_tiles(const moe_kv_desc* d, const moe_kv_batch* b) {
   return seen / kAttnTile + 2;
 }
 
+// Workgroups of a CU, and a head's row tiles or parts that run at once.
+int attn_resident(const moe_kv_desc* d, int row_tiles, int32_t dtype, int waves) {
+  return attn_waves(d->head_dim, row_tiles, attn_terms(dtype)) * kAttnWaves / waves;
+}
+int attn_slots(const moe_kv_desc* d, int row_tiles, int32_t dtype, int waves) {
+  return 256 * attn_resident(d, row_tiles, dtype, waves) / d->n_kv_heads;
+}
+
 // Splits of one tree's row tiles, which see the same tokens, so that parts are
 // alike, and what they cost, in tiles: those of a part, and what it costs to
 // begin and to join.  Row tiles of a head and a split are one group, groups go
@@ -134,14 +142,25 @@ int64_t attn_seen_tiles(const moe_kv_desc* d, const moe_kv_batch* b) {
 // for takes a second round, whose row tiles no longer read the same tokens at the
 // same time: 24 rows over 40000 tokens, 4 heads, eight waves 101 us with four
 // splits, 146 with five to ten.
+//   More parts than run at once fill the rounds of row tiles of which few fit: 65
+// rows of 64 heads on 4 over 60000 tokens, bf16, D = 192 (33 row tiles, room for
+// 128) 319 us with ten, 478 with two.  They have twelve steps a wave at least (65
+// rows of 128 heads on 8, fp16, 65 row tiles and room for 64: over 2000 tokens 54
+// us, 60 in thirds; over 3500 82, 77 in halves), and are up to three times what
+// runs at once (with four times, in thirds, 327 us over 20000 tokens instead of 343;
+// uncut 419).  Row tiles that pass what runs at once by more than a quarter fill
+// about half of a round, which takes half the time: not cut (96 of those rows over
+// 3500 tokens 84 us, 90 in halves).
 struct TreeSplits {
   int splits;
   int64_t cost;
 };
-TreeSplits tree_splits(int64_t row_tiles, int heads, int resident, int64_t tiles, int min_tiles, int64_t most_parts) {
+TreeSplits tree_splits(int64_t row_tiles, int heads, int resident, int64_t tiles, int min_tiles, int64_t at_once,
+                       int64_t most_parts, int step) {
   const int64_t group = row_tiles < 64 ? row_tiles : 64, room = 256 / 8 * resident;  // workgroups of an XCD at once
   TreeSplits best{1, 0};
   for (int s = 1; s <= kMaxSplits && (s - 1) * min_tiles < tiles && row_tiles * s <= most_parts; ++s) {
+    if (s > 1 && row_tiles * s > at_once && (tiles < (int64_t)12 * step * s || 4 * row_tiles > 5 * at_once)) break;
     const int64_t groups = (row_tiles * s + group - 1) / group * heads;
     const int64_t rounds = ((groups + 7) / 8 * group + room - 1) / room;
     int64_t cost = (tiles + s - 1) / s;
@@ -164,16 +183,13 @@ bool attn_split(AttnPlan& p, const moe_kv_desc* d, const moe_kv_batch* b, int32_
   // 777 tokens 11.2 us, 12.4 with one, 13.6 with three; fp32, a window of 512
   // 18.8 and 23.6).
   if (tree && p.row_tiles == 1) p.min_tiles *= 2;
-  // Work of a head that runs at once.
-  const int resident = attn_waves(d->head_dim, p.row_tiles, attn_terms(dtype)) * kAttnWaves / p.waves;
-  const int slots = 256 * resident / d->n_kv_heads;
+  const int resident = attn_resident(d, p.row_tiles, dtype, p.waves), slots = attn_slots(d, p.row_tiles, dtype, p.waves);
   // Every row tile has one part that is half full on the average.  Where two of
   // each are more than run at once, even sequences are not cut: 97 of 2000
   // tokens 35 us (46 in halves), and longer ones into parts of the mean.
   int64_t share = slots - all / 2;
   if (2 * all > slots && share > all) share = all;
   p.share = (int)(share > slots / 2 ? share : slots / 2);
-  if (tree && b->n_seqs == 1) p.share = slots;  // parts alike (61 rows over 60000 tokens 256 us, 275 without)
   // Trees have work for longer parts than single rows do, and more of them on the
   // average than run at once: parts of the mean however many row tiles there are
   // (up to twice what runs at once, by the workspace), eight steps a wave at
@@ -187,8 +203,9 @@ bool attn_split(AttnPlan& p, const moe_kv_desc* d, const moe_kv_batch* b, int32_
   p.share = p.share > 0 ? p.share : 1;
   const int64_t tiles = attn_seen_tiles(d, b), most = (tiles + p.min_tiles - 1) / p.min_tiles;
   if (tree && b->n_seqs == 1) {
-    const TreeSplits t = tree_splits(all, d->n_kv_heads, resident, tiles, p.min_tiles, 4 * (int64_t)slots);
+    const TreeSplits t = tree_splits(all, d->n_kv_heads, resident, tiles, p.min_tiles, slots, 3 * (int64_t)slots, p.waves);
     p.splits = t.splits;
+    p.share = (int)(all * t.splits);  // the kernel's parts are these, and alike (61 rows over 60000 tokens 256 us, 275 if not)
     p.cost = t.cost;
   } else if (b->n_seqs == 1) {
     const int64_t s = 2 * all > slots ? 1 : slots / all;
@@ -254,10 +271,10 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype, b
 }
 
 // What the plan of any batch of up to these sizes needs.  Row tiles times
-// splits are at most what runs at once for one sequence, four times that for one
-// tree, 4 1/4 for several (at most a quarter of it row tiles, each with a part
-// too many); where the last workgroup joins, twice p.share, which is at most what
-// runs at once, of trees twice that.
+// splits are at most what runs at once for one sequence, three times that for one
+// tree, 4 1/4 for several sequences (at most a quarter of it row tiles, each with a
+// part too many); where the last workgroup joins, twice p.share, which is at most
+// what runs at once, of trees twice that.
 size_t attn_most_bytes(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   if (b->n_seqs == 0 || b->n_tokens == 0 || b->max_rows == 0) return 0;
   if (attn_seen_tiles(d, b) <= kAttnWaves) return 0;  // never cut
@@ -265,8 +282,8 @@ size_t attn_most_bytes(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtyp
                        (d->n_heads / d->n_kv_heads);
   size_t most = 0;
   for (int rt = 1; rt <= attn_row_tiles(rows, d->head_dim, dtype); ++rt) {
-    const int slots = 256 * attn_waves(d->head_dim, rt, attn_terms(dtype)) / d->n_kv_heads;
-    const int parts = slots < 1 ? 2 : 4 * slots + slots / 4;
+    const int slots = attn_slots(d, rt, dtype, kAttnWaves);
+    const int64_t parts = b->n_seqs == 1 ? 3 * (int64_t)slots : slots < 1 ? 2 : 4 * slots + slots / 4;
     const size_t n = (size_t)parts * d->n_kv_heads * 16 * rt;
     const size_t bytes = kAttnCounters * sizeof(unsigned) + ((n * d->head_dim * 4 + 255) & ~(size_t)255) + n * 8;
     most = bytes > most ? bytes : most;
