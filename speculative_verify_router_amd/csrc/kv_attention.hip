@@ -155,6 +155,9 @@ struct TreeSplits {
   int splits;
   int64_t cost;
 };
+// The most parts of one tree, in what runs at once: row tiles of which eight or
+// more fit waste little of it, and need the workspace that they need without masks.
+int64_t tree_rounds(int64_t row_tiles, int64_t at_once) { return 8 * row_tiles < at_once ? 1 : 3; }
 TreeSplits tree_splits(int64_t row_tiles, int heads, int resident, int64_t tiles, int min_tiles, int64_t at_once,
                        int64_t most_parts, int step) {
   const int64_t group = row_tiles < 64 ? row_tiles : 64, room = 256 / 8 * resident;  // workgroups of an XCD at once
@@ -203,7 +206,8 @@ bool attn_split(AttnPlan& p, const moe_kv_desc* d, const moe_kv_batch* b, int32_
   p.share = p.share > 0 ? p.share : 1;
   const int64_t tiles = attn_seen_tiles(d, b), most = (tiles + p.min_tiles - 1) / p.min_tiles;
   if (tree && b->n_seqs == 1) {
-    const TreeSplits t = tree_splits(all, d->n_kv_heads, resident, tiles, p.min_tiles, slots, 3 * (int64_t)slots, p.waves);
+    const int64_t rounds = tree_rounds(all, attn_slots(d, p.row_tiles, dtype, kAttnWaves));
+    const TreeSplits t = tree_splits(all, d->n_kv_heads, resident, tiles, p.min_tiles, slots, slots * rounds, p.waves);
     p.splits = t.splits;
     p.share = (int)(all * t.splits);  // the kernel's parts are these, and alike (61 rows over 60000 tokens 256 us, 275 if not)
     p.cost = t.cost;
@@ -272,9 +276,9 @@ AttnPlan attn_plan(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype, b
 
 // What the plan of any batch of up to these sizes needs.  Row tiles times
 // splits are at most what runs at once for one sequence, three times that for one
-// tree, 4 1/4 for several sequences (at most a quarter of it row tiles, each with a
-// part too many); where the last workgroup joins, twice p.share, which is at most
-// what runs at once, of trees twice that.
+// tree of more than a few row tiles, 4 1/4 for several sequences (at most a quarter
+// of it row tiles, each with a part too many); where the last workgroup joins, twice
+// p.share, which is at most what runs at once, of trees twice that.
 size_t attn_most_bytes(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype) {
   if (b->n_seqs == 0 || b->n_tokens == 0 || b->max_rows == 0) return 0;
   if (attn_seen_tiles(d, b) <= kAttnWaves) return 0;  // never cut
@@ -283,7 +287,9 @@ size_t attn_most_bytes(const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtyp
   size_t most = 0;
   for (int rt = 1; rt <= attn_row_tiles(rows, d->head_dim, dtype); ++rt) {
     const int slots = attn_slots(d, rt, dtype, kAttnWaves);
-    const int64_t parts = b->n_seqs == 1 ? 3 * (int64_t)slots : slots < 1 ? 2 : 4 * slots + slots / 4;
+    const int64_t parts = b->n_seqs == 1 ? slots * tree_rounds((rows + 16 * rt - 1) / (16 * rt), slots)
+                          : slots < 1    ? 2
+                                         : 4 * slots + slots / 4;
     const size_t n = (size_t)parts * d->n_kv_heads * 16 * rt;
     const size_t bytes = kAttnCounters * sizeof(unsigned) + ((n * d->head_dim * 4 + 255) & ~(size_t)255) + n * 8;
     most = bytes > most ? bytes : most;

@@ -399,3 +399,19 @@ def test_random_trees_are_trees():
         assert max([p.count(i) for i in range(rows)]) <= kids
     off, par = forest([3, 0, 5], 2, rng)
     assert off.tolist() == [0, 3, 3, 8] and len(par) == 8
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,rows", [(64, 4, 192, 4), (64, 4, 192, 15), (16, 2, 128, 61), (32, 8, 64, 4)])
+def test_few_rows_need_the_workspace_of_what_runs_at_once(heads, kv_heads, dim, rows):
+    """Row tiles of which eight or more run at once are cut into what does, with masks or without: 256
+    compute units of two to four workgroups, whose rows are 16 or 32, D sums of 32 bits and two more."""
+    off, table = torch.zeros(2, dtype=torch.int32), torch.zeros((1, 1000), dtype=torch.int32)
+    n = svr.moe_kv_attention_workspace_bytes(svr.KvDesc(heads, kv_heads, dim, 64), svr.KvBatch(off, off[:1], table, rows), rows)
+    most = 0
+    for wide in (16, 32):
+        for terms in (1, 2, 3):
+            regs = wide // 16 * (dim // 8 * terms + dim // 4)  # of queries and sums
+            groups = 4 if regs <= 48 else 3 if regs <= 72 else 2 if regs <= 160 else 1
+            if wide == 16 or (rows * heads // kv_heads > 16 and groups >= 2):
+                most = max(most, 256 * groups // kv_heads * kv_heads * wide)
+    assert n <= most * (4 * dim + 8) + B.KV_COUNTER_BYTES + 255
