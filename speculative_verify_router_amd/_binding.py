@@ -701,12 +701,14 @@ TREE_MAX_CACHES = 256
 class DraftTree:
     """Trees of drafts of a batch of sequences (moe_tree): int32 device tensors
     q_offsets [B+1] and parents [T] (None: chains, parents i - 1); max_rows: no
-    sequence has more rows; max_children: no row has more children.  The tensors
-    are captured by reference, as those of KvBatch."""
+    sequence has more rows; max_children: no row has more children, or those behind
+    are never accepted (None: as many as a row can have, one in chains; drawn drafts
+    take a launch for each, so say it for those).  The tensors are captured by
+    reference, as those of KvBatch."""
     q_offsets: torch.Tensor
     parents: Optional[torch.Tensor]
     max_rows: int
-    max_children: int = 1
+    max_children: Optional[int] = None
 
     def __post_init__(self):
         i32, dev = torch.int32, self.q_offsets.device
@@ -716,6 +718,8 @@ class DraftTree:
             raise ValueError("parents: expected [rows]")
         args = (_on(dev, self.q_offsets, i32, None, "q_offsets"),
                 _on(dev, self.parents, i32, None, "parents"))
+        if self.max_children is None:
+            object.__setattr__(self, "max_children", 1 if self.parents is None else max(1, self.max_rows - 1))
         _check_int32(self, "max_rows", "max_children")
         object.__setattr__(self, "_args", args)
         object.__setattr__(self, "_device", dev)

@@ -415,3 +415,13 @@ def test_few_rows_need_the_workspace_of_what_runs_at_once(heads, kv_heads, dim, 
             if wide == 16 or (rows * heads // kv_heads > 16 and groups >= 2):
                 most = max(most, 256 * groups // kv_heads * kv_heads * wide)
     assert n <= most * (4 * dim + 8) + B.KV_COUNTER_BYTES + 255
+
+
+def test_a_tree_without_a_number_of_children_leaves_none_out():
+    i32 = dict(dtype=torch.int32)
+    off, parents = torch.tensor([0, 9], **i32), torch.tensor([-1] + [0] * 8, **i32)
+    for tree, kids in ((svr.DraftTree(off, parents, 9), 8), (svr.DraftTree(off, None, 9), 1),
+                       (svr.DraftTree(off, parents, 1), 1), (svr.DraftTree(off, parents, 9, 2), 2),
+                       (svr.DraftTree(off, parents, svr.TREE_MAX_ROWS), svr.TREE_MAX_ROWS - 1)):
+        assert tree.max_children == tree.c(9).max_children == kids
+        assert svr.moe_sample_workspace_bytes(tree, 9, 1000) > 0
