@@ -41,8 +41,10 @@
 // every further one of a wave, and 2.9 where parts are joined: 9.5 over 777
 // tokens, 20.8 over 60000 (the second kernel, and a third of the rate of the
 // cache's bytes).  29 sequences of up to 5000 tokens, fp16, 32 on 8 heads of 128:
-// 24 us (82 MB, 3.4 TB/s); with trees of up to 26 rows 71 (280 TFLOP/s, four
-// products for one that counts).
+// 24 us (82 MB, 3.4 TB/s); with trees of up to 26 rows 71 (280 TFLOP/s; two products
+// for one that counts, and row and token tiles that are not full make them 2.5,
+// so 710 are issued where 61 rows over 60000 tokens issue 1070: 94 tiles for each
+// workgroup that runs at once would be even, and the parts end at 124).
 // Addresses by vector arithmetic in every tile instead of once: 892 and 1056 us
 // in fp16 and fp32, 1 us for 4 rows.
 // Others that were measured, for the first bf16 call, the verify batch and the

@@ -21,13 +21,18 @@
 // Bound, large: a column takes about 22 instructions of 64 bits, 4.6 clocks each
 // for a wave (every kind, conversions and roundings too), so 48 sequences of three
 // rows in bf16 take 12 us of arithmetic beside 7.5 of bytes; 26 us a call (without
-// the weights 18), and 41 with drawn drafts.  A table of 32 or 128 powers takes as
-// many instructions with its look-ups; weights of 32 bits for the rows and of 64
-// for the last ones only, two launches, would save a tenth.  Small: latency, 10.4
-// us for 4 rows of float: the row's place 0.9 us, its children 0.3, logits and
-// weights 1.4, arrival of the row 1.2, its sum and children 1.4, arrival of the
-// sequence 1.0, the path 1.2, its tile 0.9, the column 1.8.  16.6 us with drawn
-// drafts.  61 rows of float (32 MB, of which a path needs 5) 17 us.  A last
+// the weights 18), and 41 with drawn drafts, whose round takes 18 to 20 us though it
+// sums 16 to 27 of 141 rows (3 us of bytes, 2 of arithmetic): a row is cut by how
+// many rows there are, not by how many are open, so some 240 workgroups have work,
+// each wave three tiles one after another with none asked for ahead.  A table of 32
+// or 128 powers takes as many instructions with its look-ups; weights of 32 bits for
+// the rows and of 64 for the last ones only, two launches, would save a tenth.
+//   Small: latency, 10.6 us for 4 rows of float (with a hidden state of 4096 numbers
+// 12.4, of 7168 14.0: it is copied before the path's tile is looked for): the row's
+// place 0.9 us, its children 0.3, logits and weights 1.4, arrival of the row 1.2,
+// its sum and children 1.4, arrival of the sequence 1.0, the path 1.2, its tile 0.9,
+// the column 1.8.  16.6 us with drawn drafts.  61 rows of float (32 MB, of which a
+// path needs 5) 17 us.  A last
 // workgroup meets its code for the first time, so what is not a loop over columns
 // is kept short: with everything inlined, and four tiles a lane in a row's sum, a
 // round of drawn drafts took 18 us instead of 9.  For trees of up to four rows,
@@ -46,7 +51,8 @@ namespace {
 constexpr size_t kSampleCounterBytes = 2 * MOE_SAMPLE_MAX_ROWS * sizeof(unsigned);
 // Workgroups of a call that are wanted, for all rows and for the rounds of drawn
 // drafts, most of whose rows are done (48 chains and 9 trees of drawn drafts:
-// 41.4 and 54.7 us; with 1024 44.1 and 59.7, with 8192 42.1 and 56.4).
+// 41.4 and 54.7 us; with 1024 44.1 and 59.7, with 8192 42.1 and 56.4: more for the
+// open rows are also more that start only to leave).
 constexpr int kSampleSpread = 2048, kRoundSpread = 2048;
 
 struct SampleArgs {
