@@ -95,6 +95,7 @@ struct AttnArgs {
   unsigned* ctr;  // [row tile that is cut][key/value head] parts made, or NULL: a second kernel joins
   float c;         // scale * log2(e)
   int row_tiles, min_tiles, by_seq, search;
+  int even_tiles;  // all splits are used where they have so many tiles, whatever runs at once
   int reach;  // tokens that a window's row tile lies over at most, with its first and last tile's
   // Rows of a tree (moe_tree.h): the new rows that each row sees, in 32-bit words; NULL: those before it.
   const uint32_t* mask;
@@ -246,7 +247,8 @@ __device__ __forceinline__ KvPer kv_per_most(const AttnArgs& a, const KvRows& s)
   // Rounded up, by the bits that the divider takes.
   const int shift = max(0, 34 - (int)__builtin_clzll(all | 1));
   const int64_t fair = (int64_t)(a.share.of((int)(all >> shift) + a.share.d - 1) + (shift ? 1 : 0)) << shift;
-  const int per = max(a.min_tiles, max((int)min(fair, (int64_t)kWholeRange), a.splits.of(most + a.splits.d - 1)));
+  const int even = a.splits.of(most + a.splits.d - 1);  // of the longest sequence, in all splits
+  const int per = even >= a.even_tiles ? even : max(a.min_tiles, max((int)min(fair, (int64_t)kWholeRange), even));
   return KvPer{most <= 3 * a.min_tiles ? max(per, most) : per, most};  // four rounds of the waves take as long as joining
 }
 __device__ __forceinline__ int kv_per(const AttnArgs& a, const KvRows& s) { return kv_per_most(a, s).per; }

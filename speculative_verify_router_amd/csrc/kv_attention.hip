@@ -112,7 +112,7 @@ void launch_kv_join(const AttnArgs& a, int32_t dtype, unsigned n, hipStream_t st
 
 // How a batch is cut, as far as its sizes say (the lengths are on the device).
 struct AttnPlan {
-  int row_tiles, tiles, waves, splits, min_tiles, share, group, by_seq, search, first, extra;
+  int row_tiles, tiles, waves, splits, min_tiles, even_tiles, share, group, by_seq, search, first, extra;
   bool join_here;
   int64_t part_rows;
   int64_t cost;  // of one tree's parts
@@ -151,6 +151,7 @@ int attn_slots(const moe_kv_desc* d, int row_tiles, int32_t dtype, int waves) {
 // uncut 419).  Row tiles that pass what runs at once by more than a quarter fill
 // about half of a round, which takes half the time: not cut (96 of those rows over
 // 3500 tokens 84 us, 90 in halves).
+constexpr int kTreeSteps = 12;
 struct TreeSplits {
   int splits;
   int64_t cost;
@@ -163,7 +164,7 @@ TreeSplits tree_splits(int64_t row_tiles, int heads, int resident, int64_t tiles
   const int64_t group = row_tiles < 64 ? row_tiles : 64, room = 256 / 8 * resident;  // workgroups of an XCD at once
   TreeSplits best{1, 0};
   for (int s = 1; s <= kMaxSplits && (s - 1) * min_tiles < tiles && row_tiles * s <= most_parts; ++s) {
-    if (s > 1 && row_tiles * s > at_once && (tiles < (int64_t)12 * step * s || 4 * row_tiles > 5 * at_once)) break;
+    if (s > 1 && row_tiles * s > at_once && (tiles < (int64_t)kTreeSteps * step * s || 4 * row_tiles > 5 * at_once)) break;
     const int64_t groups = (row_tiles * s + group - 1) / group * heads;
     const int64_t rounds = ((groups + 7) / 8 * group + room - 1) / room;
     int64_t cost = (tiles + s - 1) / s;
@@ -179,6 +180,7 @@ TreeSplits tree_splits(int64_t row_tiles, int heads, int resident, int64_t tiles
 // Returns whether row tiles are few, and tables long, enough for four splits
 // or more and as many as there is room for.
 bool attn_split(AttnPlan& p, const moe_kv_desc* d, const moe_kv_batch* b, int32_t dtype, int64_t all, bool tree) {
+  p.even_tiles = kWholeRange;
   // A part is a tile a wave at least, and as many more for every 64 sequences
   // behind the first, which a workgroup passes over to find it.
   p.min_tiles = p.waves * (1 + (b->n_seqs - 1) / kWave);
@@ -199,6 +201,7 @@ bool attn_split(AttnPlan& p, const moe_kv_desc* d, const moe_kv_batch* b, int32_
   // least (29 trees of up to 26 rows over 5000 tokens, fp16, 75 us, 82 without; 40
   // of up to 7 over 20000 198 and 241; with one step at least 60 of up to 10 over
   // 3000 54 us, 48 with eight).  Even trees are not cut, as before.
+  if (tree && b->n_seqs == 1) p.share = slots;  // as even (61 rows over 60000 tokens 256 us, 275 without)
   if (tree && b->n_seqs > 1 && 2 * all > slots) {
     p.share = (int)(all < 2 * slots ? all : 2 * slots);
     p.min_tiles = p.min_tiles > 8 * p.waves ? p.min_tiles : 8 * p.waves;
@@ -209,7 +212,10 @@ bool attn_split(AttnPlan& p, const moe_kv_desc* d, const moe_kv_batch* b, int32_
     const int64_t rounds = tree_rounds(all, attn_slots(d, p.row_tiles, dtype, kAttnWaves));
     const TreeSplits t = tree_splits(all, d->n_kv_heads, resident, tiles, p.min_tiles, slots, slots * rounds, p.waves);
     p.splits = t.splits;
-    p.share = (int)(all * t.splits);  // the kernel's parts are these, and alike (61 rows over 60000 tokens 256 us, 275 if not)
+    // By the length, which the table may pass by far: parts of fewer steps are as many
+    // as run at once, by share (65 rows of 64 heads on 4 over 2000 tokens in a table
+    // of 60000 36 us, 46 in all splits; over 20000 127, 153 by share).
+    p.even_tiles = kTreeSteps * p.waves;
     p.cost = t.cost;
   } else if (b->n_seqs == 1) {
     const int64_t s = 2 * all > slots ? 1 : slots / all;
@@ -335,6 +341,7 @@ int32_t attention(const moe_kv_desc* desc, const moe_kv_batch* batch, int32_t dt
   a.share = make_divider(p.share);
   a.group = make_divider(p.group);
   a.min_tiles = p.min_tiles;
+  a.even_tiles = p.even_tiles;
   a.row_tiles = p.row_tiles;
   // Rows of a tile: whole tokens, and one cut at either end; those of a tree: all of them.
   a.reach = a.kv.window + (mask ? batch->max_rows : 16 * p.row_tiles / a.G.d) + 2 + kAttnTile;

@@ -45,8 +45,8 @@ def reference(lay, plan, cache, q64):
     return [x.cpu().numpy() for x in (out, lse, size, reach)] + [seen.sum(1)]
 
 
-def check_one(lay, rows, length, dtype, rng, kids=4, ref=reference):
-    plan = TreePlan(lay, [rows], [length], rng, kids=kids)
+def check_one(lay, rows, length, dtype, rng, kids=4, width=None):
+    plan = TreePlan(lay, [rows], [length], rng, kids=kids, width=width)
     cache = plan.filled_cache(rng)
     q, q64 = rounded(rng.standard_normal((rows, lay.heads, lay.dim)), dtype)
     desc, batch, mask, c = desc_of(lay), plan.batch(), as_words(plan.mask), dev(cache)
@@ -57,7 +57,7 @@ def check_one(lay, rows, length, dtype, rng, kids=4, ref=reference):
     svr.moe_kv_tree_attention(desc, batch, mask, q, c, again, ws=ws)
     torch.cuda.synchronize()
     assert torch.equal(out, again)
-    want, rl, size, reach, seen = ref(lay, plan, cache, q64)
+    want, rl, size, reach, seen = reference(lay, plan, cache, q64)
     tol = attention_tolerance(dtype, want, size, reach, seen, lay.dim)
     err = np.abs(out.double().cpu().numpy() - want)
     assert np.all(err <= tol), (np.nanmax(err - tol), np.nanmax(err))
@@ -135,3 +135,32 @@ def test_the_largest_tree(dtype, window, kids):
     """1024 rows, masks of sixteen words; a chain, whose windows lie among the rows alone, and a tree."""
     log(f"1024 rows {dtype} W={window} kids={kids}")
     check_one(ko.Layout(4, 2, 64, 32, window), 1024, 1500, dtype, np.random.default_rng(82 + window), kids=kids)
+
+
+# A table of 60000 tokens for fewer; row tiles of a head that run at once.
+WIDE = [(64, 4, 192, "bf16", 65, 700, 128), (64, 4, 192, "bf16", 65, 2000, 128), (64, 4, 192, "bf16", 65, 20000, 128),
+        (32, 8, 128, "bf16", 300, 700, 64), (128, 8, 192, "f16", 65, 2000, 64)]
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,dtype,rows,length,at_once", WIDE)
+def test_one_tree_that_is_short_for_its_table(heads, kv_heads, dim, dtype, rows, length, at_once):
+    """Parts of twelve steps of four waves at least, or about as many as run at once (the last one of each row
+    tile may be a short one more); what is written to the workspace says how many there are."""
+    log(f"short {heads}/{kv_heads} D={dim} {dtype} {rows} rows, {length} tokens")
+    lay = ko.Layout(heads, kv_heads, dim, 64)
+    rng = np.random.default_rng(85 + length)
+    check_one(lay, rows, length, dtype, rng, width=938)
+    plan = TreePlan(lay, [rows], [length], rng, width=938)
+    desc, batch = desc_of(lay), plan.batch()
+    ws = svr.kv_workspace(desc, batch, rows)
+    ws[svr._binding.KV_COUNTER_BYTES:] = 0xA5
+    q = torch.ones((rows, heads, dim), dtype=TYPES[dtype], device="cuda")
+    cache = torch.zeros((plan.n_pages, kv_heads, lay.page_bytes), dtype=torch.uint8, device="cuda")
+    svr.moe_kv_tree_attention(desc, batch, as_words(plan.mask), q, cache, torch.empty_like(q), ws=ws)
+    written = int((ws[svr._binding.KV_COUNTER_BYTES:].view(torch.int32) == 0).sum())  # sums of zeros
+    n = row_tiles(heads, kv_heads, dim, dtype, rows)
+    parts = written / (rows * heads * dim) * n  # of a head
+    if length <= 2000:
+        assert parts <= at_once + n
+    else:
+        assert parts > 2 * at_once
